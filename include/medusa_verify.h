@@ -293,7 +293,7 @@ typedef struct mv_model mv_model;
 typedef struct mv_session mv_session;
 
 /* Storage and arithmetic type of a model: its weights, activations and KV cache. */
-typedef enum { MV_DTYPE_BF16 = 0, MV_DTYPE_F32 = 1 } mv_dtype;
+typedef enum { MV_DTYPE_BF16 = 0, MV_DTYPE_F32 = 1, MV_DTYPE_E4M3 = 2 /* paged caches only */ } mv_dtype;
 
 /* Limits: d % 8 == 0, d <= 8192, head_dim in {16, 32, 64, 128}, ffn % 8 == 0, 1 <= n_medusa <= 8; every
  * pointer 16-byte aligned. MV_ERR_SHAPE otherwise. Builds the weights' TMA descriptors (host only). */
@@ -434,6 +434,104 @@ enum {
 };
 mv_status mv_session_profile(mv_session* session, int32_t enable);
 mv_status mv_session_profile_read(mv_session* session, float* ms_by_kind, int32_t* launches_by_kind);
+
+/* ============================================================================================
+ * Attention over whole prompts, several packed in one call
+ * ============================================================================================
+ * The serving form of the prompt pass: `n_seq` prompts of any lengths lie one after the other in q, k and v. For
+ * token i of a prompt (counted from its first), query head h and kv head c = h / (n_heads / n_kv_heads):
+ *   out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h] . k[j][c]) v[j][c],   j a token of the same prompt.
+ * Scores, softmax statistics and output sums in fp32; the weights are rounded to bf16 for the product with v.
+ * Nothing at a masked place reaches a row: a NaN or infinity in token j's k or v changes only rows i >= j of its
+ * own prompt.
+ *
+ * A plan holds what depends on the lengths alone: the prompts' places and the work items, longest first. It is
+ * made once for a batch of prompts and serves every layer. lens: host [n_seq], each >= 0; group = n_heads /
+ * n_kv_heads of the calls it will serve. The work items are copied to the current device (without a CUDA device
+ * the handle keeps the host copy only). Creating and destroying a plan may synchronise the device: not during
+ * stream capture, and destroy it only when no captured graph will be replayed that uses it.
+ * Errors: MV_ERR_INVALID_ARG (null, n_seq < 0, a negative length, group < 1), MV_ERR_SHAPE (group > 256, more than
+ * 2^31 - 1 tokens or 2^22 work items), MV_ERR_CAPACITY (out of device memory), MV_ERR_CUDA.
+ */
+typedef struct mv_prompt_plan mv_prompt_plan;
+typedef struct mv_prompt_plan_desc {
+  int32_t n_seq, group, n_tokens, n_items;
+  const int32_t* items; /* host [n_items][4]: first token of the prompt, its length, first sub-tile, key tiles. A
+                           prompt's queries fall into sub-tiles of 128 tokens of one head, sub-tile t = head t % group
+                           of a kv head and tokens 128 (t / group) ..; an item is two consecutive sub-tiles */
+} mv_prompt_plan_desc;
+mv_status mv_prompt_plan_create(const int32_t* lens, int32_t n_seq, int32_t group, mv_prompt_plan** out);
+mv_status mv_prompt_plan_describe(const mv_prompt_plan* plan, mv_prompt_plan_desc* out);
+void mv_prompt_plan_destroy(mv_prompt_plan* plan);
+
+/* Where rows of [n_tokens][heads][head_dim] bf16 lie: element d of token t and head h at
+ * ptr[t * token_stride + h * head_stride + d] (strides in elements). So packed rows, a slice of a fused QKV output and
+ * a [H][S][D] cache plane are all such rows. ptr 16-byte aligned, strides >= 0 and multiples of 8. */
+typedef struct mv_rows {
+  void* ptr;
+  int64_t token_stride, head_stride;
+} mv_rows;
+
+/* q, out: n_heads heads, k, v: n_kv_heads, all plan->n_tokens tokens. Rows of out outside the plan are not touched.
+ * out must not overlap q, k or v. Limits: head_dim % 8 == 0, 8 <= head_dim <= 128; n_heads = group * n_kv_heads <=
+ * 256; token_stride >= head_dim or one token, head_stride >= head_dim or one head; scale finite.
+ * Errors: MV_ERR_INVALID_ARG (null, unaligned, a plan of another device), MV_ERR_SHAPE, MV_ERR_CUDA (also a plan
+ * made without a device). */
+mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                           const mv_prompt_plan* plan, float scale, mv_rows out, mv_stream stream);
+
+/* ============================================================================================
+ * Paged key/value cache of one layer: written, read back, and attended to by one new token per sequence
+ * ============================================================================================
+ * The pool: k, v device [n_pages][n_kv_heads][page_size][head_dim], bf16 or e4m3 (MV_DTYPE_E4M3: one sign, four
+ * exponent, three fraction bits, no infinities). An e4m3 pool has an exponent byte for every row, k_exp, v_exp device
+ * [n_pages][n_kv_heads][page_size]: the row stands for x8 * 2^(byte - 127). Writing a row x takes the smallest e in
+ * [-100, 120] with max|x| <= 448 * 2^e (NaNs apart; a row of zeros: -100) and rounds x * 2^-e to the nearest e4m3, ties
+ * to even. The scale is a power of two, so what a row stands for is exact in bf16 (where its exponent reaches). A NaN
+ * stays a NaN, an infinity becomes 448 * 2^120, which reads back as an infinity.
+ * The sequences: block_table device int32 [n_seq][ld_table], the first max_pages entries of a row used: position p
+ * of sequence b lies in page block_table[b][p / page_size] at slot p % page_size; seq_lens device int32 [n_seq]: each
+ * sequence's length, the rows of this call included. Entries past a sequence's last page are not read.
+ * Every call reads the table and the lengths on the device, so it can be captured and replayed as they change. Found
+ * there out of range (a page outside the pool, a length that is negative or over max_pages * page_size), they set the
+ * device error word, and what belongs to them is neither read nor written.
+ * Limits: page_size % 16 == 0, 16 <= page_size <= 1024; head_dim % 16 == 0, 16 <= head_dim <= 128; 1 <= n_kv_heads <=
+ * 256; 0 <= n_seq <= 4096; pools 16-byte aligned.
+ */
+typedef struct mv_paged_kv {
+  void *k, *v;
+  uint8_t *k_exp, *v_exp; /* e4m3 pools; NULL for bf16 */
+  int32_t dtype;          /* MV_DTYPE_BF16 or MV_DTYPE_E4M3 */
+  int32_t n_pages, page_size, n_kv_heads, head_dim;
+} mv_paged_kv;
+
+/* Writes / reads the last rows of every sequence. cu_rows device int32 [n_seq + 1] from 0, not decreasing: rows
+ * cu_rows[b] .. cu_rows[b + 1] - 1 of k and v are sequence b's last ones, the last at position seq_lens[b] - 1. The
+ * rows have n_rows tokens; those behind cu_rows[n_seq] are padding, neither written from nor written to. A position of
+ * a page that two sequences share must not be written by both in one call (either row may stay, or a mix).
+ * paged_kv_read turns rows back into bf16: a parked sequence into packed rows, or into a session's [H][S][D] planes.
+ * cu_rows out of order or past n_rows, or a sequence with more rows than seq_lens[b], set the device error word.
+ * Errors: MV_ERR_INVALID_ARG (null, unaligned, bad strides or dtype), MV_ERR_SHAPE (see the limits), MV_ERR_CUDA. */
+mv_status paged_kv_append(mv_rows k, mv_rows v, int32_t n_rows, const int32_t* cu_rows, const mv_paged_kv* cache,
+                          const int32_t* block_table, int32_t ld_table, int32_t max_pages, const int32_t* seq_lens,
+                          int32_t n_seq, mv_stream stream);
+mv_status paged_kv_read(const mv_paged_kv* cache, const int32_t* block_table, int32_t ld_table, int32_t max_pages,
+                        const int32_t* seq_lens, int32_t n_seq, const int32_t* cu_rows, int32_t n_rows, mv_rows k,
+                        mv_rows v, mv_stream stream);
+
+/* One new token per sequence: for sequence b, query head h and kv head c = h / (n_heads / n_kv_heads),
+ *   out[b][h] = sum_{j < seq_lens[b]} softmax_j(scale * q[b][h] . k_j[c]) v_j[c],   zeros when seq_lens[b] = 0.
+ * The token's own row is in the cache already (paged_kv_append first). What pages hold behind a sequence's length does
+ * not matter, NaN included. q, out device bf16 rows, token b = sequence b. Scores, softmax statistics and output
+ * sums in fp32. The result does not depend on the order in which the parts of a split sequence finish.
+ * Limits: n_heads % n_kv_heads == 0, n_heads <= 256. workspace: device memory of paged_attention_workspace() bytes,
+ * 16-byte aligned, zero-filled before its first use (see the conventions above). Errors as above; MV_ERR_CAPACITY: the
+ * workspace is too small. */
+mv_status paged_attention_workspace(int32_t n_seq, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                    size_t* bytes);
+mv_status paged_attention(mv_rows q, int32_t n_heads, const mv_paged_kv* cache, const int32_t* block_table,
+                          int32_t ld_table, int32_t max_pages, const int32_t* seq_lens, int32_t n_seq, float scale,
+                          mv_rows out, void* workspace, size_t ws_bytes, mv_stream stream);
 
 /* ============================================================================================
  * Errors

@@ -19,7 +19,9 @@ __all__ = ["lib", "MVError", "Tree", "AcceptParams", "PosteriorResult", "GREEDY"
            "linear_bf16", "linear_bf16_workspace", "ModelDims",
            "medusa_heads_topk", "medusa_heads_topk_workspace", "build_candidates", "tree_attention",
            "tree_attention_workspace", "evaluate_posterior", "evaluate_posterior_workspace", "kv_compact",
-           "get_error", "fill_normal", "selftest_wait_timeout", "DTYPE_BF16", "DTYPE_F32", "MAX_NODES",
+           "get_error", "fill_normal", "selftest_wait_timeout", "DTYPE_BF16", "DTYPE_F32", "DTYPE_E4M3", "MAX_NODES",
+           "PromptPlan", "prompt_attention", "PagedKV", "paged_kv_append", "paged_kv_read", "paged_attention",
+           "paged_attention_workspace",
            "MAX_DEPTH", "EXPORTED_SYMBOLS"]
 
 MAX_NODES = 256
@@ -27,7 +29,7 @@ NOALLOC_MAX_NODES = 64
 MAX_DEPTH = 8
 MASK_WORDS = 4
 GREEDY, TYPICAL = 0, 1
-DTYPE_BF16, DTYPE_F32 = 0, 1
+DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
 ROOT_ARGMAX, ROOT_TYPICAL, ROOT_NUCLEUS = 0, 1, 2
 
 _lib = None
@@ -73,6 +75,22 @@ class PosteriorResult(ctypes.Structure):
                 ("nodes", ctypes.c_int32 * (MAX_DEPTH + 1)), ("tokens", ctypes.c_int32 * (MAX_DEPTH + 1))]
 
 
+class _Rows(ctypes.Structure):
+    """mv_rows: bf16 rows [tokens][heads][head_dim] by address and strides."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _PromptPlanDesc(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int32), ("group", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+                ("n_items", ctypes.c_int32), ("items", ctypes.POINTER(ctypes.c_int32))]
+
+
+class _PagedKVDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 RESULT_INTS = ctypes.sizeof(PosteriorResult) // 4
 
 _P, _I, _U, _F, _S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_float, ctypes.c_size_t
@@ -114,6 +132,14 @@ _SIGS = {
     "medusa_verify_steps_graph": ([_P, AcceptParams, _I, _P], _I),
     "mv_session_profile": ([_P, _I], _I),
     "mv_session_profile_read": ([_P, _P, _P], _I),
+    "mv_prompt_plan_create": ([_P, _I, _I, ctypes.POINTER(_P)], _I),
+    "mv_prompt_plan_describe": ([_P, ctypes.POINTER(_PromptPlanDesc)], _I),
+    "mv_prompt_plan_destroy": ([_P], None),
+    "prompt_attention": ([_Rows, _Rows, _Rows, _I, _I, _I, _P, _F, _Rows, _P], _I),
+    "paged_kv_append": ([_Rows, _Rows, _I, _P, ctypes.POINTER(_PagedKVDesc), _P, _I, _I, _P, _I, _P], _I),
+    "paged_kv_read": ([ctypes.POINTER(_PagedKVDesc), _P, _I, _I, _P, _I, _P, _I, _Rows, _Rows, _P], _I),
+    "paged_attention_workspace": ([_I, _I, _I, _I, ctypes.POINTER(_S)], _I),
+    "paged_attention": ([_Rows, _I, ctypes.POINTER(_PagedKVDesc), _P, _I, _I, _P, _I, _F, _Rows, _P, _S, _P], _I),
     "mv_get_error": ([ctypes.POINTER(_U)], _I),
     "mv_get_error_detail": ([ctypes.POINTER(_U)], _I),
     "mv_selftest_wait_timeout": ([_U, _P, _P], _I),
@@ -360,6 +386,200 @@ def pack_model_weights(w, drop_source=False):
     out["lm_head"] = pack_weight(w["lm_head"], 128)
     out["packed"] = True
     return out
+
+
+# --------------------------------------------------------------------------------------------- serving operators
+
+def _rows(t, what, heads=None, dim=None, tokens=None):
+    """A bf16 CUDA tensor [tokens, heads, head_dim] as mv_rows; its last dimension must be contiguous."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{what}: a bf16 CUDA tensor [tokens, heads, head_dim] is wanted, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    n, h, d = t.shape
+    if (heads is not None and h != heads) or (dim is not None and d != dim) or (tokens is not None and n != tokens):
+        raise ValueError(f"{what}: [{'tokens' if tokens is None else tokens}, {'heads' if heads is None else heads}, "
+                         f"{'head_dim' if dim is None else dim}] is wanted, got {tuple(t.shape)}")
+    ts, hs, ds = t.stride()
+    if ds != 1 and d != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous, got strides {t.stride()}")
+    return _Rows(t.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0)
+
+
+def _ints(t, what, dim, device):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != dim or t.device != device:
+        raise ValueError(f"{what}: an int32 tensor of {dim} dimension(s) on {device} is wanted, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if t.numel() > 1 and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous, got strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _call_on(device, stream, fn, *args):
+    """fn(*args, stream) with ``device`` current, on ``stream`` or on the device's current stream."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors are on {device}")
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    _check(status, fn.__name__)
+
+
+class PromptPlan:
+    """Where the prompts of a packed batch lie and how prompt_attention goes over them, from their lengths alone (see
+    mv_prompt_plan_create). ``group``: query heads per kv head. Made for the current device, or for ``device``."""
+
+    def __init__(self, lens, group=1, device=None):
+        L = lib()
+        lens = [int(n) for n in lens]
+        if any(not 0 <= n < 2 ** 31 for n in lens):
+            raise ValueError(f"PromptPlan: lengths lie in 0 .. 2^31 - 1, got {lens}")
+        arr = (ctypes.c_int32 * max(1, len(lens)))(*lens)
+        h = ctypes.c_void_p()
+        if device is None:
+            status = L.mv_prompt_plan_create(arr, len(lens), group, ctypes.byref(h))
+        else:
+            import torch
+            with torch.cuda.device(device):
+                status = L.mv_prompt_plan_create(arr, len(lens), group, ctypes.byref(h))
+        _check(status, "mv_prompt_plan_create")
+        self.handle = h
+        d = _PromptPlanDesc()
+        _check(L.mv_prompt_plan_describe(h, ctypes.byref(d)), "mv_prompt_plan_describe")
+        self.lens, self.group, self.n_tokens, self.n_items = lens, d.group, d.n_tokens, d.n_items
+
+    def items(self):
+        """int32 [n_items, 4]: first token of the prompt, its length, first sub-tile, key tiles."""
+        d = _PromptPlanDesc()
+        _check(lib().mv_prompt_plan_describe(self.handle, ctypes.byref(d)), "mv_prompt_plan_describe")
+        if not d.n_items:
+            return np.zeros((0, 4), dtype=np.int32)
+        return np.ctypeslib.as_array(d.items, shape=(d.n_items, 4)).copy()
+
+    def __del__(self):
+        if getattr(self, "handle", None) is not None and _lib is not None:
+            _lib.mv_prompt_plan_destroy(self.handle)
+            self.handle = None
+
+
+def prompt_attention(q, k, v, plan: PromptPlan, scale, out, stream=None):
+    """Causal attention of packed prompts: q, out bf16 [tokens, heads, D]; k, v bf16 [tokens, kv heads, D] (any strides
+    that are multiples of 8, last dimension contiguous); tokens = plan.n_tokens at least, later rows are not touched."""
+    n, d = plan.n_tokens, q.shape[-1]
+    if q.dim() != 3 or k.dim() != 3 or q.shape[0] < n:
+        raise ValueError(f"prompt_attention: q and k are [tokens, heads, head_dim] of {n} tokens at least, got "
+                         f"{tuple(q.shape)} and {tuple(k.shape)}")
+    hq, hk, t = q.shape[1], k.shape[1], q.shape[0]
+    _same_device(q.device, k=k, v=v, out=out)
+    _call_on(q.device, stream, lib().prompt_attention, _rows(q, "q"), _rows(k, "k", hk, d, t), _rows(v, "v", hk, d, t),
+             hq, hk, d, plan.handle, float(scale), _rows(out, "out", hq, d, t))
+
+
+class PagedKV:
+    """One layer's paged cache over the caller's tensors: k, v [n_pages, kv heads, page_size, D], bf16 or
+    torch.float8_e4m3fn; for the latter k_exp, v_exp uint8 [n_pages, kv heads, page_size] (see mv_paged_kv)."""
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        import torch
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype:
+            raise ValueError(f"PagedKV: k and v are both bf16 or both float8_e4m3fn, got {k.dtype} and {v.dtype}")
+        if k.dim() != 4 or v.shape != k.shape or not k.is_cuda:
+            raise ValueError(f"PagedKV: k and v are CUDA tensors [n_pages, kv heads, page_size, head_dim], got "
+                             f"{tuple(k.shape)} and {tuple(v.shape)} on {k.device}")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        for name, e in (("k_exp", k_exp), ("v_exp", v_exp)):
+            if (e is not None) != e4m3:
+                raise ValueError(f"PagedKV: {name} belongs to e4m3 pages and to no others")
+            if e is not None and (e.dtype != torch.uint8 or e.shape != k.shape[:3]):
+                raise ValueError(f"PagedKV: {name} is uint8 {tuple(k.shape[:3])}, got {e.dtype} {tuple(e.shape)}")
+        _same_device(k.device, v=v, k_exp=k_exp, v_exp=v_exp)
+        if any(t is not None and not t.is_contiguous() for t in (k, v, k_exp, v_exp)):
+            raise ValueError("PagedKV: the pages must be contiguous")
+        self.k, self.v, self.k_exp, self.v_exp, self.device = k, v, k_exp, v_exp, k.device
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self._desc = _PagedKVDesc(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
+                                  v_exp.data_ptr() if e4m3 else None, DTYPE_E4M3 if e4m3 else DTYPE_BF16,
+                                  self.n_pages, self.page_size, self.n_kv_heads, self.head_dim)
+
+    @classmethod
+    def zeros(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=DTYPE_BF16, device="cuda"):
+        """A pool of zero pages, DTYPE_BF16 or DTYPE_E4M3."""
+        import torch
+        if dtype not in (DTYPE_BF16, DTYPE_E4M3):
+            raise ValueError(f"PagedKV.zeros: DTYPE_BF16 or DTYPE_E4M3, got {dtype}")
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        if dtype == DTYPE_BF16:
+            return cls(torch.zeros(shape, dtype=torch.bfloat16, device=device),
+                       torch.zeros(shape, dtype=torch.bfloat16, device=device))
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+        ke, ve = (torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in range(2))
+        return cls(k, v, ke, ve)
+
+    def _seqs(self, block_table, seq_lens):
+        """block_table int32 [n_seq, pages] and seq_lens int32 [n_seq] as the arguments of the C entry points."""
+        table, lens = _ints(block_table, "block_table", 2, self.device), _ints(seq_lens, "seq_lens", 1, self.device)
+        n, pages = block_table.shape
+        if seq_lens.shape[0] != n:
+            raise ValueError(f"block_table has {n} rows, seq_lens {seq_lens.shape[0]}")
+        return table, block_table.stride(0) if n > 1 else pages, pages, lens, n
+
+
+def _cu(cu_rows, n_seq, device):
+    p = _ints(cu_rows, "cu_rows", 1, device)
+    if cu_rows.shape[0] != n_seq + 1:
+        raise ValueError(f"cu_rows has {cu_rows.shape[0]} entries, {n_seq + 1} are wanted")
+    return p
+
+
+def paged_kv_append(k, v, cu_rows, cache: PagedKV, block_table, seq_lens, stream=None):
+    """Writes rows cu_rows[b] .. of k, v bf16 [rows, kv heads, D] as the last ones of sequence b (the last at position
+    seq_lens[b] - 1); cu_rows int32 [n_seq + 1], block_table int32 [n_seq, pages], seq_lens int32 [n_seq]."""
+    table, ld, pages, lens, n = cache._seqs(block_table, seq_lens)
+    cu = _cu(cu_rows, n, cache.device)
+    _same_device(cache.device, k=k, v=v)
+    rk = _rows(k, "k", cache.n_kv_heads, cache.head_dim)
+    _call_on(cache.device, stream, lib().paged_kv_append, rk,
+             _rows(v, "v", cache.n_kv_heads, cache.head_dim, k.shape[0]), k.shape[0], cu, cache._desc, table, ld,
+             pages, lens, n)
+
+
+def paged_kv_read(cache: PagedKV, block_table, seq_lens, cu_rows, k_out, v_out, stream=None):
+    """The last rows of every sequence as bf16 [rows, kv heads, D]: the mirror of paged_kv_append."""
+    table, ld, pages, lens, n = cache._seqs(block_table, seq_lens)
+    cu = _cu(cu_rows, n, cache.device)
+    _same_device(cache.device, k_out=k_out, v_out=v_out)
+    rk = _rows(k_out, "k_out", cache.n_kv_heads, cache.head_dim)
+    _call_on(cache.device, stream, lib().paged_kv_read, cache._desc, table, ld, pages, lens, n, cu, k_out.shape[0], rk,
+             _rows(v_out, "v_out", cache.n_kv_heads, cache.head_dim, k_out.shape[0]))
+
+
+def paged_attention_workspace(n_seq, n_heads, n_kv_heads, head_dim):
+    return _ws_size(lib().paged_attention_workspace, n_seq, n_heads, n_kv_heads, head_dim)
+
+
+def paged_attention(q, cache: PagedKV, block_table, seq_lens, scale, out, workspace, stream=None):
+    """One new token per sequence: q, out bf16 [n_seq, heads, D]; attends to the first seq_lens[b] rows of sequence b."""
+    table, ld, pages, lens, n = cache._seqs(block_table, seq_lens)
+    _same_device(cache.device, q=q, out=out, workspace=workspace)
+    rq = _rows(q, "q", None, cache.head_dim, n)
+    heads = q.shape[1]
+    if not workspace.is_contiguous():
+        raise ValueError("paged_attention: the workspace must be contiguous")
+    _call_on(cache.device, stream, lib().paged_attention, rq, heads, cache._desc, table, ld, pages, lens, n,
+             float(scale), _rows(out, "out", heads, cache.head_dim, n), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size())
 
 
 # --------------------------------------------------------------------------------------------- model / session

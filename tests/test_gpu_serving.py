@@ -1,0 +1,592 @@
+"""GPU parity of the serving operators (packed prompt attention, paged cache rows, paged attention) with the oracle.
+
+Tolerances. What a cache holds is compared bit for bit. An attention's element may be off its float64 value by
+  u |ref|                the result's rounding to bf16, u = 2^-8 of its magnitude at most (half a step),
+  (w + 2 s + n 2^-23) A  with A = sum_j p_j |v_j|: the weights' own rounding w (bf16: 2^-8), the error s of an exponent,
+                         (D + 8) 2^-23 scale max_j sum_d |q_d k_jd| for products summed in fp32 plus the rounding of the
+                         exponent itself, and fp32 sums over n keys.
+"""
+import numpy as np
+import pytest
+import torch
+
+import medusa_tree_speculative_verify_gb300 as mv
+from oracle import serving
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+BF16, E4M3 = mv.DTYPE_BF16, mv.DTYPE_E4M3
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    mv.lib()
+
+
+def normal(seed, *shape, std=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(torch.bfloat16)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def check(got, ref, mag, q, k, scale, keys):
+    """Every element within the bound above; q [.., Hq, D], k [.., Hk, D] float64 (their finite entries)."""
+    d = q.shape[-1]
+    group = q.shape[-2] // k.shape[-2]
+    kmax = np.max(np.abs(np.where(np.isfinite(k), k, 0.0)).reshape(-1, k.shape[-2], d), axis=0, initial=0.0)
+    dots = scale * np.sum(np.abs(np.where(np.isfinite(q), q, 0.0)) * np.repeat(kmax, group, axis=0), axis=-1)
+    s = ((d + 8) * 2.0 ** -23 * dots)[..., None]
+    tol = U * np.abs(ref) + (U + 2 * s + (keys + 8) * 2.0 ** -23) * mag + 1e-30
+    fin = np.isfinite(ref)
+    assert np.array_equal(np.isnan(ref), np.isnan(got))
+    assert np.array_equal(ref[~fin & ~np.isnan(ref)], got[~fin & ~np.isnan(ref)])
+    off = np.abs(got - ref)[fin] / tol[fin]
+    assert off.size == 0 or off.max() <= 1.0, f"{off.max():.2f} of the bound"
+
+
+# ------------------------------------------------------------------------------------------------ prompts
+
+def run_prompt(lens, hq, hk, d, seed=0, scale=None, std=1.0, extra=0):
+    t = sum(lens) + extra
+    q, k, v = normal(seed, t, hq, d, std=std), normal(seed + 1, t, hk, d, std=std), normal(seed + 2, t, hk, d)
+    out = torch.full_like(q, 7.0)
+    scale = d ** -0.5 if scale is None else scale
+    mv.prompt_attention(q, k, v, mv.PromptPlan(lens, hq // hk), scale, out)
+    torch.cuda.synchronize()
+    return q, k, v, out, scale
+
+
+def check_prompt(q, k, v, out, lens, scale):
+    n = sum(lens)
+    ref, mag = serving.prompt_attention(f64(q)[:n], f64(k)[:n], f64(v)[:n], lens, scale)
+    check(f64(out)[:n], ref, mag, f64(q)[:n], f64(k)[:n], scale, max(lens, default=0))
+
+
+@pytest.mark.parametrize("lens", [[1], [2], [127], [128], [129], [256], [257, 1, 64], [0, 5, 0, 300], [640, 33]])
+@pytest.mark.parametrize("hq,hk,d", [(2, 2, 128), (4, 2, 64)])
+def test_prompt_lengths(lens, hq, hk, d):
+    q, k, v, out, scale = run_prompt(lens, hq, hk, d)
+    check_prompt(q, k, v, out, lens, scale)
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (3, 1), (5, 1), (7, 1), (16, 2), (6, 3)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_groups(hq, hk, d):
+    lens = [300, 70, 129]
+    q, k, v, out, scale = run_prompt(lens, hq, hk, d, seed=hq)
+    check_prompt(q, k, v, out, lens, scale)
+
+
+@pytest.mark.parametrize("d", [8, 16, 24, 32, 40, 72, 80, 96, 104, 120])
+def test_prompt_head_dims(d):
+    lens = [200, 17]
+    q, k, v, out, scale = run_prompt(lens, 4, 2, d, seed=d)
+    check_prompt(q, k, v, out, lens, scale)
+
+
+@pytest.mark.parametrize("scale,std", [(0.0, 1.0), (0.5, 4.0), (1.0, 6.0), (1e-3, 1.0)])
+def test_prompt_scales(scale, std):
+    """Uniform weights, and scores whose maximum moves by far more than any threshold within a row."""
+    lens = [500, 90]
+    q, k, v, out, scale = run_prompt(lens, 2, 1, 64, seed=9, scale=scale, std=std)
+    check_prompt(q, k, v, out, lens, scale)
+
+
+def test_prompt_rising_scores():
+    """Each later key scores higher, so every tile moves the running maximum."""
+    n, d = 900, 64
+    q = torch.ones(n, 1, d, dtype=torch.bfloat16, device="cuda")
+    k = (torch.arange(n, device="cuda")[:, None, None] * 0.05).expand(n, 1, d).to(torch.bfloat16).contiguous()
+    v, out = normal(3, n, 1, d), torch.empty_like(q)
+    mv.prompt_attention(q, k, v, mv.PromptPlan([n]), 0.2, out)
+    check_prompt(q, k, v, out, [n], 0.2)
+
+
+def test_prompt_long():
+    lens = [2500, 1111]
+    q, k, v, out, scale = run_prompt(lens, 2, 1, 128, seed=4)
+    check_prompt(q, k, v, out, lens, scale)
+
+
+def test_prompt_leaves_rows_behind_the_plan():
+    lens = [130, 20]
+    q, k, v, out, scale = run_prompt(lens, 2, 2, 64, extra=45)
+    check_prompt(q, k, v, out, lens, scale)
+    assert (out[150:] == 7.0).all()
+
+
+@pytest.mark.parametrize("layout", ["fused_qkv", "head_major"])
+def test_prompt_strides(layout):
+    lens, hq, hk, d = [190, 61], 4, 2, 64
+    n = sum(lens)
+    if layout == "fused_qkv":
+        x = normal(1, n, hq + 2 * hk, d)
+        q, k, v = x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:]
+        out = torch.full((n, hq + 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        dst = out[:, :hq]
+    else:
+        q, k, v = (normal(i, h, n + 9, d)[:, :n].transpose(0, 1) for i, h in ((1, hq), (2, hk), (3, hk)))
+        out = torch.full((hq, n + 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        dst = out[:, :n].transpose(0, 1)
+    mv.prompt_attention(q, k, v, mv.PromptPlan(lens, hq // hk), 0.125, dst)
+    check_prompt(q, k, v, dst, lens, 0.125)
+    assert (out[:, hq:] == 7.0).all() if layout == "fused_qkv" else (out[:, n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("at", [0, 100, 131, 299])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_masked_places_hold_anything(bad, at, d):
+    """A NaN or infinity in one token's v (and k) leaves the rows before it and the other prompts as they were."""
+    lens, hq, hk = [150, 300, 40], 4, 2
+    n = sum(lens)
+    q, k, v = normal(1, n, hq, d), normal(2, n, hk, d), normal(3, n, hk, d)
+    plan = mv.PromptPlan(lens, 2)
+    clean, out = torch.empty_like(q), torch.empty_like(q)
+    mv.prompt_attention(q, k, v, plan, 0.125, clean)
+    v2, k2 = v.clone(), k.clone()
+    v2[150 + at, 1, 3] = bad
+    mv.prompt_attention(q, k, v2, plan, 0.125, out)
+    torch.cuda.synchronize()
+    hit = torch.zeros_like(q, dtype=torch.bool)
+    hit[150 + at:450, 2:, 3] = True                           # the rows that see it, their heads, its element
+    # a row that sees it is computed again another way: the same value within the roundings, not bit for bit
+    near = torch.zeros_like(hit)
+    near[150:450, 2:] = True
+    assert torch.equal(out[~near], clean[~near])
+    assert torch.isfinite(out[~hit]).all() and not torch.isfinite(out[hit]).any()
+    ref, mag = serving.prompt_attention(f64(q), f64(k), f64(v2), lens, 0.125)
+    fin = np.isfinite(ref)
+    assert np.array_equal(fin, ~hit.cpu().numpy())
+    off = np.abs(f64(out)[fin] - ref[fin]) / (U * np.abs(ref) + 1.1 * U * mag)[fin]
+    assert off.max() <= 1.0
+    k2[150 + at, 0, 0] = bad
+    mv.prompt_attention(q, k2, v, plan, 0.125, out)
+    torch.cuda.synchronize()
+    keep = torch.ones_like(hit)
+    keep[150 + at:450, :2] = False
+    assert torch.equal(out[keep], clean[keep])
+
+
+def test_prompt_rows_do_not_depend_on_the_pack():
+    lens, hq, hk, d = [200, 77, 400], 4, 1, 128
+    q, k, v, out, scale = run_prompt(lens, hq, hk, d, seed=5)
+    t = 0
+    for n in lens:
+        alone = torch.empty_like(out[t:t + n])
+        mv.prompt_attention(q[t:t + n], k[t:t + n], v[t:t + n], mv.PromptPlan([n], hq // hk), scale, alone)
+        assert torch.equal(alone, out[t:t + n])
+        t += n
+
+
+def test_prompt_captured_and_on_another_stream():
+    lens, hq, hk, d = [260, 33], 2, 1, 64
+    q, k, v, out, scale = run_prompt(lens, hq, hk, d, seed=6)
+    plan, got = mv.PromptPlan(lens, 2), torch.zeros_like(out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    mv.prompt_attention(q, k, v, plan, scale, got, stream=side)
+    side.synchronize()
+    assert torch.equal(got, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mv.prompt_attention(q, k, v, plan, scale, got)
+    got.zero_()
+    q.copy_(normal(60, *q.shape))
+    g.replay()
+    torch.cuda.synchronize()
+    check_prompt(q, k, v, got, lens, scale)
+
+
+def test_prompt_of_no_tokens():
+    e = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    mv.prompt_attention(e, e, e, mv.PromptPlan([0, 0]), 1.0, torch.empty_like(e))
+    mv.prompt_attention(e, e, e, mv.PromptPlan([]), 1.0, torch.empty_like(e))
+
+
+# ------------------------------------------------------------------------------------------------ paged rows
+
+class Pool:
+    """A paged cache with shuffled pages, sequences of ``lens`` rows and spare table columns that name no page."""
+
+    def __init__(self, lens, hk, d, page, dtype, seed=0, spare=2):
+        r = np.random.default_rng(seed)
+        need = [-(-n // page) for n in lens]
+        self.lens, self.page, self.dtype, n_pages = list(lens), page, dtype, sum(need) + 3
+        order, at = r.permutation(n_pages), 0
+        self.table = np.full((len(lens), max(need, default=0) + spare), -77)
+        for b, k in enumerate(need):
+            self.table[b, :k] = order[at:at + k]
+            at += k
+        self.cache = mv.PagedKV.zeros(n_pages, page, hk, d, dtype)
+        self.d_table, self.d_lens = i32(self.table), i32(lens)
+
+    def fill(self, seed, std=1.0):
+        """Every row of the pool random, rows of very different sizes; values() are what they stand for."""
+        c = self.cache
+        for x, e, s in ((c.k, c.k_exp, seed), (c.v, c.v_exp, seed + 1)):
+            rows = normal(s, *x.shape, std=std) * torch.exp(normal(s + 50, *x.shape[:3], 1).float()).to(torch.bfloat16)
+            if self.dtype == BF16:
+                x.copy_(rows)
+            else:
+                q, ex = serving.quantise(f64(rows))
+                x.view(torch.uint8).copy_(torch.as_tensor(q))
+                e.copy_(torch.as_tensor(ex))
+        return self
+
+    def values(self):
+        c = self.cache
+        if self.dtype == BF16:
+            return f64(c.k), f64(c.v)
+        return tuple(serving.stored_value(x.view(torch.uint8).cpu().numpy(), e.cpu().numpy())
+                     for x, e in ((c.k, c.k_exp), (c.v, c.v_exp)))
+
+    def bits(self):
+        c = self.cache
+        return [t.view(torch.uint8).clone() for t in (c.k, c.v, c.k_exp, c.v_exp) if t is not None]
+
+
+def same_bits(a, b):
+    return len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def rows_like_a_model(seed, *shape):
+    """Rows of very different sizes, some all zero, some tiny, some near the type's limits."""
+    x = normal(seed, *shape).float() * torch.exp2(normal(seed + 1, *shape[:-1], 1).float() * 6)
+    x[::7, 0] = 0.0
+    x[3::11, -1] *= 2.0 ** -110
+    x[5::13, 0] *= 2.0 ** 100
+    x[:, :, 1::5] *= 0.01
+    return x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("hk,d,page,lens,rows", [
+    (2, 128, 16, [5, 40, 16], [5, 40, 16]), (1, 64, 32, [33, 1, 0, 70], [1, 1, 0, 1]), (3, 16, 48, [100, 7], [55, 0]),
+    (5, 80, 16, [31], [17]), (8, 128, 64, [500, 64, 65], [500, 64, 65]), (2, 32, 1024, [1030, 9], [1030, 9]),
+    (1, 112, 256, [300], [299])])
+def test_append_and_read_back(dtype, hk, d, page, lens, rows):
+    pool = Pool(lens, hk, d, page, dtype)
+    before = pool.bits()
+    cu = np.concatenate([[0], np.cumsum(rows)])
+    n = int(cu[-1]) + 6                                       # padded rows behind the last sequence
+    k, v = rows_like_a_model(1, n, hk, d), rows_like_a_model(9, n, hk, d)
+    mv.paged_kv_append(k, v, i32(cu), pool.cache, pool.d_table, pool.d_lens)
+    torch.cuda.synchronize()
+    want = [x.cpu().numpy().copy() for x in before]
+    for plane, x in enumerate((k, v)):
+        if dtype == E4M3:
+            q, e = serving.quantise(f64(x))
+        else:
+            q = x.view(torch.uint8).cpu().numpy()
+        for b in range(len(lens)):
+            for i in range(rows[b]):
+                pos = lens[b] - rows[b] + i
+                at = pool.table[b, pos // page], slice(None), pos % page
+                want[plane][at] = q[cu[b] + i]
+                if dtype == E4M3:
+                    want[2 + plane][at] = e[cu[b] + i]
+    assert same_bits(pool.bits(), [torch.as_tensor(w).cuda() for w in want])
+    ko, vo = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    mv.paged_kv_read(pool.cache, pool.d_table, pool.d_lens, i32(cu), ko, vo)
+    torch.cuda.synchronize()
+    for x, y in ((k, ko), (v, vo)):
+        assert (y[cu[-1]:] == 7.0).all()
+        ref = f64(x)[:cu[-1]]
+        if dtype == E4M3:
+            ref = serving.stored_value(*serving.quantise(ref))
+        with np.errstate(over="ignore"):
+            ref = torch.as_tensor(ref.astype(np.float32)).to(torch.bfloat16)
+        assert torch.equal(y[:cu[-1]].cpu(), ref)
+
+
+def test_append_nan_and_infinity():
+    d = 64
+    x = torch.zeros(4, 1, d, dtype=torch.bfloat16, device="cuda")
+    x[:, 0, 0] = torch.tensor([1.0, float("nan"), float("inf"), -float("inf")])
+    x[:, 0, 1] = 3.0
+    pool = Pool([4], 1, d, 16, E4M3)
+    out = torch.empty_like(x)
+    mv.paged_kv_append(x, x, i32([0, 4]), pool.cache, pool.d_table, pool.d_lens)
+    mv.paged_kv_read(pool.cache, pool.d_table, pool.d_lens, i32([0, 4]), out, torch.empty_like(x))
+    got = out[:, 0].float().cpu()
+    assert got[0, 0] == 1.0 and torch.isnan(got[1, 0]) and got[2, 0] == float("inf") and got[3, 0] == -float("inf")
+    assert got[:2, 1].tolist() == [3.0, 3.0]                  # a NaN leaves its row's other values alone
+    assert (got[:, 2:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_rows_with_strides_into_a_session_layout(dtype):
+    """Written from and read into [H][S][D] planes, the layout of a session's cache."""
+    hk, d, n = 4, 64, 90
+    pool = Pool([n], hk, d, 32, dtype)
+    src = normal(1, 2, hk, 128, d)
+    dst = torch.full_like(src, 7.0)
+    k, v = (src[c, :, 20:20 + n].transpose(0, 1) for c in range(2))
+    ko, vo = (dst[c, :, 3:3 + n].transpose(0, 1) for c in range(2))
+    mv.paged_kv_append(k, v, i32([0, n]), pool.cache, pool.d_table, pool.d_lens)
+    mv.paged_kv_read(pool.cache, pool.d_table, pool.d_lens, i32([0, n]), ko, vo)
+    torch.cuda.synchronize()
+    assert (dst[:, :, :3] == 7.0).all() and (dst[:, :, 3 + n:] == 7.0).all()
+    for x, y in ((k, ko), (v, vo)):
+        want = f64(x) if dtype == BF16 else serving.stored_value(*serving.quantise(f64(x)))
+        assert np.array_equal(f64(y), want)
+
+
+def take_error(site):
+    st, code = mv.get_error()
+    assert st == 6 and code >> 16 == site and code & 0xffff == 2
+
+
+@pytest.mark.parametrize("what", ["page_high", "page_low", "len_high", "len_negative", "too_many_rows", "cu_falls",
+                                  "cu_past_rows", "cu_first"])
+def test_rows_out_of_range_are_reported_and_left_alone(what):
+    hk, d, page = 2, 64, 16
+    pool = Pool([20, 40], hk, d, page, E4M3, spare=0)
+    table, lens, cu = pool.table.copy(), [20, 40], [0, 20, 60]
+    if what == "page_high":
+        table[1, 1] = pool.cache.n_pages
+    elif what == "page_low":
+        table[1, 1] = -1
+    elif what == "len_high":
+        lens[1] = 49                                          # three pages of 16 in the table's row
+    elif what == "len_negative":
+        lens[1] = -5
+    elif what == "too_many_rows":
+        lens[1] = 39
+    elif what == "cu_falls":
+        cu = [0, 20, 5]
+    elif what == "cu_past_rows":
+        cu = [0, 20, 61]
+        lens[1] = 41
+    elif what == "cu_first":
+        cu = [3, 20, 60]
+        lens[0] = 17
+    x = normal(1, 60, hk, d)
+    before = pool.bits()
+    mv.paged_kv_append(x, x, i32(cu), pool.cache, i32(table), i32(lens))
+    take_error(40)
+    changed = [(a != b) for a, b in zip(pool.bits(), before)]
+    legal = set(int(p) for p in pool.table.ravel() if p >= 0)
+    for c in changed:                                         # nothing outside the sequences' own pages
+        rest = [p for p in range(pool.cache.n_pages) if p not in legal]
+        assert not c[rest].any()
+    out = torch.full_like(x, 7.0)
+    mv.paged_kv_read(pool.cache, i32(table), i32(lens), i32(cu), out, out.clone())
+    take_error(40)
+
+
+# ------------------------------------------------------------------------------------------------ paged attention
+
+def run_paged(pool, q, scale, table=None, lens=None, ws=None):
+    b, hq, d = q.shape
+    if ws is None:
+        ws = torch.zeros(mv.paged_attention_workspace(b, hq, pool.cache.n_kv_heads, d), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 7.0)
+    mv.paged_attention(q, pool.cache, pool.d_table if table is None else table, pool.d_lens if lens is None else lens,
+                       scale, out, ws)
+    torch.cuda.synchronize()
+    return out
+
+
+def check_paged(pool, q, out, scale, lens=None):
+    lens = pool.lens if lens is None else lens
+    kp, vp = pool.values()
+    ref, mag = serving.paged_attention(f64(q), kp, vp, pool.table, lens, scale)
+    got = f64(out)
+    for b, n in enumerate(lens):
+        k = serving.sequence_rows(kp, pool.table[b], n)
+        check(got[b:b + 1], ref[b:b + 1], mag[b:b + 1], f64(q)[b:b + 1], k, scale, n)
+
+
+LENS = [[1], [0], [16, 15, 17, 0, 1], [127, 128, 129, 255, 257], [700, 3], [1], [64] * 9]
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("hq,hk,d,page", [(8, 2, 128, 16), (4, 4, 64, 32)])
+def test_paged_attention_lengths(dtype, lens, hq, hk, d, page):
+    pool = Pool(lens, hk, d, page, dtype).fill(1)
+    q = normal(3, len(lens), hq, d)
+    out = run_paged(pool, q, d ** -0.5)
+    check_paged(pool, q, out, d ** -0.5)
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert (out[b] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (3, 1), (7, 1), (8, 1), (9, 1), (10, 2), (16, 1), (17, 1), (40, 2), (33, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_attention_groups(dtype, hq, hk, d):
+    lens = [200, 35]
+    pool = Pool(lens, hk, d, 16, dtype).fill(hq)
+    q = normal(3, len(lens), hq, d)
+    check_paged(pool, q, run_paged(pool, q, d ** -0.5), d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("d", [16, 32, 48, 80, 96, 112])
+@pytest.mark.parametrize("page", [16, 48, 1024])
+def test_paged_attention_head_dims_and_pages(dtype, d, page):
+    lens = [333, 48, 49]
+    pool = Pool(lens, 2, d, page, dtype).fill(d)
+    q = normal(3, len(lens), 6, d)
+    check_paged(pool, q, run_paged(pool, q, d ** -0.5), d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_paged_attention_long_and_many(dtype):
+    """One sequence long enough to be split over the whole GPU, and more sequences than SMs."""
+    pool = Pool([9001, 2], 1, 64, 64, dtype).fill(1)
+    q = normal(3, 2, 4, 64)
+    check_paged(pool, q, run_paged(pool, q, 0.125), 0.125)
+    lens = [int(x) for x in np.random.default_rng(0).integers(0, 300, 400)]
+    pool = Pool(lens, 2, 64, 16, dtype).fill(1)
+    q = normal(3, len(lens), 4, 64)
+    check_paged(pool, q, run_paged(pool, q, 0.125), 0.125)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("scale,std", [(0.0, 1.0), (1.0, 3.0)])
+def test_paged_attention_scales(dtype, scale, std):
+    pool = Pool([400, 50], 2, 64, 16, dtype).fill(1, std)
+    q = normal(3, 2, 6, 64, std=std)
+    check_paged(pool, q, run_paged(pool, q, scale), scale)
+
+
+def test_paged_attention_value_rows_of_any_size():
+    """Value rows whose scales lie far apart, a row of zeros under the largest weight among them."""
+    n, d = 64, 64
+    k = normal(1, n, 1, d, std=0.1)
+    v = (normal(2, n, 1, d).float() * torch.exp2(torch.linspace(-60, 40, n, device="cuda"))[:, None, None])
+    q = normal(3, 1, 2, d)
+    k[5], v[5] = q[0, :1] * 3, 0.0
+    v = v.to(torch.bfloat16)
+    pool = Pool([n], 1, d, 16, E4M3)
+    mv.paged_kv_append(k, v, i32([0, n]), pool.cache, pool.d_table, pool.d_lens)
+    out = run_paged(pool, q, 1.0)
+    check_paged(pool, q, out, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n", [1, 13, 16, 100])
+def test_paged_attention_ignores_what_lies_behind(dtype, n):
+    pool = Pool([n], 2, 128, 64, dtype).fill(1)
+    q = normal(3, 1, 8, 128)
+    clean = run_paged(pool, q, 0.1)
+    c = pool.cache
+    for x in (c.k, c.v, c.k_exp, c.v_exp):
+        if x is None:
+            continue
+        raw = x.view(torch.uint8)
+        keep = [(int(pool.table[0, p // 64]), p % 64) for p in range(n)]
+        junk = torch.full_like(raw, 0x7f) if x.dtype != torch.uint8 else torch.full_like(raw, 0xff)
+        for page, slot in keep:
+            junk[page, :, slot] = raw[page, :, slot]
+        if dtype == BF16:
+            junk = torch.where(junk == 0x7f, torch.full_like(junk, 0xff), junk)  # 0xffff: a NaN
+            for page, slot in keep:
+                junk[page, :, slot] = raw[page, :, slot]
+        raw.copy_(junk)
+    assert torch.equal(run_paged(pool, q, 0.1), clean)
+
+
+def test_paged_attention_strides_and_shared_pages():
+    """q and out as slices of wider rows; two sequences that share their first pages."""
+    pool = Pool([100, 70], 2, 64, 16, BF16).fill(1)
+    pool.table[1, :4] = pool.table[0, :4]
+    pool.d_table = i32(np.pad(pool.table, ((0, 0), (0, 5)), constant_values=-9))[:, :pool.table.shape[1]]
+    x = normal(3, 2, 9, 64)
+    q, buf = x[:, 2:6], torch.full((4, 2, 64 + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[:, :, :64].transpose(0, 1)
+    ws = torch.zeros(mv.paged_attention_workspace(2, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    mv.paged_attention(q, pool.cache, pool.d_table, pool.d_lens, 0.125, out, ws)
+    check_paged(pool, q, out, 0.125)
+    assert (buf[:, :, 64:] == 7.0).all()
+
+
+def test_paged_attention_repeats_bit_for_bit_and_leaves_its_workspace_clean():
+    pool = Pool([5000, 3, 800], 2, 128, 16, E4M3).fill(1)
+    q = normal(3, 3, 8, 128)
+    ws = torch.zeros(mv.paged_attention_workspace(3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    first = run_paged(pool, q, 0.1, ws=ws)
+    small = Pool([40], 1, 64, 16, BF16).fill(2)               # another shape through the same workspace in between
+    run_paged(small, normal(4, 1, 2, 64), 0.1, ws=ws)
+    for _ in range(20):
+        assert torch.equal(run_paged(pool, q, 0.1, ws=ws), first)
+
+
+@pytest.mark.parametrize("what", ["page_high", "page_low", "len_high", "len_negative"])
+def test_paged_attention_out_of_range_is_reported(what):
+    pool = Pool([200, 40, 30], 2, 64, 16, E4M3, spare=0).fill(1)
+    q = normal(3, 3, 4, 64)
+    ws = torch.zeros(mv.paged_attention_workspace(3, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    good = run_paged(pool, q, 0.1, ws=ws)
+    table, lens = pool.table.copy(), list(pool.lens)
+    if what == "page_high":
+        table[0, 7] = pool.cache.n_pages
+    elif what == "page_low":
+        table[0, 7] = -1
+    elif what == "len_high":
+        lens[1] = table.shape[1] * 16 + 1
+    else:
+        lens[1] = -1
+    run_paged(pool, q, 0.1, i32(table), i32(lens), ws)
+    take_error(41)
+    assert torch.equal(run_paged(pool, q, 0.1, ws=ws), good)  # the workspace serves later calls
+
+
+def test_paged_attention_of_no_sequences():
+    c = mv.PagedKV.zeros(1, 16, 2, 64)
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(mv.paged_attention_workspace(0, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    mv.paged_attention(q, c, i32(np.zeros((0, 3))), i32([]), 1.0, torch.empty_like(q), ws)
+
+
+def test_decode_loop_captured_once_and_replayed():
+    """Prefill, then a captured step (write the new token's row, attend) replayed as the lengths grow in place."""
+    lens, hq, hk, d, page, steps = [30, 77], 4, 2, 64, 16, 5
+    t, scale = sum(lens), 0.125
+    full = [normal(i, 2, 100, h, d) for i, h in ((1, hq), (2, hk), (3, hk))]   # every sequence's whole stream
+    pool = Pool([n + steps for n in lens], hk, d, page, BF16)
+    cur = i32(lens)
+    pack = [torch.cat([x[b, :n] for b, n in enumerate(lens)]) for x in full]
+    out = torch.empty_like(pack[0])
+    mv.prompt_attention(*pack, mv.PromptPlan(lens, hq // hk), scale, out)
+    check_prompt(*pack, out, lens, scale)
+    mv.paged_kv_append(pack[1], pack[2], i32(np.cumsum([0] + lens)), pool.cache, pool.d_table, cur)
+    q, k, v = (torch.zeros(2, x.shape[2], d, dtype=torch.bfloat16, device="cuda") for x in full)
+    o, one = torch.zeros_like(q), i32([0, 1, 2])
+    ws = torch.zeros(mv.paged_attention_workspace(2, hq, hk, d), dtype=torch.uint8, device="cuda")
+    saved = cur.clone()
+
+    def step():
+        cur.add_(1)
+        mv.paged_kv_append(k, v, one, pool.cache, pool.d_table, cur)
+        mv.paged_attention(q, pool.cache, pool.d_table, cur, scale, o, ws)
+
+    step()                                                    # warm-up; its row is written again by the replay
+    cur.copy_(saved)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(steps):
+        for x, y in ((q, full[0]), (k, full[1]), (v, full[2])):
+            x.copy_(torch.stack([y[b, n + i] for b, n in enumerate(lens)]))
+        g.replay()
+        torch.cuda.synchronize()
+        for b, n in enumerate(lens):
+            m = n + i + 1
+            ref, mag = serving.prompt_attention(f64(full[0][b, :m]), f64(full[1][b, :m]), f64(full[2][b, :m]), [m], scale)
+            check(f64(o[b:b + 1]), ref[-1:], mag[-1:], f64(q[b:b + 1]), f64(full[1][b, :m]), scale, m)

@@ -1,0 +1,165 @@
+"""The serving operators on the host (no GPU needed): the prompt plan's work items, the refusals of every entry point
+before anything is launched, and the oracle's e4m3 against torch's type."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import medusa_tree_speculative_verify_gb300 as mv
+from oracle import serving
+
+INVALID, SHAPE, CAPACITY, CUDA = 1, 2, 4, 5
+FAKE = 0x100000                                 # never dereferenced: every call here fails its checks first
+
+
+@pytest.mark.parametrize("lens,group", [([1], 1), ([128], 1), ([129], 1), ([0, 5, 0, 300], 3), ([257, 1, 64], 2),
+                                        ([1000, 3, 513], 8), ([], 4), ([0, 0], 1)])
+def test_plan_covers_every_sub_tile_once_longest_first(lens, group):
+    plan = mv.PromptPlan(lens, group)
+    items = plan.items()
+    assert plan.n_tokens == sum(lens) and plan.n_items == len(items)
+    starts = np.cumsum([0] + lens)[:-1]
+    want = {(int(s), t) for s, n in zip(starts, lens) for t in range(-(-n // 128) * group)}
+    got = []
+    for start, n, t, keys in items.tolist():
+        assert n in [m for s, m in zip(starts, lens) if s == start and m]
+        tiles = -(-n // 128) * group
+        assert t % 2 == 0 and 0 <= t < tiles and keys == min(t + 1, tiles - 1) // group + 1
+        got += [(start, u) for u in (t, t + 1) if u < tiles]
+    assert len(got) == len(set(got)) and set(got) == want
+    assert (np.diff(items[:, 3]) <= 0).all()
+
+
+@pytest.mark.parametrize("lens,group,status", [([-1], 1, INVALID), ([1], 0, INVALID), ([1], 257, SHAPE),
+                                               ([2 ** 31 - 1], 1, SHAPE), ([2 ** 30, 2 ** 30], 1, SHAPE),
+                                               ([2 ** 29] * 3, 256, SHAPE)])
+def test_plan_refusals(lens, group, status):
+    arr, out = (ctypes.c_int32 * len(lens))(*lens), ctypes.c_void_p(1)
+    assert mv.lib().mv_prompt_plan_create(arr, len(lens), group, ctypes.byref(out)) == status
+    assert not out.value
+    assert mv.lib().mv_prompt_plan_create(None, 1, 1, ctypes.byref(out)) == INVALID
+    assert mv.lib().mv_prompt_plan_create(arr, 1, 1, None) == INVALID
+    with pytest.raises(ValueError):
+        mv.PromptPlan([-1])
+
+
+def rows(ptr=FAKE, ts=1024, hs=128):
+    return mv._Rows(ptr, ts, hs)
+
+
+def cache(**kw):
+    d = dict(k=FAKE, v=FAKE, k_exp=FAKE, v_exp=FAKE, dtype=mv.DTYPE_E4M3, n_pages=8, page_size=16, n_kv_heads=2,
+             head_dim=128)
+    d.update(kw)
+    return mv._PagedKVDesc(*(d[n] for n, _ in mv._PagedKVDesc._fields_))
+
+
+BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(k_exp=None), INVALID), (dict(v_exp=None), INVALID),
+              (dict(dtype=mv.DTYPE_F32), INVALID), (dict(dtype=7), INVALID), (dict(k=FAKE + 8), INVALID),
+              (dict(n_pages=0), SHAPE), (dict(page_size=8), SHAPE), (dict(page_size=24), SHAPE),
+              (dict(page_size=2048), SHAPE), (dict(n_kv_heads=0), SHAPE), (dict(n_kv_heads=257), SHAPE),
+              (dict(head_dim=8), SHAPE), (dict(head_dim=72), SHAPE), (dict(head_dim=144), SHAPE)]
+BAD_ROWS = [dict(ptr=None), dict(ptr=FAKE + 2), dict(ts=-8), dict(ts=1028), dict(hs=132), dict(ts=64), dict(hs=64),
+            dict(ts=2 ** 30)]
+
+
+def append(c=None, k=None, v=None, n=4, cu=FAKE, table=FAKE, ld=4, pages=4, lens=FAKE, n_seq=2):
+    return mv.lib().paged_kv_append(k or rows(), v or rows(), n, cu, c or cache(), table, ld, pages, lens, n_seq, None)
+
+
+def read(c=None, k=None, v=None, n=4, cu=FAKE, table=FAKE, ld=4, pages=4, lens=FAKE, n_seq=2):
+    return mv.lib().paged_kv_read(c or cache(), table, ld, pages, lens, n_seq, cu, n, k or rows(), v or rows(), None)
+
+
+def attention(c=None, q=None, out=None, heads=4, table=FAKE, ld=4, pages=4, lens=FAKE, n_seq=2, scale=0.1, ws=FAKE,
+              nbytes=1 << 30):
+    return mv.lib().paged_attention(q or rows(), heads, c or cache(), table, ld, pages, lens, n_seq, scale,
+                                    out or rows(), ws, nbytes, None)
+
+
+@pytest.mark.parametrize("call", [append, read, attention])
+def test_paged_refusals_of_every_call(call):
+    for kw, status in BAD_CACHES:
+        assert call(cache(**kw)) == status, kw
+    assert call(table=None) == call(lens=None) == INVALID
+    assert call(n_seq=-1) == INVALID
+    assert call(n_seq=4097) == SHAPE
+    assert call(pages=0) == SHAPE and call(ld=3) == SHAPE
+    assert call(ld=1 << 28, pages=1 << 28) == SHAPE           # more positions than 31 bits count
+    assert call(n_seq=0) == 0                                 # nothing to do
+
+
+@pytest.mark.parametrize("call", [append, read])
+def test_paged_row_refusals(call):
+    for kw in BAD_ROWS:
+        assert call(k=rows(**kw)) == INVALID and call(v=rows(**kw)) == INVALID, kw
+    assert call(cu=None) == INVALID and call(n=-1) == INVALID
+    assert call(n=0) == 0
+    if call is read:                                          # rows that overlap may be read, not written
+        assert call(k=rows(ts=128, hs=128)) == INVALID
+
+
+def test_paged_attention_refusals():
+    for kw in BAD_ROWS:
+        assert attention(q=rows(**kw)) == INVALID and attention(out=rows(**kw)) == INVALID, kw
+    assert attention(out=rows(ts=128, hs=128)) == INVALID
+    assert attention(heads=3) == attention(heads=0) == attention(heads=258) == SHAPE
+    assert attention(ws=None) == attention(ws=FAKE + 4) == INVALID
+    assert attention(nbytes=64) == CAPACITY
+    for s in (float("nan"), float("inf"), -0.5):
+        assert attention(scale=s) == INVALID
+    assert mv.paged_attention_workspace(4, 8, 2, 64) > 0
+    for bad in ((4097, 8, 2, 64), (4, 7, 2, 64), (4, 8, 0, 64), (4, 8, 2, 72), (4, 512, 2, 64)):
+        with pytest.raises(mv.MVError):
+            mv.paged_attention_workspace(*bad)
+
+
+def test_prompt_attention_refusals():
+    plan = mv.PromptPlan([3, 200], 2)
+
+    def call(q=None, k=None, v=None, out=None, hq=4, hk=2, d=128, p=plan.handle, scale=0.1):
+        return mv.lib().prompt_attention(q or rows(), k or rows(), v or rows(), hq, hk, d, p, scale, out or rows(), None)
+
+    for kw in BAD_ROWS:
+        for name in ("q", "k", "v", "out"):
+            assert call(**{name: rows(**kw)}) == INVALID, (name, kw)
+    assert call(out=rows(ts=128, hs=128)) == INVALID
+    assert call(p=None) == INVALID
+    assert call(hq=6) == call(hk=1) == call(hq=0, hk=0) == call(hq=512, hk=256) == SHAPE
+    assert call(d=4) == call(d=136) == call(d=100) == SHAPE
+    for s in (float("nan"), float("inf"), -0.5):
+        assert call(scale=s) == INVALID
+    if not torch.cuda.is_available():
+        assert call() == CUDA                                 # a plan without a device cannot run
+    empty = mv.PromptPlan([0, 0], 2)
+    assert call(p=empty.handle) == 0
+
+
+def test_binding_refuses_what_the_library_cannot_see():
+    t = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mv._rows(t, "q")                                      # not on a GPU
+    with pytest.raises(ValueError):
+        mv.PagedKV(t, t)
+    with pytest.raises(ValueError):
+        mv.PagedKV(torch.zeros(2, 2, 16, 64), torch.zeros(2, 2, 16, 64))
+    with pytest.raises(ValueError):
+        mv.PagedKV.zeros(2, 16, 2, 64, dtype=mv.DTYPE_F32, device="cpu")
+
+
+def test_oracle_e4m3_is_torchs():
+    b = torch.arange(256, dtype=torch.uint8)
+    want = b.view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(serving.e4m3_value(b.numpy()), want, equal_nan=True)
+    x = np.random.default_rng(0).uniform(-448, 448, 20000) * 2.0 ** -np.random.default_rng(1).integers(0, 18, 20000)
+    mid = (want[:126] + want[1:127]) / 2                      # ties
+    x = np.concatenate([x, mid, -mid, [0.0, 448.0, -448.0]]).astype(np.float32)
+    got = torch.tensor(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    assert np.array_equal(serving.e4m3_byte(x), got)
+
+
+def test_oracle_row_exponent():
+    for a, e in [(448.0, 0), (449.0, 1), (1.75, -8), (1.7578125, -7), (0.0, -100), (1e-38, -100), (3.3e38, 120),
+                 (float("inf"), 120), (224.0, -1), (224.1, 0)]:
+        assert serving.row_exponent([[a, 0.0, -a / 2, float("nan")]])[0] == e, a
