@@ -160,16 +160,12 @@ def test_prompt_masked_places_hold_anything(bad, at, d):
     torch.cuda.synchronize()
     hit = torch.zeros_like(q, dtype=torch.bool)
     hit[150 + at:450, 2:, 3] = True                           # the rows that see it, their heads, its element
-    # a row that sees it is computed again another way: the same value within the roundings, not bit for bit
-    near = torch.zeros_like(hit)
-    near[150:450, 2:] = True
-    assert torch.equal(out[~near], clean[~near])
-    assert torch.isfinite(out[~hit]).all() and not torch.isfinite(out[hit]).any()
-    ref, mag = serving.prompt_attention(f64(q), f64(k), f64(v2), lens, 0.125)
+    assert torch.equal(out[~hit], clean[~hit])
+    assert not torch.isfinite(out[hit]).any()
+    ref, _ = serving.prompt_attention(f64(q), f64(k), f64(v2), lens, 0.125)
     fin = np.isfinite(ref)
     assert np.array_equal(fin, ~hit.cpu().numpy())
-    off = np.abs(f64(out)[fin] - ref[fin]) / (U * np.abs(ref) + 1.1 * U * mag)[fin]
-    assert off.max() <= 1.0
+    assert np.array_equal(np.isnan(ref), torch.isnan(out).cpu().numpy())
     k2[150 + at, 0, 0] = bad
     mv.prompt_attention(q, k2, v, plan, 0.125, out)
     torch.cuda.synchronize()
