@@ -522,7 +522,8 @@ mv_status paged_kv_read(const mv_paged_kv* cache, const int32_t* block_table, in
 /* One new token per sequence: for sequence b, query head h and kv head c = h / (n_heads / n_kv_heads),
  *   out[b][h] = sum_{j < seq_lens[b]} softmax_j(scale * q[b][h] . k_j[c]) v_j[c],   zeros when seq_lens[b] = 0.
  * The token's own row is in the cache already (paged_kv_append first). What pages hold behind a sequence's length does
- * not matter, NaN included. q, out device bf16 rows, token b = sequence b. Scores, softmax statistics and output
+ * not matter, NaN included; an infinity or a NaN in a row that is attended to makes that element of out one of the two.
+ * q, out device bf16 rows, token b = sequence b. Scores, softmax statistics and output
  * sums in fp32. The result does not depend on the order in which the parts of a split sequence finish.
  * Limits: n_heads % n_kv_heads == 0, n_heads <= 256. workspace: device memory of paged_attention_workspace() bytes,
  * 16-byte aligned, zero-filled before its first use (see the conventions above). Errors as above; MV_ERR_CAPACITY: the

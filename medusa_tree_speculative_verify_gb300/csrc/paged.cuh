@@ -47,6 +47,9 @@ inline mv_status mv_paged_check(const mv_paged_kv* c, const int32_t* table, int3
   if (c->dtype != MV_DTYPE_BF16 && c->dtype != MV_DTYPE_E4M3) return MV_ERR_INVALID_ARG;
   if (c->dtype == MV_DTYPE_E4M3 && (!c->k_exp || !c->v_exp)) return MV_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15) return MV_ERR_INVALID_ARG;
+  if (c->dtype == MV_DTYPE_E4M3 &&
+      ((reinterpret_cast<uintptr_t>(c->k_exp) | reinterpret_cast<uintptr_t>(c->v_exp)) & 15))
+    return MV_ERR_INVALID_ARG;
   if (c->n_pages < 1 || c->page_size < 16 || c->page_size > kPagedMaxPage || c->page_size % 16) return MV_ERR_SHAPE;
   if (c->n_kv_heads < 1 || c->n_kv_heads > kPagedMaxHeads) return MV_ERR_SHAPE;
   if (c->head_dim < 16 || c->head_dim > kPagedMaxDim || c->head_dim % 16) return MV_ERR_SHAPE;

@@ -1,82 +1,657 @@
 // Attention of one new token for each sequence over a paged cache (bf16, or e4m3 with an exponent for each row).
 //
-// A warp computes one (sequence, query head): a lane holds four of the dim values, the warp goes over the keys with
-// the running maximum and sum of the softmax.
+// Bound by the cache's bytes: every row is read once. What a kv head's query heads share is read for all of them
+// together, 8 (or 16) heads a work unit, on the tensor cores with the keys as the rows of the products (mma.sync
+// m16n8k16): S^T = K Q^T and O^T += V^T P^T. At 8 heads a unit the products cost 16 to 24 instructions for each 16 keys'
+// 4 to 8 KB, far below what the copies take, and keys as rows waste nothing on padding the heads.
+//
+// Copies. The order of the dim in a dot product, and of the dim as output rows, is free, so each lane copies (cp.async)
+// exactly the 16-byte pieces that it needs as its own operands into a place of its own and reads them back alone: a
+// first-in first-out queue for each lane, with no bank conflict, no barrier and kStages - 1 steps in flight.
+//   K: lane (g, t) = (lane / 4, lane % 4) takes rows g and g + 8 of 16 keys, pieces t, t + 4, ..; the words of a piece
+//      are consecutive dim pairs, a product's k index 2 t, 2 t + 1, 2 t + 8, 2 t + 9. Q is read in the same order.
+//   V: rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9, piece g: pairs of rows are interleaved byte-wise (prmt) to operands.
+// P goes from the layout of S^T to that of P^T by a transposing movmatrix.
+//
+// e4m3: K and V convert exactly to fp16. Q is brought to fp16 with a power of two for each head (largest element in
+// [2^14, 2^15), so what fp16 loses lies 2^-38 below it). A key row's scale multiplies its score; a value row's scale
+// 2^e goes into the weight's exponent: 2^(x + e - ref) with a reference of its own, so weights of the largest values are
+// in fp16's range and what underflows lies 2^-24 below them; the sum of the softmax keeps the reference of x. Weights in
+// fp16 have 11 bits. bf16: the weights are split in two bf16 (16 bits), one more product each.
+//
+// Split. The work is a line of steps, kWarps tiles of keys each, over all units (sequence, kv head, 8 or 16 of its
+// heads); every CTA takes an equal piece of the line, whatever the lengths are. A unit within one CTA is done there; one
+// that crosses pieces leaves partial results (reference, sum, output in fp32) in the workspace, and the CTA that adds
+// the last one joins all of them in the order of the line, so the result does not depend on who comes last.
+#include <algorithm>
+
 #include "kernels.cuh"
 #include "paged.cuh"
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kCounters = 1024;
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kStages = 3;       // steps of a warp's queue
+constexpr int kMaxCtas = 320;   // counters at the start of the workspace
+constexpr int kChunkSeq = 1024;  // sequences of one launch
 
 struct AttnArgs {
   PagedArgs c;
   RowsArgs q, out;
-  int n_heads;
+  int group, parts;  // query heads of a kv head, units of a kv head
   float scale_log2;
+  unsigned int* count;  // [kMaxCtas]
+  float* part;          // [CTAs][2] partial results
   unsigned int* err;
 };
 
-template <bool kE4M3>
-MV_DEV float4 load4(const uint8_t* pages, const uint8_t* exps, int64_t row, int D, int d0) {
-  if (kE4M3) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(pages + row * D + d0);
-    const float s = exp_byte_scale(exps[row]);
-    const float2 a = half2_to_float2(e4m3x2_to_half2((uint16_t)w)), b = half2_to_float2(e4m3x2_to_half2((uint16_t)(w >> 16)));
-    return make_float4(a.x * s, a.y * s, b.x * s, b.y * s);
-  }
-  const uint2 w = *reinterpret_cast<const uint2*>(pages + (row * D + d0) * 2);
-  return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-}
+template <int kDim, bool kE4M3, int kNT>
+struct Layout {
+  static constexpr int kSub = kE4M3 ? 2 : 1;        // 16-key tiles of a warp's step
+  static constexpr int kKeys = 16 * kSub;           // keys of a warp's step
+  static constexpr int kRow = kE4M3 ? kDim : 2 * kDim;  // bytes
+  static constexpr int kVPiece = kRow / 8 < 16 ? 8 : 16;  // bytes a lane copies of a value row at once
+  static constexpr int kKPieces = 2 * (kRow / 64);  // of a lane and 16 keys: rows g, g + 8
+  static constexpr int kVPieces = 4 * (kRow / 8 / kVPiece);
+  static constexpr int kTileBytes = 32 * (16 * kKPieces + kVPiece * kVPieces);  // 16 keys, K and V
+  static constexpr int kStage = kSub * kTileBytes + (kE4M3 ? 64 : 0);           // and their exponents
+  static constexpr int kMT = kDim / 16;             // 16-row tiles of O^T
+  static constexpr int kHeads = 8 * kNT;
+  static constexpr int kSlot = kMT * 4 * 32;        // floats of one warp's O^T of 8 heads
+  static constexpr int kPart = kHeads * (kDim + 4); // floats of a partial result
+  static constexpr int kQueue = kWarps * kStages * kStage, kMerge = 4 * kSlot * 4;
+  static int bytes(int n_seq) { return kQueue + kMerge + (2 * n_seq + 1) * 4; }
+};
 
-template <bool kE4M3>
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const AttnArgs a) {
+MV_DEV void cp16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+MV_DEV void cp8(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+MV_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+MV_DEV void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+MV_DEV uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+MV_DEV uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+MV_DEV uint32_t lds_byte(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+template <bool kF16>
+MV_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (kF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+MV_DEV uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+MV_DEV uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+MV_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 2^(a - b) where both may be -inf (then the weight of nothing: 0)
+MV_DEV float weight(float a, float b) { return a == -INFINITY ? 0.0f : exp2f(a - b); }
+
+// A place on the line of steps: the sequence and, of that sequence's steps, which one.
+struct Place {
+  int b, in_b;  // in_b / nb: its unit of the sequence, in_b % nb: its step of the unit
+};
+
+template <int kDim, bool kE4M3, int kNT>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const AttnArgs a) {
+  using Ly = Layout<kDim, kE4M3, kNT>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float s_ml[kWarps][3][8];
+  __shared__ int s_scan[kWarps];
+  __shared__ unsigned int s_last;
+  float* s_merge = reinterpret_cast<float*>(smem + Ly::kQueue);
+  int* s_pre = reinterpret_cast<int*>(smem + Ly::kQueue + Ly::kMerge);  // [n_seq + 1] first step of each sequence
+  int* s_len = s_pre + a.c.n_seq + 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int n_seq = a.c.n_seq, units = a.c.heads * a.parts;  // units of a sequence
+  constexpr int kStepKeys = kWarps * Ly::kKeys;
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31, u = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (u >= a.c.n_seq * a.n_heads) return;
-  const int b = u / a.n_heads, h = u % a.n_heads, kh = h / (a.n_heads / a.c.heads);
-  const int D = a.c.dim, P = a.c.page_size, d0 = lane * 4;
-  const bool on = d0 < D;
-  const int len = __ldcg(a.c.seq_lens + b);
-  if (len < 0 || len > a.c.max_pages * P) {
-    if (lane == 0) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)b);
-    return;
-  }
-  float4 q = make_float4(0.f, 0.f, 0.f, 0.f), o = q;
-  const int64_t qat = (int64_t)b * a.q.ts + (int64_t)h * a.q.hs + d0;
-  if (on) {
-    const uint2 w = *reinterpret_cast<const uint2*>(a.q.p + qat);
-    q = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-  }
-  float m = -INFINITY, l = 0.0f;
-  for (int j = 0; j < len; ++j) {
-    const int page = __ldcg(a.c.table + (int64_t)b * a.c.ld_table + j / P);
-    if (page < 0 || page >= a.c.n_pages) {
-      if (lane == 0) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)page);
-      return;
+
+  // ---- the line: every sequence's steps (one for an empty sequence: its zeros are written; none for a bad length)
+  int carry = 0;
+  for (int base = 0; base < n_seq; base += kThreads) {
+    const int b = base + tid;
+    int steps = 0;
+    if (b < n_seq) {
+      int len = __ldcg(a.c.seq_lens + b);
+      const bool bad = len < 0 || len > a.c.max_pages * a.c.page_size;
+      if (bad && blockIdx.x == 0) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)b);
+      steps = bad ? 0 : max(1, (len + kStepKeys - 1) / kStepKeys) * units;
+      s_len[b] = bad ? 0 : len;
     }
-    const int64_t row = ((int64_t)page * a.c.heads + kh) * P + j % P;
-    float x = 0.0f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on) {
-      const float4 k = load4<kE4M3>(a.c.k, a.c.k_exp, row, D, d0);
-      v = load4<kE4M3>(a.c.v, a.c.v_exp, row, D, d0);
-      x = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-    }
+    int incl = steps;
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    x *= a.scale_log2;
-    const float mn = fmaxf(m, x), f = m == mn ? 1.0f : exp2f(m - mn), p = exp2f(x - mn);
-    m = mn;
-    l = l * f + p;
-    o = make_float4(o.x * f + p * v.x, o.y * f + p * v.y, o.z * f + p * v.z, o.w * f + p * v.w);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    int before = carry, all = carry;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_scan[w];
+      all += s_scan[w];
+    }
+    if (b < n_seq) s_pre[b] = before + incl - steps;
+    carry = all;
+    __syncthreads();
   }
-  const float inv = len > 0 ? 1.0f / l : 0.0f;
-  if (on)
-    *reinterpret_cast<uint2*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)h * a.out.hs + d0) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (tid == 0) s_pre[n_seq] = carry;
+  __syncthreads();
+  const int total = carry, ctas = min((int)gridDim.x, total), cta = blockIdx.x;
+  if (cta >= ctas) return;
+  auto piece = [&](int c) { return (int)((int64_t)total * c / ctas); };
+  const int s_begin = piece(cta), s_end = piece(cta + 1);  // at least one step
+  auto place_of = [&](int s) {
+    int lo = 0, hi = n_seq;  // the last b with pre[b] <= s; sequences without steps are stepped over
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_pre[mid] <= s) lo = mid;
+      else hi = mid;
+    }
+    return Place{lo, s - s_pre[lo]};
+  };
+  auto steps_of = [&](int b) { return max(1, (s_len[b] + kStepKeys - 1) / kStepKeys); };
+
+  // ---- this lane's queue
+  const uint32_t queue = smem_u32(smem) + warp * kStages * Ly::kStage;
+  const int page16 = a.c.page_size >> 4;
+  Place ahead = place_of(s_begin);
+  int s_ahead = s_begin, n_ahead = steps_of(ahead.b);
+  int pages[Ly::kSub];  // of the step that is copied next
+  auto look_up = [&]() {
+    if (s_ahead >= s_end) return;
+    const int key0 = (ahead.in_b % n_ahead * kWarps + warp) * Ly::kKeys;
+#pragma unroll
+    for (int u = 0; u < Ly::kSub; ++u) {
+      const int key = key0 + 16 * u;
+      pages[u] = key < s_len[ahead.b] ? __ldcg(a.c.table + (int64_t)ahead.b * a.c.ld_table + (key >> 4) / page16) : 0;
+    }
+  };
+  auto copy_step = [&](int slot) {
+    if (s_ahead < s_end) {
+      const int len = s_len[ahead.b], unit = ahead.in_b / n_ahead, h = unit / a.parts;
+      const int key0 = (ahead.in_b - unit * n_ahead) * kStepKeys + warp * Ly::kKeys;
+#pragma unroll
+      for (int u = 0; u < Ly::kSub; ++u) {
+        const int left = len - key0 - 16 * u;  // rows of this tile that the sequence has
+        if (left <= 0) break;
+        const bool ok = pages[u] >= 0 && pages[u] < a.c.n_pages;
+        if (!ok && lane == 0) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)pages[u]);
+        const int64_t row0 =
+            ok ? ((int64_t)pages[u] * a.c.heads + h) * a.c.page_size + ((key0 >> 4) + u) % page16 * 16 : 0;
+        const int bytes = kE4M3 ? a.c.dim : 2 * a.c.dim;  // of a row
+        uint32_t dst = queue + slot * Ly::kStage + u * Ly::kTileBytes + lane * 16;
+#pragma unroll
+        for (int i = 0; i < Ly::kKPieces; ++i) {
+          const int r = g + 8 * (i & 1), at = 16 * (t + 4 * (i >> 1));
+          const bool on = ok && r < left && at < bytes;
+          cp16(dst, a.c.k + (on ? (row0 + r) * bytes + at : 0), on);
+          dst += 512;
+        }
+        dst -= lane * (16 - Ly::kVPiece);
+#pragma unroll
+        for (int i = 0; i < Ly::kVPieces; ++i) {
+          const int r = 2 * t + (i & 1) + 8 * ((i >> 1) & 1), at = Ly::kVPiece * (g + 8 * (i >> 2));
+          const bool on = ok && r < left && at < bytes;
+          const uint8_t* src = a.c.v + (on ? (row0 + r) * bytes + at : 0);
+          if (Ly::kVPiece == 16) cp16(dst, src, on);
+          else cp8(dst, src, on);
+          dst += 32 * Ly::kVPiece;
+        }
+        if (kE4M3 && lane < 2)
+          cp16(queue + slot * Ly::kStage + Ly::kSub * Ly::kTileBytes + (2 * u + lane) * 16,
+               (lane ? a.c.v_exp : a.c.k_exp) + row0, ok);
+      }
+      ++s_ahead;
+      if (s_ahead < s_end) {
+        ++ahead.in_b;
+        while (s_pre[ahead.b + 1] <= s_ahead) {  // s_ahead < total: ends at the last sequence with steps
+          ++ahead.b;
+          ahead.in_b = 0;
+        }
+        n_ahead = steps_of(ahead.b);
+      }
+    }
+    cp_commit();
+    look_up();
+  };
+  look_up();
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) copy_step(i);
+
+  // ---- unit after unit
+  Place here = place_of(s_begin);
+  int s = s_begin, slot = 0;
+  while (s < s_end) {
+    const int b = here.b, len = s_len[b], nb = steps_of(b), unit = here.in_b / nb, step0 = here.in_b - unit * nb;
+    const int steps = min(nb - step0, s_end - s);  // of this unit, here
+    const int kh = unit / a.parts, head0 = kh * a.group + (unit % a.parts) * Ly::kHeads;
+    const int n_heads = min(Ly::kHeads, (kh + 1) * a.group - head0);
+
+    // Q as the second operand: head g (of each tile of 8), the dim in the order of the K pieces
+    uint32_t qf[kNT][kDim / 16][2];
+    float mult[kNT][2];  // score of head 2 t (+ 1) into the exponent
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      const int h = 8 * n + g;
+      const uint16_t* row = a.q.p + (int64_t)b * a.q.ts + (int64_t)(head0 + (h < n_heads ? h : 0)) * a.q.hs;
+      constexpr int kWords = kE4M3 ? 8 : 4;  // words of Q for a piece of K
+      uint32_t w[kDim / 8];
+#pragma unroll
+      for (int i = 0; i < Ly::kKPieces / 2; ++i) {
+        const int d = 2 * kWords * (t + 4 * i);
+#pragma unroll
+        for (int j = 0; j < kWords; j += 4) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (h < n_heads && d + 2 * j < a.c.dim) v = *reinterpret_cast<const uint4*>(row + d + 2 * j);
+          w[i * kWords + j] = v.x;
+          w[i * kWords + j + 1] = v.y;
+          w[i * kWords + j + 2] = v.z;
+          w[i * kWords + j + 3] = v.w;
+        }
+      }
+      if (kE4M3) {
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i) top = fmaxf(top, fmaxf(fabsf(bf16lo(w[i])), fabsf(bf16hi(w[i]))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t e = max(15u, __float_as_uint(top) >> 23);
+        const float up = __uint_as_float((268u - e) << 23), back = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i) qf[n][i >> 1][i & 1] = pack_f16x2(bf16lo(w[i]) * up, bf16hi(w[i]) * up);
+        mult[n][0] = __shfl_sync(0xffffffffu, back, 8 * t) * a.scale_log2;
+        mult[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4) * a.scale_log2;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kDim / 8; ++i) qf[n][i >> 1][i & 1] = w[i];
+        mult[n][0] = mult[n][1] = a.scale_log2;
+      }
+    }
+    float o[kNT][Ly::kMT][4], mx[kNT][2], my[kNT][2], l[kNT][2];
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+      for (int m = 0; m < Ly::kMT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][m][e] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[n][e] = my[n][e] = -INFINITY;
+        l[n][e] = 0.0f;
+      }
+    }
+
+    for (int i = 0; i < steps; ++i) {
+      if (kE4M3) __syncwarp();  // every lane has read the exponents that the next copy overwrites
+      copy_step(slot == 0 ? kStages - 1 : slot - 1);
+      cp_wait<kStages - 1>();
+      if (kE4M3) __syncwarp();  // the exponents come from other lanes' copies
+      const int key0 = (step0 + i) * kStepKeys + warp * Ly::kKeys;
+      const uint32_t at = queue + slot * Ly::kStage;
+      slot = slot + 1 == kStages ? 0 : slot + 1;
+      if (key0 >= len) continue;
+
+      // S^T: rows keys g, g + 8 of each tile, columns heads 2 t, 2 t + 1
+      float x[kNT][Ly::kSub][4];
+#pragma unroll
+      for (int u = 0; u < Ly::kSub; ++u) {
+        if (u > 0 && key0 + 16 * u >= len) {  // nothing was copied there
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[n][u][e] = -INFINITY;
+          continue;
+        }
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[n][u][e] = 0.0f;
+        const uint32_t kt = at + u * Ly::kTileBytes + lane * 16;
+#pragma unroll
+        for (int i2 = 0; i2 < Ly::kKPieces / 2; ++i2) {
+          const uint4 lo = lds16(kt + i2 * 1024), hi = lds16(kt + i2 * 1024 + 512);  // keys g, g + 8
+          const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+          if (kE4M3) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a0 = e4m3x2_to_half2((uint16_t)wl[j]), a2 = e4m3x2_to_half2((uint16_t)(wl[j] >> 16));
+              const uint32_t a1 = e4m3x2_to_half2((uint16_t)wh[j]), a3 = e4m3x2_to_half2((uint16_t)(wh[j] >> 16));
+#pragma unroll
+              for (int n = 0; n < kNT; ++n)
+                mma<true>(x[n][u], a0, a1, a2, a3, qf[n][4 * i2 + j][0], qf[n][4 * i2 + j][1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int n = 0; n < kNT; ++n)
+                mma<false>(x[n][u], wl[2 * j], wh[2 * j], wl[2 * j + 1], wh[2 * j + 1], qf[n][2 * i2 + j][0],
+                           qf[n][2 * i2 + j][1]);
+          }
+        }
+      }
+      // scores into the exponent's base; the value rows' exponents
+      float ev[Ly::kSub][2];
+#pragma unroll
+      for (int u = 0; u < Ly::kSub; ++u)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int key = key0 + 16 * u + g + 8 * r;
+          float ks = 1.0f;
+          ev[u][r] = 0.0f;
+          if (kE4M3) {
+            const uint32_t ex = at + Ly::kSub * Ly::kTileBytes + 32 * u + g + 8 * r;
+            ks = exp_byte_scale(lds_byte(ex));
+            ev[u][r] = (float)((int)lds_byte(ex + 16) - 127);
+          }
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& v = x[n][u][2 * r + e];
+              v = key < len ? v * (kE4M3 ? ks * mult[n][e] : mult[n][e]) : -INFINITY;
+            }
+        }
+      // the references: moved when a score outgrows them by 2^8 (as far as fp16 weights reach)
+      bool grow = false;
+      float tx[kNT][2], ty[kNT][2];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          tx[n][e] = ty[n][e] = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < Ly::kSub; ++u)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              tx[n][e] = fmaxf(tx[n][e], x[n][u][2 * r + e]);
+              ty[n][e] = fmaxf(ty[n][e], x[n][u][2 * r + e] + ev[u][r]);
+            }
+          // from nothing: at the first key that is seen
+          grow |= tx[n][e] > mx[n][e] + 8.0f || (kE4M3 && ty[n][e] > my[n][e] + 8.0f);
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int w = 4; w <= 16; w <<= 1) {
+              tx[n][e] = fmaxf(tx[n][e], __shfl_xor_sync(0xffffffffu, tx[n][e], w));
+              if (kE4M3) ty[n][e] = fmaxf(ty[n][e], __shfl_xor_sync(0xffffffffu, ty[n][e], w));
+            }
+            const float nx = fmaxf(mx[n][e], tx[n][e]), ny = kE4M3 ? fmaxf(my[n][e], ty[n][e]) : nx;
+            l[n][e] *= weight(mx[n][e], nx);
+            const float f = weight(my[n][e], ny);
+#pragma unroll
+            for (int m = 0; m < Ly::kMT; ++m) {
+              o[n][m][e] *= f;
+              o[n][m][2 + e] *= f;
+            }
+            mx[n][e] = nx;
+            my[n][e] = ny;
+          }
+      }
+      // weights, their sum, and P^T as the second operand
+      uint32_t ph[kNT][Ly::kSub][2], pl[kNT][Ly::kSub][2];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int u = 0; u < Ly::kSub; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float p[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float v = x[n][u][2 * r + e], bx = mx[n][e] == -INFINITY ? 0.0f : mx[n][e];
+              p[e] = ex2(v - bx);
+              l[n][e] += p[e];
+              if (kE4M3) p[e] = ex2(v + ev[u][r] - (my[n][e] == -INFINITY ? 0.0f : my[n][e]));
+            }
+            if (kE4M3) {
+              ph[n][u][r] = transpose8x8(pack_f16x2(p[0], p[1]));
+            } else {
+              const uint32_t hi = pack_bf16x2(p[0], p[1]);
+              ph[n][u][r] = transpose8x8(hi);
+              pl[n][u][r] = transpose8x8(pack_bf16x2(p[0] - bf16lo(hi), p[1] - bf16hi(hi)));
+            }
+          }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int u = 0; u < Ly::kSub; ++u) {
+        if (u > 0 && key0 + 16 * u >= len) continue;
+        const uint32_t vt = at + u * Ly::kTileBytes + 512 * Ly::kKPieces + lane * Ly::kVPiece;
+        constexpr int kPieces = Ly::kVPieces / 4, kWords = Ly::kVPiece / 4;
+#pragma unroll
+        for (int i2 = 0; i2 < kPieces; ++i2) {
+          uint32_t w[4][kWords];  // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t src = vt + (4 * i2 + r) * 32 * Ly::kVPiece;
+            if (kWords == 4) {
+              const uint4 v = lds16(src);
+              w[r][0] = v.x;
+              w[r][1] = v.y;
+              w[r][kWords - 2] = v.z;
+              w[r][kWords - 1] = v.w;
+            } else {
+              const uint2 v = lds8(src);
+              w[r][0] = v.x;
+              w[r][1] = v.y;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) {
+            if (kE4M3) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {  // two of the word's four dims
+                const uint32_t sel = half ? 0x7362u : 0x5140u;
+                const uint32_t lo = __byte_perm(w[0][j], w[1][j], sel), hi = __byte_perm(w[2][j], w[3][j], sel);
+                const uint32_t a0 = e4m3x2_to_half2((uint16_t)lo), a1 = e4m3x2_to_half2((uint16_t)(lo >> 16));
+                const uint32_t a2 = e4m3x2_to_half2((uint16_t)hi), a3 = e4m3x2_to_half2((uint16_t)(hi >> 16));
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+                  mma<true>(o[n][2 * j + half], a0, a1, a2, a3, ph[n][u][0], ph[n][u][1]);
+              }
+            } else {
+              const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5410), a1 = __byte_perm(w[0][j], w[1][j], 0x7632);
+              const uint32_t a2 = __byte_perm(w[2][j], w[3][j], 0x5410), a3 = __byte_perm(w[2][j], w[3][j], 0x7632);
+#pragma unroll
+              for (int n = 0; n < kNT; ++n) {
+                mma<false>(o[n][4 * i2 + j], a0, a1, a2, a3, ph[n][u][0], ph[n][u][1]);
+                mma<false>(o[n][4 * i2 + j], a0, a1, a2, a3, pl[n][u][0], pl[n][u][1]);
+              }
+            }
+          }
+        }
+      }
+    }
+
+    // ---- the warps' results together, 8 heads at a time
+    const bool whole = steps == nb;
+    const int u0 = s - step0, u1 = u0 + nb;                     // the unit on the line
+    const int part = u0 <= s_begin ? 0 : 1;                     // this CTA's partial result of it
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int w = 4; w <= 16; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
+        if (g == 0) {
+          s_ml[warp][0][2 * t + e] = mx[n][e];
+          s_ml[warp][1][2 * t + e] = my[n][e];
+          s_ml[warp][2][2 * t + e] = l[n][e];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][1][2 * t + e]);
+        const float f = weight(my[n][e], top);
+#pragma unroll
+        for (int m = 0; m < Ly::kMT; ++m) {
+          o[n][m][e] *= f;
+          o[n][m][2 + e] *= f;
+        }
+      }
+      float* mine = s_merge + (warp & 3) * Ly::kSlot + lane;
+      if (warp >= 4) {
+#pragma unroll
+        for (int m = 0; m < Ly::kMT; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mine[(4 * m + e) * 32] = o[n][m][e];
+      }
+      __syncthreads();
+      if (warp < 4) {
+#pragma unroll
+        for (int m = 0; m < Ly::kMT; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mine[(4 * m + e) * 32] += o[n][m][e];
+      }
+      __syncthreads();
+      // thread: one head of the tile, 8 consecutive dims
+      for (int e = tid; e < 8 * kDim / 8; e += kThreads) {
+        const int ln = e & 31, odd = (e >> 5) & 1, i2 = e >> 6, hh = 2 * (ln & 3) + odd, h = 8 * n + hh;
+        const int d = kE4M3 ? kDim / 8 * (ln >> 2) + 8 * i2 : 8 * ((ln >> 2) + 8 * i2);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float* src = s_merge + ((4 * (4 * i2 + (k >> 1))) + 2 * (k & 1) + odd) * 32 + ln;
+          v[k] = (src[0] + src[Ly::kSlot]) + (src[2 * Ly::kSlot] + src[3 * Ly::kSlot]);
+        }
+        float tx = -INFINITY, ty = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          tx = fmaxf(tx, s_ml[w][0][hh]);
+          ty = fmaxf(ty, s_ml[w][1][hh]);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += s_ml[w][2][hh] * weight(s_ml[w][0][hh], tx);
+        if (h >= n_heads) continue;
+        if (whole) {
+          const float f = len > 0 ? (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum : 0.0f;
+          if (d < a.c.dim)
+            *reinterpret_cast<uint4*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)(head0 + h) * a.out.hs + d) =
+                make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
+                           pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
+        } else {
+          float* dst = a.part + (int64_t)(2 * cta + part) * Ly::kPart;
+          *reinterpret_cast<float4*>(dst + h * kDim + d) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(dst + h * kDim + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+          if (d == 0) *reinterpret_cast<float4*>(dst + Ly::kHeads * kDim + 4 * h) = make_float4(tx, ty, sum, 0.0f);
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- a unit over several CTAs: the last one to come joins the partial results in the order of the line
+    if (!whole) {
+      auto cta_of = [&](int step) {  // the CTA whose piece holds a step
+        int c = (int)((int64_t)step * ctas / total);
+        while (piece(c + 1) <= step) ++c;
+        while (piece(c) > step) --c;
+        return c;
+      };
+      const int c0 = cta_of(u0), c1 = cta_of(u1 - 1);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const unsigned int seen = atomicAdd(a.count + c0, 1u);
+        s_last = seen == (unsigned int)(c1 - c0);
+        if (s_last) atomicExch(a.count + c0, 0u);
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_last) {
+        for (int e = tid; e < Ly::kHeads * kDim / 8; e += kThreads) {
+          const int h = e / (kDim / 8), d = e % (kDim / 8) * 8;
+          if (h >= n_heads || d >= a.c.dim) continue;
+          const float* first = a.part + (int64_t)(2 * c0 + (u0 == piece(c0) ? 0 : 1)) * Ly::kPart;
+          float tx = -INFINITY, ty = -INFINITY, sum = 0.0f, v[8] = {};
+          for (int c = c0; c <= c1; ++c) {
+            const float* src = c == c0 ? first : a.part + (int64_t)(2 * c) * Ly::kPart;
+            const float4 ml = __ldcg(reinterpret_cast<const float4*>(src + Ly::kHeads * kDim + 4 * h));
+            const float4 lo = __ldcg(reinterpret_cast<const float4*>(src + h * kDim + d));
+            const float4 hi = __ldcg(reinterpret_cast<const float4*>(src + h * kDim + d + 4));
+            const float nx = fmaxf(tx, ml.x), ny = fmaxf(ty, ml.y);
+            sum = sum * weight(tx, nx) + ml.z * weight(ml.x, nx);
+            const float f0 = weight(ty, ny), f1 = weight(ml.y, ny);
+            const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = v[k] * f0 + w[k] * f1;
+            tx = nx;
+            ty = ny;
+          }
+          const float f = (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum;
+          *reinterpret_cast<uint4*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)(head0 + h) * a.out.hs + d) =
+              make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
+                         pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
+        }
+      }
+    }
+    s += steps;
+    if (s < s_end) {
+      here.in_b += steps;
+      while (s_pre[here.b + 1] <= s) {
+        ++here.b;
+        here.in_b = 0;
+      }
+    }
+  }
+  cp_wait<0>();
+}
+
+template <int kDim, bool kE4M3, int kNT>
+mv_status launch(const AttnArgs& a, cudaStream_t stream) {
+  using Ly = Layout<kDim, kE4M3, kNT>;
+  static int flags[64] = {};
+  const int bytes = Ly::bytes(a.c.n_seq);
+  if (!mv_set_smem_once((const void*)paged_attn_kernel<kDim, kE4M3, kNT>, Ly::bytes(kChunkSeq), flags)) return MV_ERR_CUDA;
+  const int64_t most = (int64_t)a.c.n_seq * a.c.heads * a.parts *
+                       (((int64_t)a.c.max_pages * a.c.page_size + kWarps * Ly::kKeys - 1) / (kWarps * Ly::kKeys));
+  if (most > 0x7fffffff) return MV_ERR_SHAPE;
+  const int grid = (int)std::min<int64_t>(most, std::min(mv_sm_count(), kMaxCtas));
+  const cudaError_t e = mv_launch(paged_attn_kernel<kDim, kE4M3, kNT>, dim3(grid), dim3(kThreads), bytes, stream, a);
+  return e == cudaSuccess ? mv_last_launch("paged_attention") : MV_ERR_CUDA;
 }
 
 }  // namespace
@@ -87,7 +662,8 @@ extern "C" mv_status paged_attention_workspace(int32_t n_seq, int32_t n_heads, i
   if (n_seq > kPagedMaxSeq || n_kv_heads < 1 || n_heads < n_kv_heads || n_heads > kPagedMaxHeads ||
       n_heads % n_kv_heads || head_dim < 16 || head_dim > kPagedMaxDim || head_dim % 16)
     return MV_ERR_SHAPE;
-  *bytes = kCounters * sizeof(uint32_t);
+  // counters, and two partial results of 16 heads for each CTA
+  *bytes = kMaxCtas * sizeof(uint32_t) + (size_t)kMaxCtas * 2 * Layout<128, false, 2>::kPart * sizeof(float);
   return MV_OK;
 }
 
@@ -106,15 +682,28 @@ extern "C" mv_status paged_attention(mv_rows q, int32_t n_heads, const mv_paged_
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) || !(scale >= 0.0f && scale < INFINITY))
     return MV_ERR_INVALID_ARG;
   if (ws_bytes < need) return MV_ERR_CAPACITY;
-  a.q = {static_cast<uint16_t*>(q.ptr), q.token_stride, q.head_stride};
-  a.out = {static_cast<uint16_t*>(out.ptr), out.token_stride, out.head_stride};
-  a.n_heads = n_heads;
+  a.group = n_heads / a.c.heads;
+  const bool wide = a.group > 8;  // 16 heads a unit: their second tile of 8 shares the copies
+  a.parts = wide ? (a.group + 15) / 16 : 1;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.count = static_cast<unsigned int*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxCtas * sizeof(uint32_t));
   a.err = mv_error_word();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid((n_seq * n_heads + kWarps - 1) / kWarps);
-  const cudaError_t e = cache->dtype == MV_DTYPE_E4M3
-                            ? mv_launch(paged_attn_kernel<true>, grid, dim3(kWarps * 32), 0, st, a)
-                            : mv_launch(paged_attn_kernel<false>, grid, dim3(kWarps * 32), 0, st, a);
-  return e == cudaSuccess ? mv_last_launch("paged_attention") : MV_ERR_CUDA;
+  const bool e4m3 = cache->dtype == MV_DTYPE_E4M3, big = a.c.dim > 64;
+  for (int first = 0; first < n_seq; first += kChunkSeq) {
+    a.c.n_seq = std::min(kChunkSeq, n_seq - first);
+    a.c.table = block_table + (int64_t)first * ld_table;
+    a.c.seq_lens = seq_lens + first;
+    a.q = {static_cast<uint16_t*>(q.ptr) + first * q.token_stride, q.token_stride, q.head_stride};
+    a.out = {static_cast<uint16_t*>(out.ptr) + first * out.token_stride, out.token_stride, out.head_stride};
+    if (big)
+      s = e4m3 ? (wide ? launch<128, true, 2>(a, st) : launch<128, true, 1>(a, st))
+               : (wide ? launch<128, false, 2>(a, st) : launch<128, false, 1>(a, st));
+    else
+      s = e4m3 ? (wide ? launch<64, true, 2>(a, st) : launch<64, true, 1>(a, st))
+               : (wide ? launch<64, false, 2>(a, st) : launch<64, false, 1>(a, st));
+    if (s != MV_OK) return s;
+  }
+  return MV_OK;
 }

@@ -56,7 +56,7 @@ def cache(**kw):
 
 
 BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(k_exp=None), INVALID), (dict(v_exp=None), INVALID),
-              (dict(dtype=mv.DTYPE_F32), INVALID), (dict(dtype=7), INVALID), (dict(k=FAKE + 8), INVALID),
+              (dict(dtype=mv.DTYPE_F32), INVALID), (dict(dtype=7), INVALID), (dict(k=FAKE + 8), INVALID), (dict(v_exp=FAKE + 4), INVALID),
               (dict(n_pages=0), SHAPE), (dict(page_size=8), SHAPE), (dict(page_size=24), SHAPE),
               (dict(page_size=2048), SHAPE), (dict(n_kv_heads=0), SHAPE), (dict(n_kv_heads=257), SHAPE),
               (dict(head_dim=8), SHAPE), (dict(head_dim=72), SHAPE), (dict(head_dim=144), SHAPE)]
