@@ -5,10 +5,11 @@
 // m16n8k16): S^T = K Q^T and O^T += V^T P^T. At 8 heads a unit the products cost 16 to 24 instructions for each 16 keys'
 // 4 to 8 KB, far below what the copies take, and keys as rows waste nothing on padding the heads.
 //
-// Copies. The order of the dim in a dot product, and of the dim as output rows, is free, so each lane copies (cp.async)
-// exactly the 16-byte pieces that it needs as its own operands into a place of its own and reads them back alone: a
-// first-in first-out queue for each lane, with no bank conflict, no barrier and kStages - 1 steps in flight.
-//   K: lane (g, t) = (lane / 4, lane % 4) takes rows g and g + 8 of 16 keys, pieces t, t + 4, ..; the words of a piece
+// Copies: by TMA, 16 rows of a page's head at a time, a queue of kStages steps of 8 KB for each warp, which waits for
+// nobody else. The order of the dim in a dot product, and of the dim as output rows, is free, so that each lane's operands
+// are whole 16-byte pieces of rows, read from shared memory without shuffles; the 128-byte swizzle of the copy keeps the
+// value reads free of bank conflicts and the key reads at two a bank.
+//   K: lane (g, t) = (lane / 4, lane % 4) reads rows g and g + 8 of 16 keys, pieces t, t + 4, ..; the words of a piece
 //      are consecutive dim pairs, a product's k index 2 t, 2 t + 1, 2 t + 8, 2 t + 9. Q is read in the same order.
 //   V: rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9, piece g: pairs of rows are interleaved byte-wise (prmt) to operands.
 // P goes from the layout of S^T to that of P^T by a transposing movmatrix.
@@ -47,33 +48,27 @@ struct AttnArgs {
 
 template <int kDim, bool kE4M3, int kNT>
 struct Layout {
-  static constexpr int kSub = kE4M3 ? 2 : 1;        // 16-key tiles of a warp's step
-  static constexpr int kKeys = 16 * kSub;           // keys of a warp's step
-  static constexpr int kRow = kE4M3 ? kDim : 2 * kDim;  // bytes
-  static constexpr int kVPiece = kRow / 8 < 16 ? 8 : 16;  // bytes a lane copies of a value row at once
-  static constexpr int kKPieces = 2 * (kRow / 64);  // of a lane and 16 keys: rows g, g + 8
-  static constexpr int kVPieces = 4 * (kRow / 8 / kVPiece);
-  static constexpr int kTileBytes = 32 * (16 * kKPieces + kVPiece * kVPieces);  // 16 keys, K and V
-  static constexpr int kStage = kSub * kTileBytes + (kE4M3 ? 64 : 0);           // and their exponents
-  static constexpr int kMT = kDim / 16;             // 16-row tiles of O^T
+  static constexpr int kRow = kE4M3 ? kDim : 2 * kDim;   // bytes of a row in shared memory
+  static constexpr int kBox = kRow < 128 ? kRow : 128;   // bytes of a row that a copy takes, and of the swizzle
+  static constexpr int kBoxes = kRow / kBox;             // copies for 16 rows
+  static constexpr int kRegion = 16 * kBox;              // bytes of one
+  static constexpr int kSub = 256 / kRow;                // 16-key tiles of a warp's step: 8 KB
+  static constexpr int kKeys = 16 * kSub;                // keys of a warp's step
+  static constexpr int kTile = 32 * kRow;                // bytes of 16 keys, K then V
+  static constexpr int kStage = kSub * kTile;
+  static constexpr int kExps = kE4M3 ? 32 * kSub : 0;    // bytes of their exponents
+  static constexpr int kOps = kSub * (2 * kBoxes + (kE4M3 ? 2 : 0));  // copies of a step, one lane each
+  static constexpr int kVPiece = kRow / 8 < 16 ? 8 : 16; // bytes a lane reads of a value row at once
+  static constexpr int kMT = kDim / 16;                  // 16-row tiles of O^T
   static constexpr int kHeads = 8 * kNT;
-  static constexpr int kSlot = kMT * 4 * 32;        // floats of one warp's O^T of 8 heads
-  static constexpr int kPart = kHeads * (kDim + 4); // floats of a partial result
+  static constexpr int kSlot = kMT * 4 * 32;             // floats of one warp's O^T of 8 heads
+  static constexpr int kPart = kHeads * (kDim + 4);      // floats of a partial result
   static constexpr int kQueue = kWarps * kStages * kStage, kMerge = 4 * kSlot * 4;
-  static int bytes(int n_seq) { return kQueue + kMerge + (2 * n_seq + 1) * 4; }
+  static constexpr int kExpsAt = kQueue, kMergeAt = kExpsAt + kWarps * kStages * kExps, kPreAt = kMergeAt + kMerge;
+  static_assert(kStage == 8192 && kOps <= 32 && kMergeAt % 16 == 0, "");
+  static int bytes(int n_seq) { return 1024 + kPreAt + (2 * n_seq + 1) * 4; }
 };
 
-MV_DEV void cp16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-MV_DEV void cp8(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
-}
-MV_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int n>
-MV_DEV void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
-}
 MV_DEV uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -88,6 +83,12 @@ MV_DEV uint32_t lds_byte(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
+}
+// 16 bytes of global memory to shared memory, counted on `bar`
+MV_DEV void bulk16(uint32_t dst, const void* src, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
+               "l"(src), "r"(smem_u32(bar))
+               : "memory");
 }
 template <bool kF16>
 MV_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -120,25 +121,28 @@ MV_DEV float ex2(float x) {
 // 2^(a - b) where both may be -inf (then the weight of nothing: 0)
 MV_DEV float weight(float a, float b) { return a == -INFINITY ? 0.0f : exp2f(a - b); }
 
-// A place on the line of steps: the sequence and, of that sequence's steps, which one.
-struct Place {
-  int b, in_b;  // in_b / nb: its unit of the sequence, in_b % nb: its step of the unit
-};
-
 template <int kDim, bool kE4M3, int kNT>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
   using Ly = Layout<kDim, kE4M3, kNT>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
   __shared__ float s_ml[kWarps][3][8];
   __shared__ int s_scan[kWarps];
   __shared__ unsigned int s_last;
-  float* s_merge = reinterpret_cast<float*>(smem + Ly::kQueue);
-  int* s_pre = reinterpret_cast<int*>(smem + Ly::kQueue + Ly::kMerge);  // [n_seq + 1] first step of each sequence
+  float* s_merge = reinterpret_cast<float*>(smem + Ly::kMergeAt);
+  int* s_pre = reinterpret_cast<int*>(smem + Ly::kPreAt);  // [n_seq + 1] first step of each sequence
   int* s_len = s_pre + a.c.n_seq + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int n_seq = a.c.n_seq, units = a.c.heads * a.parts;  // units of a sequence
   constexpr int kStepKeys = kWarps * Ly::kKeys;
   pdl_trigger();
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
+    mbar_fence_init();
+  }
   pdl_wait();
 
   // ---- the line: every sequence's steps (one for an empty sequence: its zeros are written; none for a bad length)
@@ -177,91 +181,120 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const AttnArgs 
   if (cta >= ctas) return;
   auto piece = [&](int c) { return (int)((int64_t)total * c / ctas); };
   const int s_begin = piece(cta), s_end = piece(cta + 1);  // at least one step
-  auto place_of = [&](int s) {
-    int lo = 0, hi = n_seq;  // the last b with pre[b] <= s; sequences without steps are stepped over
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_pre[mid] <= s) lo = mid;
-      else hi = mid;
-    }
-    return Place{lo, s - s_pre[lo]};
-  };
   auto steps_of = [&](int b) { return max(1, (s_len[b] + kStepKeys - 1) / kStepKeys); };
 
-  // ---- this lane's queue
-  const uint32_t queue = smem_u32(smem) + warp * kStages * Ly::kStage;
-  const int page16 = a.c.page_size >> 4;
-  Place ahead = place_of(s_begin);
-  int s_ahead = s_begin, n_ahead = steps_of(ahead.b);
-  int pages[Ly::kSub];  // of the step that is copied next
-  auto look_up = [&]() {
-    if (s_ahead >= s_end) return;
-    const int key0 = (ahead.in_b % n_ahead * kWarps + warp) * Ly::kKeys;
-#pragma unroll
-    for (int u = 0; u < Ly::kSub; ++u) {
-      const int key = key0 + 16 * u;
-      pages[u] = key < s_len[ahead.b] ? __ldcg(a.c.table + (int64_t)ahead.b * a.c.ld_table + (key >> 4) / page16) : 0;
+  // A place on the line: step `step` of the `n` of a unit (sequence b, kv head h, part of its query heads).
+  struct Place {
+    int b, h, part, step, n, len;
+  };
+  Place ahead;
+  {
+    int lo = 0, hi = n_seq;  // the last b with pre[b] <= s_begin: one with steps
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_pre[mid] <= s_begin) lo = mid;
+      else hi = mid;
     }
+    ahead.b = lo;
+    ahead.n = steps_of(lo);
+    ahead.len = s_len[lo];
+    const int in_b = s_begin - s_pre[lo], unit = in_b / ahead.n;
+    ahead.step = in_b - unit * ahead.n;
+    ahead.h = unit / a.parts;
+    ahead.part = unit - ahead.h * a.parts;
+  }
+  Place here = ahead;
+  // to the next unit, whose first step is s < total
+  auto next_unit = [&](Place& p, int s) {
+    p.step = 0;
+    if (++p.part < a.parts) return;
+    p.part = 0;
+    if (++p.h < a.c.heads) return;
+    p.h = 0;
+    do ++p.b;
+    while (s_pre[p.b + 1] <= s);
+    p.n = steps_of(p.b);
+    p.len = s_len[p.b];
+  };
+
+  // ---- this warp's queue. Each of the first kOps lanes does one of a step's copies: its 16-key tile u, K or V, a box of
+  // the row or the exponents. Page and tile in it are carried along: a step is kWarps * kSub tiles after the one before.
+  const uint32_t queue = smem_u32(smem) + warp * kStages * Ly::kStage;
+  const uint32_t exps = smem_u32(smem) + Ly::kExpsAt + warp * kStages * Ly::kExps;
+  const int page16 = a.c.page_size >> 4;
+  const int my_u = lane % Ly::kSub, my_op = lane / Ly::kSub;  // op: K boxes, V boxes, K and V exponents
+  const bool my_v = my_op >= 2 * Ly::kBoxes ? my_op & 1 : my_op >= Ly::kBoxes;
+  const int page_add = kWarps * Ly::kSub / page16, tile_add = kWarps * Ly::kSub % page16;
+  const int page_0 = (warp * Ly::kSub + my_u) / page16, tile_0 = (warp * Ly::kSub + my_u) % page16;
+  int s_ahead = s_begin, s_stop = s_end, page, tile, entry = 0;  // entry: the table's, of the step that is copied next
+  {
+    const int first = (ahead.step * kWarps + warp) * Ly::kSub + my_u;
+    page = first / page16;
+    tile = first - page * page16;
+  }
+  auto look_up = [&]() {
+    if (ahead.step * kStepKeys + warp * Ly::kKeys + 16 * my_u < ahead.len)
+      entry = __ldcg(a.c.table + (int64_t)ahead.b * a.c.ld_table + page);
   };
   auto copy_step = [&](int slot) {
-    if (s_ahead < s_end) {
-      const int len = s_len[ahead.b], unit = ahead.in_b / n_ahead, h = unit / a.parts;
-      const int key0 = (ahead.in_b - unit * n_ahead) * kStepKeys + warp * Ly::kKeys;
-#pragma unroll
-      for (int u = 0; u < Ly::kSub; ++u) {
-        const int left = len - key0 - 16 * u;  // rows of this tile that the sequence has
-        if (left <= 0) break;
-        const bool ok = pages[u] >= 0 && pages[u] < a.c.n_pages;
-        if (!ok && lane == 0) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)pages[u]);
-        const int64_t row0 =
-            ok ? ((int64_t)pages[u] * a.c.heads + h) * a.c.page_size + ((key0 >> 4) + u) % page16 * 16 : 0;
-        const int bytes = kE4M3 ? a.c.dim : 2 * a.c.dim;  // of a row
-        uint32_t dst = queue + slot * Ly::kStage + u * Ly::kTileBytes + lane * 16;
-#pragma unroll
-        for (int i = 0; i < Ly::kKPieces; ++i) {
-          const int r = g + 8 * (i & 1), at = 16 * (t + 4 * (i >> 1));
-          const bool on = ok && r < left && at < bytes;
-          cp16(dst, a.c.k + (on ? (row0 + r) * bytes + at : 0), on);
-          dst += 512;
+    if (s_ahead < s_stop) {
+      const int left = ahead.len - (ahead.step * kStepKeys + warp * Ly::kKeys);  // keys that are left from here
+      const bool has = lane < Ly::kOps && 16 * my_u < left;
+      const bool bad = has && (entry < 0 || entry >= a.c.n_pages);
+      if (bad) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)entry);
+      const uint32_t bytes = !has || bad ? 0u : (my_op >= 2 * Ly::kBoxes ? 16u : (uint32_t)Ly::kRegion);
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);  // also: every lane is done with the slot
+      uint64_t* bar = &s_full[warp][slot];
+      if (lane == 0) mbar_arrive_expect_tx(bar, sum);
+      if (bytes) {
+        const int row = ahead.h * a.c.page_size + tile * 16;  // of the page
+        if (my_op >= 2 * Ly::kBoxes) {
+          const uint8_t* src = (my_v ? a.c.v_exp : a.c.k_exp) + (int64_t)entry * a.c.heads * a.c.page_size + row;
+          bulk16(exps + slot * Ly::kExps + (2 * my_u + my_v) * 16, src, bar);
+        } else {
+          const int box = my_v ? my_op - Ly::kBoxes : my_op;
+          uint8_t* dst = smem + (warp * kStages + slot) * Ly::kStage + my_u * Ly::kTile + my_op * Ly::kRegion;
+          tma_load_3d(dst, my_v ? &vmap : &kmap, bar, box * (kE4M3 ? Ly::kBox : Ly::kBox / 2), row, entry);
         }
-        dst -= lane * (16 - Ly::kVPiece);
-#pragma unroll
-        for (int i = 0; i < Ly::kVPieces; ++i) {
-          const int r = 2 * t + (i & 1) + 8 * ((i >> 1) & 1), at = Ly::kVPiece * (g + 8 * (i >> 2));
-          const bool on = ok && r < left && at < bytes;
-          const uint8_t* src = a.c.v + (on ? (row0 + r) * bytes + at : 0);
-          if (Ly::kVPiece == 16) cp16(dst, src, on);
-          else cp8(dst, src, on);
-          dst += 32 * Ly::kVPiece;
-        }
-        if (kE4M3 && lane < 2)
-          cp16(queue + slot * Ly::kStage + Ly::kSub * Ly::kTileBytes + (2 * u + lane) * 16,
-               (lane ? a.c.v_exp : a.c.k_exp) + row0, ok);
       }
-      ++s_ahead;
-      if (s_ahead < s_end) {
-        ++ahead.in_b;
-        while (s_pre[ahead.b + 1] <= s_ahead) {  // s_ahead < total: ends at the last sequence with steps
-          ++ahead.b;
-          ahead.in_b = 0;
+      if (++s_ahead < s_end) {
+        if (++ahead.step < ahead.n) {
+          page += page_add;
+          tile += tile_add;
+          if (tile >= page16) {
+            tile -= page16;
+            ++page;
+          }
+        } else {
+          next_unit(ahead, s_ahead);
+          page = page_0;
+          tile = tile_0;
         }
-        n_ahead = steps_of(ahead.b);
+        look_up();
       }
     }
-    cp_commit();
-    look_up();
   };
   look_up();
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) copy_step(i);
+  // where this lane reads in a 16-row region: its piece of key row g (row g + 8: + 8 rows), of value row 2 t and 2 t + 1
+  uint32_t k_off, v_off[2];
+  if (Ly::kBox == 128) {
+    k_off = g * 128 + ((t ^ g) << 4);  // piece t; piece t + 4: ^ 64
+    v_off[0] = 2 * t * 128 + ((g ^ (2 * t)) << 4);
+    v_off[1] = (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4);
+  } else {
+    k_off = g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+    v_off[0] = 2 * t * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
+    v_off[1] = v_off[0] + 64;
+  }
 
   // ---- unit after unit
-  Place here = place_of(s_begin);
-  int s = s_begin, slot = 0;
+  int s = s_begin, slot = 0, phase = 0;
   while (s < s_end) {
-    const int b = here.b, len = s_len[b], nb = steps_of(b), unit = here.in_b / nb, step0 = here.in_b - unit * nb;
+    const int b = here.b, len = here.len, nb = here.n, step0 = here.step, kh = here.h;
     const int steps = min(nb - step0, s_end - s);  // of this unit, here
-    const int kh = unit / a.parts, head0 = kh * a.group + (unit % a.parts) * Ly::kHeads;
+    const int head0 = kh * a.group + here.part * Ly::kHeads;
     const int n_heads = min(Ly::kHeads, (kh + 1) * a.group - head0);
 
     // Q as the second operand: head g (of each tile of 8), the dim in the order of the K pieces
@@ -274,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const AttnArgs 
       constexpr int kWords = kE4M3 ? 8 : 4;  // words of Q for a piece of K
       uint32_t w[kDim / 8];
 #pragma unroll
-      for (int i = 0; i < Ly::kKPieces / 2; ++i) {
+      for (int i = 0; i < Ly::kRow / 64; ++i) {
         const int d = 2 * kWords * (t + 4 * i);
 #pragma unroll
         for (int j = 0; j < kWords; j += 4) {
@@ -319,54 +352,65 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const AttnArgs 
     }
 
     for (int i = 0; i < steps; ++i) {
-      if (kE4M3) __syncwarp();  // every lane has read the exponents that the next copy overwrites
       copy_step(slot == 0 ? kStages - 1 : slot - 1);
-      cp_wait<kStages - 1>();
-      if (kE4M3) __syncwarp();  // the exponents come from other lanes' copies
+      if (s + i < s_ahead && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase))) {
+        s_stop = s_ahead;  // nothing more is copied; what is on its way is still waited for
+        mv_set_error(a.err, kPagedAttnSite, MV_DEVERR_TIMEOUT);
+      }
       const int key0 = (step0 + i) * kStepKeys + warp * Ly::kKeys;
-      const uint32_t at = queue + slot * Ly::kStage;
-      slot = slot + 1 == kStages ? 0 : slot + 1;
+      const uint32_t at = queue + slot * Ly::kStage, ex_at = exps + slot * Ly::kExps;
+      if (++slot == kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
       if (key0 >= len) continue;
 
-      // S^T: rows keys g, g + 8 of each tile, columns heads 2 t, 2 t + 1
-      float x[kNT][Ly::kSub][4];
+      // S^T: rows keys g, g + 8 of each tile, columns heads 2 t, 2 t + 1. Tiles that nothing was copied to hold what an
+      // earlier step left: their scores are masked below, their products with V are left out. Two sums for one chain of
+      // products where there is only one.
+      constexpr int kSums = Ly::kSub * kNT == 1 ? 2 : 1;
+      float x[kNT][Ly::kSub][4], x2[4] = {};
 #pragma unroll
-      for (int u = 0; u < Ly::kSub; ++u) {
-        if (u > 0 && key0 + 16 * u >= len) {  // nothing was copied there
+      for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int n = 0; n < kNT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[n][u][e] = -INFINITY;
-          continue;
-        }
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
+        for (int u = 0; u < Ly::kSub; ++u)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[n][u][e] = 0.0f;
-        const uint32_t kt = at + u * Ly::kTileBytes + lane * 16;
 #pragma unroll
-        for (int i2 = 0; i2 < Ly::kKPieces / 2; ++i2) {
-          const uint4 lo = lds16(kt + i2 * 1024), hi = lds16(kt + i2 * 1024 + 512);  // keys g, g + 8
-          const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-          if (kE4M3) {
+      for (int i2 = 0; i2 < Ly::kRow / 64; ++i2) {
+        uint4 kw[Ly::kSub][2];  // keys g, g + 8
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t a0 = e4m3x2_to_half2((uint16_t)wl[j]), a2 = e4m3x2_to_half2((uint16_t)(wl[j] >> 16));
-              const uint32_t a1 = e4m3x2_to_half2((uint16_t)wh[j]), a3 = e4m3x2_to_half2((uint16_t)(wh[j] >> 16));
+        for (int u = 0; u < Ly::kSub; ++u)
 #pragma unroll
-              for (int n = 0; n < kNT; ++n)
-                mma<true>(x[n][u], a0, a1, a2, a3, qf[n][4 * i2 + j][0], qf[n][4 * i2 + j][1]);
+          for (int r = 0; r < 2; ++r)
+            kw[u][r] = lds16(at + u * Ly::kTile + (i2 >> 1) * Ly::kRegion + (k_off ^ (i2 & 1) * 64) + r * 8 * Ly::kBox);
+#pragma unroll
+        for (int j = 0; j < (kE4M3 ? 4 : 2); ++j)
+#pragma unroll
+          for (int u = 0; u < Ly::kSub; ++u) {
+            const uint32_t wl[4] = {kw[u][0].x, kw[u][0].y, kw[u][0].z, kw[u][0].w};
+            const uint32_t wh[4] = {kw[u][1].x, kw[u][1].y, kw[u][1].z, kw[u][1].w};
+            uint32_t f[4];
+            if (kE4M3) {
+              f[0] = e4m3x2_to_half2((uint16_t)wl[j]);
+              f[1] = e4m3x2_to_half2((uint16_t)wh[j]);
+              f[2] = e4m3x2_to_half2((uint16_t)(wl[j] >> 16));
+              f[3] = e4m3x2_to_half2((uint16_t)(wh[j] >> 16));
+            } else {
+              f[0] = wl[(2 * j) & 3];
+              f[1] = wh[(2 * j) & 3];
+              f[2] = wl[(2 * j + 1) & 3];
+              f[3] = wh[(2 * j + 1) & 3];
             }
-          } else {
+            const int qi = (kE4M3 ? 4 : 2) * i2 + j;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int n = 0; n < kNT; ++n)
-                mma<false>(x[n][u], wl[2 * j], wh[2 * j], wl[2 * j + 1], wh[2 * j + 1], qf[n][2 * i2 + j][0],
-                           qf[n][2 * i2 + j][1]);
+            for (int n = 0; n < kNT; ++n)
+              mma<kE4M3>(kSums == 2 && (qi & 1) ? x2 : x[n][u], f[0], f[1], f[2], f[3], qf[n][qi][0], qf[n][qi][1]);
           }
-        }
       }
+      if (kSums == 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[0][0][e] += x2[e];
       // scores into the exponent's base; the value rows' exponents
       float ev[Ly::kSub][2];
 #pragma unroll
@@ -377,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const AttnArgs 
           float ks = 1.0f;
           ev[u][r] = 0.0f;
           if (kE4M3) {
-            const uint32_t ex = at + Ly::kSub * Ly::kTileBytes + 32 * u + g + 8 * r;
+            const uint32_t ex = ex_at + 32 * u + g + 8 * r;
             ks = exp_byte_scale(lds_byte(ex));
             ev[u][r] = (float)((int)lds_byte(ex + 16) - 127);
           }
@@ -456,48 +500,62 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const AttnArgs 
       // O^T += V^T P^T
 #pragma unroll
       for (int u = 0; u < Ly::kSub; ++u) {
-        if (u > 0 && key0 + 16 * u >= len) continue;
-        const uint32_t vt = at + u * Ly::kTileBytes + 512 * Ly::kKPieces + lane * Ly::kVPiece;
-        constexpr int kPieces = Ly::kVPieces / 4, kWords = Ly::kVPiece / 4;
+        if (u > 0 && key0 + 16 * u >= len) break;
+        const uint32_t vt = at + u * Ly::kTile + Ly::kBoxes * Ly::kRegion;
+        const int left = len - key0 - 16 * u;
+        constexpr int kPieces = Ly::kBoxes, kWords = Ly::kVPiece / 4;
 #pragma unroll
         for (int i2 = 0; i2 < kPieces; ++i2) {
-          uint32_t w[4][kWords];  // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+          uint32_t w[4][4];  // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const uint32_t src = vt + (4 * i2 + r) * 32 * Ly::kVPiece;
+            const uint32_t src = vt + i2 * Ly::kRegion + v_off[r & 1] + (r >> 1) * 8 * Ly::kBox;
             if (kWords == 4) {
               const uint4 v = lds16(src);
               w[r][0] = v.x;
               w[r][1] = v.y;
-              w[r][kWords - 2] = v.z;
-              w[r][kWords - 1] = v.w;
+              w[r][2] = v.z;
+              w[r][3] = v.w;
             } else {
               const uint2 v = lds8(src);
               w[r][0] = v.x;
               w[r][1] = v.y;
             }
           }
+          if (left < 16) {  // rows behind the sequence hold anything: weight zero times a NaN would be one
 #pragma unroll
-          for (int j = 0; j < kWords; ++j) {
-            if (kE4M3) {
+            for (int r = 0; r < 4; ++r)
+              if (2 * t + (r & 1) + 4 * (r & 2) >= left)
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {  // two of the word's four dims
-                const uint32_t sel = half ? 0x7362u : 0x5140u;
-                const uint32_t lo = __byte_perm(w[0][j], w[1][j], sel), hi = __byte_perm(w[2][j], w[3][j], sel);
-                const uint32_t a0 = e4m3x2_to_half2((uint16_t)lo), a1 = e4m3x2_to_half2((uint16_t)(lo >> 16));
-                const uint32_t a2 = e4m3x2_to_half2((uint16_t)hi), a3 = e4m3x2_to_half2((uint16_t)(hi >> 16));
+                for (int j = 0; j < kWords; ++j) w[r][j] = 0u;
+          }
+          if (kE4M3) {
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
-                  mma<true>(o[n][2 * j + half], a0, a1, a2, a3, ph[n][u][0], ph[n][u][1]);
-              }
-            } else {
-              const uint32_t a0 = __byte_perm(w[0][j], w[1][j], 0x5410), a1 = __byte_perm(w[0][j], w[1][j], 0x7632);
-              const uint32_t a2 = __byte_perm(w[2][j], w[3][j], 0x5410), a3 = __byte_perm(w[2][j], w[3][j], 0x7632);
+            for (int m = 0; m < 2 * kWords; ++m) {  // two of a word's four dims
+              const uint32_t sel = m & 1 ? 0x7362u : 0x5140u;
+              const uint32_t lo = __byte_perm(w[0][m >> 1], w[1][m >> 1], sel), hi = __byte_perm(w[2][m >> 1], w[3][m >> 1], sel);
+              const uint32_t a0 = e4m3x2_to_half2((uint16_t)lo), a1 = e4m3x2_to_half2((uint16_t)(lo >> 16));
+              const uint32_t a2 = e4m3x2_to_half2((uint16_t)hi), a3 = e4m3x2_to_half2((uint16_t)(hi >> 16));
 #pragma unroll
-              for (int n = 0; n < kNT; ++n) {
-                mma<false>(o[n][4 * i2 + j], a0, a1, a2, a3, ph[n][u][0], ph[n][u][1]);
-                mma<false>(o[n][4 * i2 + j], a0, a1, a2, a3, pl[n][u][0], pl[n][u][1]);
-              }
+              for (int n = 0; n < kNT; ++n) mma<true>(o[n][m], a0, a1, a2, a3, ph[n][u][0], ph[n][u][1]);
+            }
+          } else {
+            uint32_t f[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              f[j][0] = __byte_perm(w[0][j], w[1][j], 0x5410);
+              f[j][1] = __byte_perm(w[0][j], w[1][j], 0x7632);
+              f[j][2] = __byte_perm(w[2][j], w[3][j], 0x5410);
+              f[j][3] = __byte_perm(w[2][j], w[3][j], 0x7632);
+            }
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma<false>(o[n][4 * i2 + j], f[j][0], f[j][1], f[j][2], f[j][3], ph[n][u][0], ph[n][u][1]);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma<false>(o[n][4 * i2 + j], f[j][0], f[j][1], f[j][2], f[j][3], pl[n][u][0], pl[n][u][1]);
             }
           }
         }
@@ -629,15 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const AttnArgs 
       }
     }
     s += steps;
-    if (s < s_end) {
-      here.in_b += steps;
-      while (s_pre[here.b + 1] <= s) {
-        ++here.b;
-        here.in_b = 0;
-      }
-    }
+    if (s < s_end) next_unit(here, s);
   }
-  cp_wait<0>();
 }
 
 template <int kDim, bool kE4M3, int kNT>
@@ -650,7 +701,18 @@ mv_status launch(const AttnArgs& a, cudaStream_t stream) {
                        (((int64_t)a.c.max_pages * a.c.page_size + kWarps * Ly::kKeys - 1) / (kWarps * Ly::kKeys));
   if (most > 0x7fffffff) return MV_ERR_SHAPE;
   const int grid = (int)std::min<int64_t>(most, std::min(mv_sm_count(), kMaxCtas));
-  const cudaError_t e = mv_launch(paged_attn_kernel<kDim, kE4M3, kNT>, dim3(grid), dim3(kThreads), bytes, stream, a);
+  // a pool as (dim, row of the page, page), boxes of 16 rows; dims behind the head's are filled with zeros
+  CUtensorMap maps[2];
+  const uint64_t row = (uint64_t)a.c.dim * (kE4M3 ? 1 : 2), rows = (uint64_t)a.c.heads * a.c.page_size;
+  const uint64_t dims[3] = {(uint64_t)a.c.dim, rows, (uint64_t)a.c.n_pages}, strides[2] = {row, row * rows};
+  const uint32_t box[3] = {(uint32_t)(kE4M3 ? Ly::kBox : Ly::kBox / 2), 16, 1};
+  for (int i = 0; i < 2; ++i)
+    if (!mv_encode_tmap(&maps[i], kE4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        i ? a.c.v : a.c.k, dims, strides, box,
+                        Ly::kBox == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+      return MV_ERR_CUDA;
+  const cudaError_t e =
+      mv_launch(paged_attn_kernel<kDim, kE4M3, kNT>, dim3(grid), dim3(kThreads), bytes, stream, maps[0], maps[1], a);
   return e == cudaSuccess ? mv_last_launch("paged_attention") : MV_ERR_CUDA;
 }
 
