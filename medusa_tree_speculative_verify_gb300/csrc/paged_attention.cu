@@ -21,8 +21,9 @@
 // fp16 have 11 bits. bf16: the weights are split in two bf16 (16 bits), one more product each.
 //
 // Split. The work is a line of steps, kWarps tiles of keys each, over all units (sequence, kv head, 8 or 16 of its
-// heads); every CTA takes an equal piece of the line, whatever the lengths are. A unit within one CTA is done there; one
-// that crosses pieces leaves partial results (reference, sum, output in fp32) in the workspace, and the CTA that adds
+// heads); every CTA takes an equal piece of the line, whatever the lengths are. A unit's start and end (its Q, putting the
+// warps' results together) cost about kUnitCost steps, which have their places on the line too, so that a piece of many
+// short sequences takes no longer than one of a long one. A unit within one CTA is done there; one that crosses pieces leaves partial results (reference, sum, output in fp32) in the workspace, and the CTA that adds
 // the last one joins all of them in the order of the line, so the result does not depend on who comes last.
 #include <algorithm>
 
@@ -33,13 +34,16 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStages = 3;       // steps of a warp's queue
-constexpr int kMaxCtas = 320;   // counters at the start of the workspace
+constexpr int kUnitCost = 1;     // what a unit costs beside its steps, in steps
+constexpr int kShortSteps = 16;  // steps of one warp up to which a sequence may go a unit to each warp
+constexpr int kMaxCtas = 160;    // counters at the start of the workspace; CTAs of a launch
 constexpr int kChunkSeq = 1024;  // sequences of one launch
 
 struct AttnArgs {
   PagedArgs c;
   RowsArgs q, out;
   int group, parts;  // query heads of a kv head, units of a kv head
+  int short_keys;    // sequences of at most so many keys go a unit to each warp
   float scale_log2;
   unsigned int* count;  // [kMaxCtas]
   float* part;          // [CTAs][2] partial results
@@ -63,7 +67,10 @@ struct Layout {
   static constexpr int kHeads = 8 * kNT;
   static constexpr int kSlot = kMT * 4 * 32;             // floats of one warp's O^T of 8 heads
   static constexpr int kPart = kHeads * (kDim + 4);      // floats of a partial result
-  static constexpr int kQueue = kWarps * kStages * kStage, kMerge = 4 * kSlot * 4;
+  static constexpr int kQueue = kWarps * kStages * kStage;
+  // the join of a unit's parts: their weights for 8 heads, a partial sum of 8 values for each thread
+  static constexpr int kJoin = (8 * kMaxCtas + 8 * kThreads) * 4;
+  static constexpr int kMerge = 4 * kSlot * 4 > kJoin ? 4 * kSlot * 4 : kJoin;
   static constexpr int kExpsAt = kQueue, kMergeAt = kExpsAt + kWarps * kStages * kExps, kPreAt = kMergeAt + kMerge;
   static_assert(kStage == 8192 && kOps <= 32 && kMergeAt % 16 == 0, "");
   static int bytes(int n_seq) { return 1024 + kPreAt + (2 * n_seq + 1) * 4; }
@@ -130,14 +137,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
   __shared__ float s_ml[kWarps][3][8];
   __shared__ int s_scan[kWarps];
-  __shared__ unsigned int s_last;
+  struct Split {
+    int b, head0, n_heads, u0, n;  // u0, n: first place and steps of the unit; n = 0: none
+  };
+  __shared__ Split s_split[2];  // the units of which this CTA holds a part
+  __shared__ bool s_last[2];
   float* s_merge = reinterpret_cast<float*>(smem + Ly::kMergeAt);
-  int* s_pre = reinterpret_cast<int*>(smem + Ly::kPreAt);  // [n_seq + 1] first step of each sequence
+  int* s_pre = reinterpret_cast<int*>(smem + Ly::kPreAt);  // [n_seq + 1] first place of each sequence
   int* s_len = s_pre + a.c.n_seq + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int n_seq = a.c.n_seq, units = a.c.heads * a.parts;  // units of a sequence
+  const int n_seq = a.c.n_seq, units = a.c.heads * a.parts, groups = (units + kWarps - 1) / kWarps;  // of a sequence
   constexpr int kStepKeys = kWarps * Ly::kKeys;
   pdl_trigger();
+  if (tid == 0) {
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
   if (lane == 0) {
 #pragma unroll
     for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
@@ -145,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
 
-  // ---- the line: every sequence's steps (one for an empty sequence: its zeros are written; none for a bad length)
+  // ---- the line: for every unit kUnitCost places that stand for its start and end, then its steps (one for an empty
+  // sequence: its zeros are written). A sequence of a bad length has none.
   int carry = 0;
   for (int base = 0; base < n_seq; base += kThreads) {
     const int b = base + tid;
@@ -154,7 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int len = __ldcg(a.c.seq_lens + b);
       const bool bad = len < 0 || len > a.c.max_pages * a.c.page_size;
       if (bad && blockIdx.x == 0) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)b);
-      steps = bad ? 0 : max(1, (len + kStepKeys - 1) / kStepKeys) * units;
+      const bool one = len <= a.short_keys;
+      steps = bad ? 0
+                  : (kUnitCost + max(1, one ? (len + Ly::kKeys - 1) / Ly::kKeys : (len + kStepKeys - 1) / kStepKeys)) *
+                        (one ? groups : units);
       s_len[b] = bad ? 0 : len;
     }
     int incl = steps;
@@ -176,46 +195,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   }
   if (tid == 0) s_pre[n_seq] = carry;
+  if (tid < 2) s_split[tid].n = 0;
   __syncthreads();
   const int total = carry, ctas = min((int)gridDim.x, total), cta = blockIdx.x;
   if (cta >= ctas) return;
   auto piece = [&](int c) { return (int)((int64_t)total * c / ctas); };
-  const int s_begin = piece(cta), s_end = piece(cta + 1);  // at least one step
-  auto steps_of = [&](int b) { return max(1, (s_len[b] + kStepKeys - 1) / kStepKeys); };
-
-  // A place on the line: step `step` of the `n` of a unit (sequence b, kv head h, part of its query heads).
+  const int s_first = piece(cta), s_end = piece(cta + 1);
+  // A place on the line: step `step` of the `n` of an entry, which is unit `idx` of sequence b for all warps (a step is
+  // kWarps tiles in turn) or, `one`, units kWarps * idx .. of a short sequence, one for each warp.
   struct Place {
-    int b, h, part, step, n, len;
+    int b, idx, step, n, len;
+    bool one;
+  };
+  auto enter = [&](Place& p, int b) {
+    p.b = b;
+    p.len = s_len[b];
+    p.one = p.len <= a.short_keys;
+    p.n = max(1, p.one ? (p.len + Ly::kKeys - 1) / Ly::kKeys : (p.len + kStepKeys - 1) / kStepKeys);
+  };
+  // to the next entry, whose first place is s < total
+  auto next_entry = [&](Place& p, int s) {
+    p.step = 0;
+    if (++p.idx < (p.one ? groups : units)) return;
+    p.idx = 0;
+    int b = p.b;
+    do ++b;
+    while (s_pre[b + 1] <= s);
+    enter(p, b);
   };
   Place ahead;
+  int s_begin;  // the first step at or after s_first that this CTA does
   {
-    int lo = 0, hi = n_seq;  // the last b with pre[b] <= s_begin: one with steps
+    int lo = 0, hi = n_seq;  // the last b with pre[b] <= s_first: one with places
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (s_pre[mid] <= s_begin) lo = mid;
+      if (s_pre[mid] <= s_first) lo = mid;
       else hi = mid;
     }
-    ahead.b = lo;
-    ahead.n = steps_of(lo);
-    ahead.len = s_len[lo];
-    const int in_b = s_begin - s_pre[lo], unit = in_b / ahead.n;
-    ahead.step = in_b - unit * ahead.n;
-    ahead.h = unit / a.parts;
-    ahead.part = unit - ahead.h * a.parts;
+    enter(ahead, lo);
+    const int in_b = s_first - s_pre[lo], width = kUnitCost + ahead.n;
+    ahead.idx = in_b / width;
+    const int at = in_b - ahead.idx * width;
+    ahead.step = max(0, at - kUnitCost);
+    s_begin = s_first - at + kUnitCost + ahead.step;
+    if (ahead.one && ahead.step > 0) {  // belongs to the CTA that holds its first step, as a whole
+      s_begin = s_first - at + width + kUnitCost;
+      if (s_begin < s_end) next_entry(ahead, s_begin - kUnitCost);
+    }
   }
+  if (s_begin >= s_end) return;
   Place here = ahead;
-  // to the next unit, whose first step is s < total
-  auto next_unit = [&](Place& p, int s) {
-    p.step = 0;
-    if (++p.part < a.parts) return;
-    p.part = 0;
-    if (++p.h < a.c.heads) return;
-    p.h = 0;
-    do ++p.b;
-    while (s_pre[p.b + 1] <= s);
-    p.n = steps_of(p.b);
-    p.len = s_len[p.b];
-  };
 
   // ---- this warp's queue. Each of the first kOps lanes does one of a step's copies: its 16-key tile u, K or V, a box of
   // the row or the exponents. Page and tile in it are carried along: a step is kWarps * kSub tiles after the one before.
@@ -225,20 +254,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int my_u = lane % Ly::kSub, my_op = lane / Ly::kSub;  // op: K boxes, V boxes, K and V exponents
   const bool my_v = my_op >= 2 * Ly::kBoxes ? my_op & 1 : my_op >= Ly::kBoxes;
   const int page_add = kWarps * Ly::kSub / page16, tile_add = kWarps * Ly::kSub % page16;
-  const int page_0 = (warp * Ly::kSub + my_u) / page16, tile_0 = (warp * Ly::kSub + my_u) % page16;
-  int s_ahead = s_begin, s_stop = s_end, page, tile, entry = 0;  // entry: the table's, of the step that is copied next
-  {
-    const int first = (ahead.step * kWarps + warp) * Ly::kSub + my_u;
-    page = first / page16;
-    tile = first - page * page16;
-  }
-  auto look_up = [&]() {
-    if (ahead.step * kStepKeys + warp * Ly::kKeys + 16 * my_u < ahead.len)
-      entry = __ldcg(a.c.table + (int64_t)ahead.b * a.c.ld_table + page);
+  const int page_one = Ly::kSub / page16, tile_one = Ly::kSub % page16;
+  int s_ahead = s_begin, page, tile, entry = 0;  // entry: the table's, of the step that is copied next
+  int key_ahead, h_ahead;                        // its first key here (past the end: nothing to do) and kv head
+  bool more = true;
+  auto enter_copy = [&]() {
+    const int first = (ahead.one ? ahead.step : ahead.step * kWarps + warp) * Ly::kSub;
+    const int unit = ahead.one ? ahead.idx * kWarps + warp : ahead.idx;
+    key_ahead = unit < units ? 16 * first : ahead.len;
+    h_ahead = unit / a.parts;
+    page = (first + my_u) / page16;
+    tile = first + my_u - page * page16;
   };
+  auto look_up = [&]() {
+    if (key_ahead + 16 * my_u < ahead.len) entry = __ldcg(a.c.table + (int64_t)ahead.b * a.c.ld_table + page);
+  };
+  enter_copy();
   auto copy_step = [&](int slot) {
-    if (s_ahead < s_stop) {
-      const int left = ahead.len - (ahead.step * kStepKeys + warp * Ly::kKeys);  // keys that are left from here
+    if (more) {
+      const int left = ahead.len - key_ahead;  // keys that are left from here
       const bool has = lane < Ly::kOps && 16 * my_u < left;
       const bool bad = has && (entry < 0 || entry >= a.c.n_pages);
       if (bad) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)entry);
@@ -247,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t* bar = &s_full[warp][slot];
       if (lane == 0) mbar_arrive_expect_tx(bar, sum);
       if (bytes) {
-        const int row = ahead.h * a.c.page_size + tile * 16;  // of the page
+        const int row = h_ahead * a.c.page_size + tile * 16;  // of the page
         if (my_op >= 2 * Ly::kBoxes) {
           const uint8_t* src = (my_v ? a.c.v_exp : a.c.k_exp) + (int64_t)entry * a.c.heads * a.c.page_size + row;
           bulk16(exps + slot * Ly::kExps + (2 * my_u + my_v) * 16, src, bar);
@@ -257,21 +291,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(dst, my_v ? &vmap : &kmap, bar, box * (kE4M3 ? Ly::kBox : Ly::kBox / 2), row, entry);
         }
       }
-      if (++s_ahead < s_end) {
-        if (++ahead.step < ahead.n) {
-          page += page_add;
-          tile += tile_add;
-          if (tile >= page16) {
-            tile -= page16;
-            ++page;
-          }
-        } else {
-          next_unit(ahead, s_ahead);
-          page = page_0;
-          tile = tile_0;
+      ++s_ahead;
+      if (++ahead.step < ahead.n) {
+        more = ahead.one || s_ahead < s_end;
+        key_ahead = key_ahead < ahead.len ? key_ahead + (ahead.one ? Ly::kKeys : kStepKeys) : ahead.len;
+        page += ahead.one ? page_one : page_add;
+        tile += ahead.one ? tile_one : tile_add;
+        if (tile >= page16) {
+          tile -= page16;
+          ++page;
         }
-        look_up();
+      } else {
+        s_ahead += kUnitCost;
+        more = s_ahead < s_end;
+        if (more) {
+          next_entry(ahead, s_ahead - kUnitCost);
+          enter_copy();
+        }
       }
+      if (more) look_up();
     }
   };
   look_up();
@@ -289,23 +327,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     v_off[1] = v_off[0] + 64;
   }
 
-  // ---- unit after unit
-  int s = s_begin, slot = 0, phase = 0;
-  while (s < s_end) {
-    const int b = here.b, len = here.len, nb = here.n, step0 = here.step, kh = here.h;
-    const int steps = min(nb - step0, s_end - s);  // of this unit, here
-    const int head0 = kh * a.group + here.part * Ly::kHeads;
-    const int n_heads = min(Ly::kHeads, (kh + 1) * a.group - head0);
-
-    // Q as the second operand: head g (of each tile of 8), the dim in the order of the K pieces
-    uint32_t qf[kNT][kDim / 16][2];
-    float mult[kNT][2];  // score of head 2 t (+ 1) into the exponent
+  // the words of Q of a unit: head g of each tile of 8, the pieces as of K
+  uint32_t q_raw[kNT][kDim / 8];
+  auto load_q = [&](const Place& p) {
+    constexpr int kWords = kE4M3 ? 8 : 4;  // words of Q for a piece of K
+    const int unit = p.one ? p.idx * kWarps + warp : p.idx, kh = unit / a.parts;
+    const int head0 = kh * a.group + (unit - kh * a.parts) * Ly::kHeads;
+    const int n_heads = unit < units ? min(Ly::kHeads, (kh + 1) * a.group - head0) : 0;
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       const int h = 8 * n + g;
-      const uint16_t* row = a.q.p + (int64_t)b * a.q.ts + (int64_t)(head0 + (h < n_heads ? h : 0)) * a.q.hs;
-      constexpr int kWords = kE4M3 ? 8 : 4;  // words of Q for a piece of K
-      uint32_t w[kDim / 8];
+      const uint16_t* row = a.q.p + (int64_t)p.b * a.q.ts + (int64_t)(h < n_heads ? head0 + h : 0) * a.q.hs;
 #pragma unroll
       for (int i = 0; i < Ly::kRow / 64; ++i) {
         const int d = 2 * kWords * (t + 4 * i);
@@ -313,12 +345,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < kWords; j += 4) {
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (h < n_heads && d + 2 * j < a.c.dim) v = *reinterpret_cast<const uint4*>(row + d + 2 * j);
-          w[i * kWords + j] = v.x;
-          w[i * kWords + j + 1] = v.y;
-          w[i * kWords + j + 2] = v.z;
-          w[i * kWords + j + 3] = v.w;
+          q_raw[n][i * kWords + j] = v.x;
+          q_raw[n][i * kWords + j + 1] = v.y;
+          q_raw[n][i * kWords + j + 2] = v.z;
+          q_raw[n][i * kWords + j + 3] = v.w;
         }
       }
+    }
+  };
+
+  // ---- unit after unit
+  int s = s_begin, slot = 0, phase = 0;
+  load_q(here);
+  while (s < s_end) {
+    const int b = here.b, len = here.len, nb = here.n, step0 = here.step;
+    const bool one = here.one;
+    const int steps = one ? nb : min(nb - step0, s_end - s);  // of this entry, here
+    const int unit = one ? here.idx * kWarps + warp : here.idx, kh = unit / a.parts;
+    const int head0 = kh * a.group + (unit - kh * a.parts) * Ly::kHeads;
+    const int n_heads = unit < units ? min(Ly::kHeads, (kh + 1) * a.group - head0) : 0;
+    // this warp's first key, and from step to step
+    int key0 = one ? 0 : step0 * kStepKeys + warp * Ly::kKeys;
+    const int key_add = one ? Ly::kKeys : kStepKeys, key_end = n_heads > 0 ? len : 0;
+
+    // Q as the second operand: head g (of each tile of 8), the dim in the order of the K pieces
+    uint32_t qf[kNT][kDim / 16][2];
+    float mult[kNT][2];  // score of head 2 t (+ 1) into the exponent
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      const uint32_t(&w)[kDim / 8] = q_raw[n];
       if (kE4M3) {
         float top = 0.0f;
 #pragma unroll
@@ -351,19 +406,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
-    for (int i = 0; i < steps; ++i) {
+    for (int i = 0; i < steps; ++i, key0 += key_add) {
       copy_step(slot == 0 ? kStages - 1 : slot - 1);
       if (s + i < s_ahead && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase))) {
-        s_stop = s_ahead;  // nothing more is copied; what is on its way is still waited for
+        more = false;  // nothing more is copied; what is on its way is still waited for
         mv_set_error(a.err, kPagedAttnSite, MV_DEVERR_TIMEOUT);
       }
-      const int key0 = (step0 + i) * kStepKeys + warp * Ly::kKeys;
       const uint32_t at = queue + slot * Ly::kStage, ex_at = exps + slot * Ly::kExps;
       if (++slot == kStages) {
         slot = 0;
         phase ^= 1;
       }
-      if (key0 >= len) continue;
+      if (key0 >= key_end) continue;
 
       // S^T: rows keys g, g + 8 of each tile, columns heads 2 t, 2 t + 1. Tiles that nothing was copied to hold what an
       // earlier step left: their scores are masked below, their products with V are left out. Two sums for one chain of
@@ -562,10 +616,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
-    // ---- the warps' results together, 8 heads at a time
+    // ---- the entry's results: the warps' together, 8 heads at a time
     const bool whole = steps == nb;
-    const int u0 = s - step0, u1 = u0 + nb;                     // the unit on the line
-    const int part = u0 <= s_begin ? 0 : 1;                     // this CTA's partial result of it
+    const int u0 = s - step0 - kUnitCost;                       // the unit's first place
+    const int part = u0 <= s_first ? 0 : 1;                     // this CTA's partial result of it
+    if (!whole && tid == 0) s_split[part] = {b, head0, n_heads, u0, nb};
+    s += steps + kUnitCost;
+    if (s < s_end) {  // the next entry's Q is on its way while this one's results are put together
+      next_entry(here, s - kUnitCost);
+      load_q(here);
+    }
+    if (one) {  // a unit of one warp: done here
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int w = 4; w <= 16; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
+          const int h = 8 * n + 2 * t + e;
+          const float f = len > 0 ? (kE4M3 ? exp2f(my[n][e] - mx[n][e]) : 1.0f) / l[n][e] : 0.0f;
+#pragma unroll
+          for (int i2 = 0; i2 < kDim / 64; ++i2) {
+            const int d = kE4M3 ? kDim / 8 * g + 8 * i2 : 8 * (g + 8 * i2);
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(o[n][4 * i2 + k][e] * f, o[n][4 * i2 + k][2 + e] * f);
+            if (h < n_heads && d < a.c.dim)
+              *reinterpret_cast<uint4*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)(head0 + h) * a.out.hs + d) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      continue;
+    }
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
 #pragma unroll
@@ -640,67 +722,119 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncthreads();
     }
+  }
 
-    // ---- a unit over several CTAs: the last one to come joins the partial results in the order of the line
-    if (!whole) {
-      auto cta_of = [&](int step) {  // the CTA whose piece holds a step
-        int c = (int)((int64_t)step * ctas / total);
-        while (piece(c + 1) <= step) ++c;
-        while (piece(c) > step) --c;
-        return c;
-      };
-      const int c0 = cta_of(u0), c1 = cta_of(u1 - 1);
+  // ---- units over several CTAs: the last one to come joins the partial results in the order of the line
+  __syncthreads();
+  auto cta_of = [&](int place) {  // the CTA whose piece holds a place
+    int c = (int)((int64_t)place * ctas / total);
+    while (piece(c + 1) <= place) ++c;
+    while (piece(c) > place) --c;
+    return c;
+  };
+  if (tid < 2) {
+    bool last = false;
+    const Split& sp = s_split[tid];
+    if (sp.n) {
+      const int c0 = cta_of(sp.u0 + kUnitCost), c1 = cta_of(sp.u0 + kUnitCost + sp.n - 1);
       __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const unsigned int seen = atomicAdd(a.count + c0, 1u);
-        s_last = seen == (unsigned int)(c1 - c0);
-        if (s_last) atomicExch(a.count + c0, 0u);
-        __threadfence();
-      }
-      __syncthreads();
-      if (s_last) {
-        for (int e = tid; e < Ly::kHeads * kDim / 8; e += kThreads) {
-          const int h = e / (kDim / 8), d = e % (kDim / 8) * 8;
-          if (h >= n_heads || d >= a.c.dim) continue;
-          const float* first = a.part + (int64_t)(2 * c0 + (u0 == piece(c0) ? 0 : 1)) * Ly::kPart;
-          float tx = -INFINITY, ty = -INFINITY, sum = 0.0f, v[8] = {};
-          for (int c = c0; c <= c1; ++c) {
-            const float* src = c == c0 ? first : a.part + (int64_t)(2 * c) * Ly::kPart;
-            const float4 ml = __ldcg(reinterpret_cast<const float4*>(src + Ly::kHeads * kDim + 4 * h));
-            const float4 lo = __ldcg(reinterpret_cast<const float4*>(src + h * kDim + d));
-            const float4 hi = __ldcg(reinterpret_cast<const float4*>(src + h * kDim + d + 4));
-            const float nx = fmaxf(tx, ml.x), ny = fmaxf(ty, ml.y);
-            sum = sum * weight(tx, nx) + ml.z * weight(ml.x, nx);
-            const float f0 = weight(ty, ny), f1 = weight(ml.y, ny);
-            const float w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      last = atomicAdd(a.count + c0, 1u) == (unsigned int)(c1 - c0);
+      if (last) atomicExch(a.count + c0, 0u);
+      __threadfence();
+    }
+    s_last[tid] = last;
+  }
+  __syncthreads();
+  for (int which = 0; which < 2; ++which) {
+    if (!s_last[which]) continue;
+    const int b = s_split[which].b, head0 = s_split[which].head0, n_heads = s_split[which].n_heads;
+    const int u0 = s_split[which].u0, c0 = cta_of(u0 + kUnitCost), c1 = cta_of(u0 + kUnitCost + s_split[which].n - 1);
+    float *s_w = s_merge, *s_sum = s_merge + 8 * kMaxCtas;
+    auto part_of = [&](int c) { return a.part + (int64_t)(2 * c + (c == c0 && u0 > piece(c0) ? 1 : 0)) * Ly::kPart; };
+    for (int n = 0; n < kNT && 8 * n < n_heads; ++n) {
+      // a warp for each head: the references' maxima, the parts' weights, the sum
+      const int h = 8 * n + warp;
+      const float4 none = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+      float4 ml[kMaxCtas / 32];
+      float tx = -INFINITY, ty = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = v[k] * f0 + w[k] * f1;
-            tx = nx;
-            ty = ny;
-          }
-          const float f = (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum;
-          *reinterpret_cast<uint4*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)(head0 + h) * a.out.hs + d) =
-              make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
-                         pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
+      for (int i = 0; i < kMaxCtas / 32; ++i) {
+        const int c = c0 + 32 * i + lane;
+        ml[i] = c <= c1 && h < n_heads ? __ldcg(reinterpret_cast<const float4*>(part_of(c) + Ly::kHeads * kDim + 4 * h)) : none;
+      }
+#pragma unroll
+      for (int i = 0; i < kMaxCtas / 32; ++i) {
+        tx = fmaxf(tx, ml[i].x);
+        ty = fmaxf(ty, ml[i].y);
+      }
+#pragma unroll
+      for (int w = 16; w >= 1; w >>= 1) {
+        tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, w));
+        ty = fmaxf(ty, __shfl_xor_sync(0xffffffffu, ty, w));
+      }
+#pragma unroll
+      for (int i = 0; i < kMaxCtas / 32; ++i) {
+        s_w[warp * kMaxCtas + 32 * i + lane] = weight(ml[i].y, ty);
+        sum += ml[i].z * weight(ml[i].x, tx);
+      }
+#pragma unroll
+      for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      if (lane == 0) s_ml[0][0][warp] = (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum;
+      __syncthreads();
+      // thread: one head, 8 dims, every kSets-th part; then the sets
+      constexpr int kSets = kThreads / kDim;
+      const int e = tid % kDim, hh = e / (kDim / 8), d = e % (kDim / 8) * 8;
+      float v[8] = {};
+      if (8 * n + hh < n_heads) {
+#pragma unroll 4
+        for (int c = c0 + tid / kDim; c <= c1; c += kSets) {
+          const float* src = part_of(c) + (8 * n + hh) * kDim + d;
+          const float4 lo = __ldcg(reinterpret_cast<const float4*>(src));
+          const float4 hi = __ldcg(reinterpret_cast<const float4*>(src + 4));
+          const float f = s_w[hh * kMaxCtas + c - c0];
+          v[0] += lo.x * f;
+          v[1] += lo.y * f;
+          v[2] += lo.z * f;
+          v[3] += lo.w * f;
+          v[4] += hi.x * f;
+          v[5] += hi.y * f;
+          v[6] += hi.z * f;
+          v[7] += hi.w * f;
         }
       }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s_sum[k * kThreads + tid] = v[k];
+      __syncthreads();
+      if (tid < kDim && 8 * n + hh < n_heads && d < a.c.dim) {
+        const float f = s_ml[0][0][hh];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float x = s_sum[k * kThreads + tid];
+#pragma unroll
+          for (int i = 1; i < kSets; ++i) x += s_sum[k * kThreads + i * kDim + tid];
+          v[k] = x * f;
+        }
+        *reinterpret_cast<uint4*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)(head0 + 8 * n + hh) * a.out.hs + d) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]));
+      }
+      __syncthreads();
     }
-    s += steps;
-    if (s < s_end) next_unit(here, s);
   }
 }
 
 template <int kDim, bool kE4M3, int kNT>
-mv_status launch(const AttnArgs& a, cudaStream_t stream) {
+mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   using Ly = Layout<kDim, kE4M3, kNT>;
   static int flags[64] = {};
-  const int bytes = Ly::bytes(a.c.n_seq);
+  const int bytes = Ly::bytes(args.c.n_seq);
   if (!mv_set_smem_once((const void*)paged_attn_kernel<kDim, kE4M3, kNT>, Ly::bytes(kChunkSeq), flags)) return MV_ERR_CUDA;
-  const int64_t most = (int64_t)a.c.n_seq * a.c.heads * a.parts *
-                       (((int64_t)a.c.max_pages * a.c.page_size + kWarps * Ly::kKeys - 1) / (kWarps * Ly::kKeys));
+  const int64_t most = (int64_t)args.c.n_seq * args.c.heads * args.parts *
+                       (((int64_t)args.c.max_pages * args.c.page_size + kWarps * Ly::kKeys - 1) / (kWarps * Ly::kKeys) + kUnitCost + kShortSteps);
   if (most > 0x7fffffff) return MV_ERR_SHAPE;
   const int grid = (int)std::min<int64_t>(most, std::min(mv_sm_count(), kMaxCtas));
+  AttnArgs a = args;
+  a.short_keys = std::min(kShortSteps, 2 * (a.c.n_seq * a.c.heads * a.parts / grid)) * Ly::kKeys;
   // a pool as (dim, row of the page, page), boxes of 16 rows; dims behind the head's are filled with zeros
   CUtensorMap maps[2];
   const uint64_t row = (uint64_t)a.c.dim * (kE4M3 ? 1 : 2), rows = (uint64_t)a.c.heads * a.c.page_size;
