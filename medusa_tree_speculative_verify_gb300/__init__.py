@@ -390,51 +390,62 @@ def pack_model_weights(w, drop_source=False):
 
 # --------------------------------------------------------------------------------------------- serving operators
 
-def _rows(t, what, heads=None, dim=None, tokens=None):
-    """A bf16 CUDA tensor [tokens, heads, head_dim] as mv_rows; its last dimension must be contiguous."""
-    import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda:
-        raise ValueError(f"{what}: a bf16 CUDA tensor [tokens, heads, head_dim] is wanted, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    n, h, d = t.shape
-    if (heads is not None and h != heads) or (dim is not None and d != dim) or (tokens is not None and n != tokens):
-        raise ValueError(f"{what}: [{'tokens' if tokens is None else tokens}, {'heads' if heads is None else heads}, "
-                         f"{'head_dim' if dim is None else dim}] is wanted, got {tuple(t.shape)}")
-    ts, hs, ds = t.stride()
-    if ds != 1 and d != 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous, got strides {t.stride()}")
-    return _Rows(t.data_ptr(), ts if n > 1 else 0, hs if h > 1 else 0)
+_torch = None       # the module, imported by the first call that takes tensors
+_raw_stream = None  # a device's current stream as an integer
 
 
-def _ints(t, what, dim, device):
+def _load_torch():
+    global _torch, _raw_stream
     import torch
-    if t.dtype != torch.int32 or t.dim() != dim or t.device != device:
-        raise ValueError(f"{what}: an int32 tensor of {dim} dimension(s) on {device} is wanted, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    if t.numel() > 1 and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{what}: the last dimension must be contiguous, got strides {t.stride()}")
+    _torch = torch
+    # torch.cuda.current_stream costs a microsecond, most of a small call's checks
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return torch
+
+
+def _rows(t, what, device, heads, dim, tokens):
+    """A bf16 tensor [tokens, heads, dim] on ``device`` (an index) as mv_rows; its last dimension must be contiguous."""
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not _torch.bfloat16 or shape != (tokens, heads, dim) or t.get_device() != device or \
+            device < 0 or (strides[2] != 1 and dim != 1):
+        raise ValueError(f"{what}: a bf16 tensor [{tokens}, {heads}, {dim}] on CUDA device {device} with a contiguous last "
+                         f"dimension is wanted, got {t.dtype} {tuple(shape)} on {t.device} with strides {strides}")
+    return _Rows(t.data_ptr(), strides[0] if tokens > 1 else 0, strides[1] if heads > 1 else 0)
+
+
+def _heads(t, what):
+    """The tokens and heads of a tensor [tokens, heads, dim]."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what}: [tokens, heads, head_dim] is wanted, got {tuple(shape)}")
+    return shape[0], shape[1]
+
+
+def _ints(t, what, device, shape):
+    """The address of a contiguous int32 tensor of ``shape`` on ``device``; a 2-D one may have longer rows."""
+    if t.dtype is not _torch.int32 or t.shape != shape or t.get_device() != device or \
+            not (t.is_contiguous() or (len(shape) == 2 and t.stride(1) == 1)):
+        raise ValueError(f"{what}: a contiguous int32 tensor {tuple(shape)} on CUDA device {device} is wanted, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device} with strides {t.stride()}")
     return t.data_ptr()
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-
-
 def _call_on(device, stream, fn, *args):
-    """fn(*args, stream) with ``device`` current, on ``stream`` or on the device's current stream."""
-    import torch
+    """fn(*args, stream) with CUDA device ``device`` current, on ``stream`` or on that device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors are on {device}")
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, stream.cuda_stream)
+        raw = _raw_stream(device)
+    elif stream.device.index == device:
+        raw = stream.cuda_stream
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, stream.cuda_stream)
-    _check(status, fn.__name__)
+        raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors are on CUDA device {device}")
+    if _torch.cuda.current_device() == device:
+        status = fn(*args, raw)
+    else:
+        with _torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status:
+        raise MVError(status, fn.__name__)
 
 
 class PromptPlan:
@@ -477,14 +488,13 @@ class PromptPlan:
 def prompt_attention(q, k, v, plan: PromptPlan, scale, out, stream=None):
     """Causal attention of packed prompts: q, out bf16 [tokens, heads, D]; k, v bf16 [tokens, kv heads, D] (any strides
     that are multiples of 8, last dimension contiguous); tokens = plan.n_tokens at least, later rows are not touched."""
-    n, d = plan.n_tokens, q.shape[-1]
-    if q.dim() != 3 or k.dim() != 3 or q.shape[0] < n:
-        raise ValueError(f"prompt_attention: q and k are [tokens, heads, head_dim] of {n} tokens at least, got "
-                         f"{tuple(q.shape)} and {tuple(k.shape)}")
-    hq, hk, t = q.shape[1], k.shape[1], q.shape[0]
-    _same_device(q.device, k=k, v=v, out=out)
-    _call_on(q.device, stream, lib().prompt_attention, _rows(q, "q"), _rows(k, "k", hk, d, t), _rows(v, "v", hk, d, t),
-             hq, hk, d, plan.handle, float(scale), _rows(out, "out", hq, d, t))
+    if _torch is None:
+        _load_torch()
+    (t, hq), (_, hk), n, d, dev = _heads(q, "q"), _heads(k, "k"), plan.n_tokens, q.shape[2], q.get_device()
+    if t < n:
+        raise ValueError(f"prompt_attention: the plan has {n} tokens, q {t}")
+    _call_on(dev, stream, lib().prompt_attention, _rows(q, "q", dev, hq, d, t), _rows(k, "k", dev, hk, d, t),
+             _rows(v, "v", dev, hk, d, t), hq, hk, d, plan.handle, scale, _rows(out, "out", dev, hq, d, t))
 
 
 class PagedKV:
@@ -492,7 +502,7 @@ class PagedKV:
     torch.float8_e4m3fn; for the latter k_exp, v_exp uint8 [n_pages, kv heads, page_size] (see mv_paged_kv)."""
 
     def __init__(self, k, v, k_exp=None, v_exp=None):
-        import torch
+        torch = _load_torch()
         if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype:
             raise ValueError(f"PagedKV: k and v are both bf16 or both float8_e4m3fn, got {k.dtype} and {v.dtype}")
         if k.dim() != 4 or v.shape != k.shape or not k.is_cuda:
@@ -504,14 +514,17 @@ class PagedKV:
                 raise ValueError(f"PagedKV: {name} belongs to e4m3 pages and to no others")
             if e is not None and (e.dtype != torch.uint8 or e.shape != k.shape[:3]):
                 raise ValueError(f"PagedKV: {name} is uint8 {tuple(k.shape[:3])}, got {e.dtype} {tuple(e.shape)}")
-        _same_device(k.device, v=v, k_exp=k_exp, v_exp=v_exp)
-        if any(t is not None and not t.is_contiguous() for t in (k, v, k_exp, v_exp)):
+        tensors = [t for t in (k, v, k_exp, v_exp) if t is not None]
+        if any(t.device != k.device for t in tensors):
+            raise ValueError(f"PagedKV: tensors on different devices: {[str(t.device) for t in tensors]}")
+        if any(not t.is_contiguous() for t in tensors):
             raise ValueError("PagedKV: the pages must be contiguous")
-        self.k, self.v, self.k_exp, self.v_exp, self.device = k, v, k_exp, v_exp, k.device
+        self.k, self.v, self.k_exp, self.v_exp, self.device = k, v, k_exp, v_exp, k.get_device()
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
         self._desc = _PagedKVDesc(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
                                   v_exp.data_ptr() if e4m3 else None, DTYPE_E4M3 if e4m3 else DTYPE_BF16,
                                   self.n_pages, self.page_size, self.n_kv_heads, self.head_dim)
+        self._ref = ctypes.byref(self._desc)
 
     @classmethod
     def zeros(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=DTYPE_BF16, device="cuda"):
@@ -529,40 +542,29 @@ class PagedKV:
 
     def _seqs(self, block_table, seq_lens):
         """block_table int32 [n_seq, pages] and seq_lens int32 [n_seq] as the arguments of the C entry points."""
-        table, lens = _ints(block_table, "block_table", 2, self.device), _ints(seq_lens, "seq_lens", 1, self.device)
-        n, pages = block_table.shape
-        if seq_lens.shape[0] != n:
-            raise ValueError(f"block_table has {n} rows, seq_lens {seq_lens.shape[0]}")
-        return table, block_table.stride(0) if n > 1 else pages, pages, lens, n
-
-
-def _cu(cu_rows, n_seq, device):
-    p = _ints(cu_rows, "cu_rows", 1, device)
-    if cu_rows.shape[0] != n_seq + 1:
-        raise ValueError(f"cu_rows has {cu_rows.shape[0]} entries, {n_seq + 1} are wanted")
-    return p
+        shape, dev = block_table.shape, self.device
+        if len(shape) != 2:
+            raise ValueError(f"block_table: [n_seq, pages] is wanted, got {tuple(shape)}")
+        n, pages = shape
+        return (_ints(block_table, "block_table", dev, shape), block_table.stride(0) if n > 1 else pages, pages,
+                _ints(seq_lens, "seq_lens", dev, (n,)), n)
 
 
 def paged_kv_append(k, v, cu_rows, cache: PagedKV, block_table, seq_lens, stream=None):
     """Writes rows cu_rows[b] .. of k, v bf16 [rows, kv heads, D] as the last ones of sequence b (the last at position
     seq_lens[b] - 1); cu_rows int32 [n_seq + 1], block_table int32 [n_seq, pages], seq_lens int32 [n_seq]."""
-    table, ld, pages, lens, n = cache._seqs(block_table, seq_lens)
-    cu = _cu(cu_rows, n, cache.device)
-    _same_device(cache.device, k=k, v=v)
-    rk = _rows(k, "k", cache.n_kv_heads, cache.head_dim)
-    _call_on(cache.device, stream, lib().paged_kv_append, rk,
-             _rows(v, "v", cache.n_kv_heads, cache.head_dim, k.shape[0]), k.shape[0], cu, cache._desc, table, ld,
-             pages, lens, n)
+    dev, h, d, seqs = cache.device, cache.n_kv_heads, cache.head_dim, cache._seqs(block_table, seq_lens)
+    rows, _ = _heads(k, "k")
+    _call_on(dev, stream, lib().paged_kv_append, _rows(k, "k", dev, h, d, rows), _rows(v, "v", dev, h, d, rows), rows,
+             _ints(cu_rows, "cu_rows", dev, (seqs[4] + 1,)), cache._ref, *seqs)
 
 
 def paged_kv_read(cache: PagedKV, block_table, seq_lens, cu_rows, k_out, v_out, stream=None):
     """The last rows of every sequence as bf16 [rows, kv heads, D]: the mirror of paged_kv_append."""
-    table, ld, pages, lens, n = cache._seqs(block_table, seq_lens)
-    cu = _cu(cu_rows, n, cache.device)
-    _same_device(cache.device, k_out=k_out, v_out=v_out)
-    rk = _rows(k_out, "k_out", cache.n_kv_heads, cache.head_dim)
-    _call_on(cache.device, stream, lib().paged_kv_read, cache._desc, table, ld, pages, lens, n, cu, k_out.shape[0], rk,
-             _rows(v_out, "v_out", cache.n_kv_heads, cache.head_dim, k_out.shape[0]))
+    dev, h, d, seqs = cache.device, cache.n_kv_heads, cache.head_dim, cache._seqs(block_table, seq_lens)
+    rows, _ = _heads(k_out, "k_out")
+    _call_on(dev, stream, lib().paged_kv_read, cache._ref, *seqs, _ints(cu_rows, "cu_rows", dev, (seqs[4] + 1,)), rows,
+             _rows(k_out, "k_out", dev, h, d, rows), _rows(v_out, "v_out", dev, h, d, rows))
 
 
 def paged_attention_workspace(n_seq, n_heads, n_kv_heads, head_dim):
@@ -571,15 +573,12 @@ def paged_attention_workspace(n_seq, n_heads, n_kv_heads, head_dim):
 
 def paged_attention(q, cache: PagedKV, block_table, seq_lens, scale, out, workspace, stream=None):
     """One new token per sequence: q, out bf16 [n_seq, heads, D]; attends to the first seq_lens[b] rows of sequence b."""
-    table, ld, pages, lens, n = cache._seqs(block_table, seq_lens)
-    _same_device(cache.device, q=q, out=out, workspace=workspace)
-    rq = _rows(q, "q", None, cache.head_dim, n)
-    heads = q.shape[1]
-    if not workspace.is_contiguous():
-        raise ValueError("paged_attention: the workspace must be contiguous")
-    _call_on(cache.device, stream, lib().paged_attention, rq, heads, cache._desc, table, ld, pages, lens, n,
-             float(scale), _rows(out, "out", heads, cache.head_dim, n), workspace.data_ptr(),
-             workspace.numel() * workspace.element_size())
+    dev, d, seqs = cache.device, cache.head_dim, cache._seqs(block_table, seq_lens)
+    n, (_, heads) = seqs[4], _heads(q, "q")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"paged_attention: a contiguous workspace on CUDA device {dev} is wanted")
+    _call_on(dev, stream, lib().paged_attention, _rows(q, "q", dev, heads, d, n), heads, cache._ref, *seqs, scale,
+             _rows(out, "out", dev, heads, d, n), workspace.data_ptr(), workspace.nbytes)
 
 
 # --------------------------------------------------------------------------------------------- model / session

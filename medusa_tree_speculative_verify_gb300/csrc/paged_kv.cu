@@ -1,12 +1,16 @@
 // Rows of keys and values written into a paged cache, and read back.
 //
-// A row is one token's head_dim values of one kv head. A group of kLanes threads moves one row, 8 elements a thread
-// (16 bytes of bf16, 8 of e4m3). Writing e4m3: the group's largest |x| gives the exponent e, the smallest with max|x| <=
+// A row is one token's head_dim values of one kv head. A group of kLanes threads moves one row, 16 bytes of the
+// pool a thread. Writing e4m3: the group's largest |x| gives the exponent e, the smallest with max|x| <=
 // 448 * 2^e: with max|x| = 1.m * 2^(E-127), 448 = 1.75 * 2^8, that is e = E - 135, one more when 1.m > 1.75. The
 // product with 2^-e is exact (short of underflow), so the row is rounded once, by the conversion, and what it stands
 // for is exact in bf16 again.
 //
-// Bound by memory: 2 * dim bytes read (written) and dim + 1 or 2 * dim written (read) for each row, K and V.
+// Bound by memory: 2 * dim bytes read (written) and dim + 1 or 2 * dim written (read) for each row, K and V. A CTA takes up
+// to 64 consecutive tokens, all heads, K and V: their places are looked up once, by 16 to 4 lanes a token, and 64 bytes a
+// thread are on their way at a time.
+#include <algorithm>
+
 #include "kernels.cuh"
 #include "paged.cuh"
 
@@ -14,44 +18,60 @@ namespace {
 
 constexpr int kThreads = 256;
 
+constexpr int kTokens = 64;   // of a CTA, at most
+constexpr int kResident = 4;  // CTAs of an SM
 struct MoveArgs {
   PagedArgs c;
   RowsArgs k, v;
   const int32_t* cu;
-  int n_rows, tokens;  // tokens: rows of a CTA
+  int n_rows, tokens, look_lanes;  // tokens of a CTA, threads that look one of them up
   unsigned int* err;
 };
 
-// Where row token t of the packed rows lies: page * page_size + slot, -1 for a row behind the last sequence, -2 when
-// the table, the lengths or cu are out of range.
-MV_DEV int64_t place_of(const MoveArgs& a, int t) {
-  if (t >= __ldcg(a.cu + a.c.n_seq)) return -1;
-  int lo = 0, hi = a.c.n_seq;  // the last b with cu[b] <= t (cu[0] = 0), found whatever cu holds
+// Where token t of the packed rows lies: page and slot; page -1 for a row behind the last sequence, -2 when the table,
+// the lengths or cu are out of range. By n = 2^k consecutive lanes, which narrow the sequences down to an n-th at a time.
+MV_DEV int2 place_of(const MoveArgs& a, int t, int n) {
+  const int lane = threadIdx.x & (n - 1), first = threadIdx.x & 31 & ~(n - 1), n_seq = a.c.n_seq;
+  const unsigned int mask = ((1u << n) - 1u) << first;  // n <= 16
+  const int end = __ldcg(a.cu + n_seq);
+  int lo = 0, hi = n_seq;  // the last b in [lo, hi) with cu[b] <= t, where cu does not decrease
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldcg(a.cu + mid) <= t) lo = mid;
-    else hi = mid;
+    const int step = (hi - lo + n - 1) / n, at = lo + lane * step;
+    const bool le = at < hi && __ldcg(a.cu + at) <= t;
+    const unsigned int all = __ballot_sync(mask, le) & mask;
+    if (all) lo += (31 - __clz(all) - first) * step;
+    hi = all ? min(hi, lo + step) : lo + 1;
   }
-  const int c0 = __ldcg(a.cu + lo), c1 = __ldcg(a.cu + lo + 1);
-  if (c0 < 0 || t < c0 || t >= c1) return -2;
-  const int len = __ldcg(a.c.seq_lens + lo);
+  const int c0 = __ldcg(a.cu + lo), c1 = __ldcg(a.cu + lo + 1), len = __ldcg(a.c.seq_lens + lo);
+  if (t >= end) return make_int2(-1, 0);
+  if (c0 < 0 || t < c0 || t >= c1) return make_int2(-2, 0);
   const int64_t pos = (int64_t)len - c1 + t;
-  if (len < c1 - c0 || pos < 0 || pos >= (int64_t)a.c.max_pages * a.c.page_size) return -2;
-  const int page = __ldcg(a.c.table + (int64_t)lo * a.c.ld_table + (int)pos / a.c.page_size);
-  if (page < 0 || page >= a.c.n_pages) return -2;
-  return (int64_t)page * a.c.page_size + (int)pos % a.c.page_size;
+  if (len < c1 - c0 || pos < 0 || pos >= (int64_t)a.c.max_pages * a.c.page_size) return make_int2(-2, 0);
+  const int nth = (int)pos / a.c.page_size;
+  const int page = __ldcg(a.c.table + (int64_t)lo * a.c.ld_table + nth);
+  if (page < 0 || page >= a.c.n_pages) return make_int2(-2, 0);
+  return make_int2(page, (int)pos - nth * a.c.page_size);
 }
 
-template <bool kE4M3, bool kWrite>
-__global__ void __launch_bounds__(kThreads) paged_rows_kernel(const MoveArgs a, int lanes) {
-  __shared__ int64_t s_place[32];
+// kLanes threads a row, the power of two from dim / kEl up
+template <bool kE4M3, bool kWrite, int kLanes>
+__global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const MoveArgs a) {
+  constexpr int kEl = kE4M3 ? 16 : 8;              // elements of a thread
+  constexpr int kAhead = kE4M3 && kWrite ? 2 : 4;  // rows on their way: 64 bytes a thread
+  constexpr int kWords = kE4M3 && kWrite ? 8 : 4;
+  __shared__ int2 s_place[kTokens];
   pdl_trigger();
   pdl_wait();
   const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n_rows - t0);
-  if ((int)threadIdx.x < nt) {
-    const int64_t at = place_of(a, t0 + threadIdx.x);
-    if (at == -2) mv_set_error_detail(a.err, kPagedRowsSite, MV_DEVERR_INDEX, (uint32_t)(t0 + threadIdx.x));
-    s_place[threadIdx.x] = at;
+  {
+    const int i = threadIdx.x / a.look_lanes;
+    if (i < nt) {
+      const int2 at = place_of(a, t0 + i, a.look_lanes);
+      if ((threadIdx.x & (a.look_lanes - 1)) == 0) {
+        if (at.x == -2) mv_set_error_detail(a.err, kPagedRowsSite, MV_DEVERR_INDEX, (uint32_t)(t0 + i));
+        s_place[i] = at;
+      }
+    }
   }
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < a.c.n_seq; b += kThreads) {
@@ -60,64 +80,98 @@ __global__ void __launch_bounds__(kThreads) paged_rows_kernel(const MoveArgs a, 
         mv_set_error_detail(a.err, kPagedRowsSite, MV_DEVERR_INDEX, (uint32_t)b);
     }
   __syncthreads();
-  const int ln = threadIdx.x & (lanes - 1), d0 = ln * 8;  // this thread's elements d0 .. d0 + 7 of its row
+  constexpr int kGroups = kThreads / kLanes;                           // rows at a time
+  const int ln = threadIdx.x % kLanes, group = threadIdx.x / kLanes, d0 = ln * kEl;  // elements d0 .. of a row
   const int H = a.c.heads, D = a.c.dim, P = a.c.page_size;
-  const int rows = nt * 2 * H;  // (token, K or V, head), heads fastest
-  // whole groups of lanes leave the loop together: rows is the same for all of a group
-  for (int r = threadIdx.x / lanes; r < rows; r += kThreads / lanes) {
-    const int h = r % H, tv = r / H, tok = tv >> 1;
-    const int64_t at = s_place[tok];
-    const bool is_v = tv & 1, live = at >= 0 && d0 < D;
-    const RowsArgs& x = is_v ? a.v : a.k;
-    uint16_t* row = x.p + (int64_t)(t0 + tok) * x.ts + (int64_t)h * x.hs + d0;
-    const int64_t prow = at < 0 ? 0 : (at / P * H + h) * P + at % P;
-    uint8_t* pages = is_v ? a.c.v : a.c.k;
-    if (!kE4M3) {
-      uint4* held = reinterpret_cast<uint4*>(pages + (prow * D + d0) * 2);
-      if (live) {
-        if (kWrite) *held = *reinterpret_cast<const uint4*>(row);
-        else *reinterpret_cast<uint4*>(row) = *held;
-      }
-    } else {
-      uint8_t* exps = is_v ? a.c.v_exp : a.c.k_exp;
-      uint2* held = reinterpret_cast<uint2*>(pages + prow * D + d0);
-      if (kWrite) {
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (live) raw = *reinterpret_cast<const uint4*>(row);
-        float f[8];
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        float top = 0.0f;
+  const int rows = nt * 2 * H;
+  // The order of the rows is the source's: heads, then K and V, then tokens of the caller's; tokens of the pool's
+  const int n_fast = kWrite ? H : nt, add_slow = kGroups / n_fast, add_fast = kGroups % n_fast;
+  int slow = group / n_fast, fast = group - slow * n_fast;
+  for (int r0 = group; r0 < rows; r0 += kAhead * kGroups) {  // the lanes of a group stay together
+    uint8_t *to[kAhead], *exp[kAhead];                       // null: nothing to move
+    uint32_t x[kAhead][kWords], byte[kAhead];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[2 * i] = bf16lo(w[i]);
-          f[2 * i + 1] = bf16hi(w[i]);
-          top = fmaxf(top, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));  // a NaN does not count
+    for (int i = 0; i < kAhead; ++i) {
+      to[i] = nullptr;
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) x[i][j] = 0u;
+      const bool is_v = kWrite ? slow & 1 : slow >= H;
+      const int tok = kWrite ? slow >> 1 : fast, h = kWrite ? fast : slow - (is_v ? H : 0);
+      const int2 at = r0 + i * kGroups < rows ? s_place[tok] : make_int2(-1, 0);
+      if (at.x >= 0 && d0 < D) {
+        const RowsArgs& p = is_v ? a.v : a.k;
+        const int64_t prow = ((int64_t)at.x * H + h) * P + at.y;
+        uint8_t* row = reinterpret_cast<uint8_t*>(p.p + (int64_t)(t0 + tok) * p.ts + (int64_t)h * p.hs + d0);
+        uint8_t* held = (is_v ? a.c.v : a.c.k) + (prow * D + d0) * (kE4M3 ? 1 : 2);
+        to[i] = kWrite ? held : row;
+        if (kE4M3) exp[i] = (is_v ? a.c.v_exp : a.c.k_exp) + prow;
+        const uint4* from = reinterpret_cast<const uint4*>(kWrite ? row : held);
+#pragma unroll
+        for (int j = 0; j < kWords / 4; ++j) {
+          const uint4 w = from[j];
+          x[i][4 * j] = w.x;
+          x[i][4 * j + 1] = w.y;
+          x[i][4 * j + 2] = w.z;
+          x[i][4 * j + 3] = w.w;
         }
-        const uint32_t mask = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
-        for (int o = lanes >> 1; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o));
+        if (kE4M3 && !kWrite) byte[i] = *exp[i];
+      }
+      slow += add_slow;
+      fast += add_fast;
+      if (fast >= n_fast) {
+        fast -= n_fast;
+        ++slow;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (!kE4M3) {
+        if (to[i]) *reinterpret_cast<uint4*>(to[i]) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+      } else if (kWrite) {
+        float f[16], top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          f[(2 * j) & 15] = bf16lo(x[i][j]);
+          f[(2 * j + 1) & 15] = bf16hi(x[i][j]);
+          top = fmaxf(top, fmaxf(fabsf(f[(2 * j) & 15]), fabsf(f[(2 * j + 1) & 15])));  // a NaN does not count
+        }
+        // groups of one warp may have left the loop: a mask of this group's lanes
+        const unsigned int mask = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
+#pragma unroll
+        for (int o = kLanes >> 1; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(mask, top, o));
         const uint32_t b = __float_as_uint(top);
         const int e = max(-100, min(120, (int)(b >> 23) - 135 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0)));
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        uint16_t q[4];
+        uint32_t q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = float2_to_e4m3x2(f[2 * i] * inv, f[2 * i + 1] * inv);
-        if (live) {
-          *held = make_uint2((uint32_t)q[0] | ((uint32_t)q[1] << 16), (uint32_t)q[2] | ((uint32_t)q[3] << 16));
-          if (ln == 0) exps[prow] = (uint8_t)(e + 127);
+        for (int j = 0; j < 4; ++j)
+          q[j] = float2_to_e4m3x2(f[4 * j] * inv, f[4 * j + 1] * inv) |
+                 ((uint32_t)float2_to_e4m3x2(f[4 * j + 2] * inv, f[4 * j + 3] * inv) << 16);
+        if (to[i]) {
+          *reinterpret_cast<uint4*>(to[i]) = make_uint4(q[0], q[1], q[2], q[3]);
+          if (ln == 0) *exp[i] = (uint8_t)(e + 127);
         }
-      } else if (live) {
-        const float s = exp_byte_scale(exps[prow]);
-        const uint2 w = *held;
-        uint32_t o[4];
+      } else if (to[i]) {
+        const float s = exp_byte_scale(byte[i]);
+        uint32_t o[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = half2_to_float2(e4m3x2_to_half2((uint16_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1)))));
-          o[i] = pack_bf16x2(f.x * s, f.y * s);
+        for (int j = 0; j < 8; ++j) {
+          const float2 f = half2_to_float2(e4m3x2_to_half2((uint16_t)(x[i][j >> 1] >> (16 * (j & 1)))));
+          o[j] = pack_bf16x2(f.x * s, f.y * s);
         }
-        *reinterpret_cast<uint4*>(row) = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4*>(to[i])[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4*>(to[i])[1] = make_uint4(o[4], o[5], o[6], o[7]);
       }
     }
   }
+}
+
+template <bool kE4M3, bool kWrite>
+cudaError_t launch_rows(const MoveArgs& a, dim3 grid, cudaStream_t st) {
+  constexpr int kMost = kE4M3 ? 8 : 16;
+  if (a.c.dim > 64) return mv_launch(paged_rows_kernel<kE4M3, kWrite, kMost>, grid, dim3(kThreads), 0, st, a);
+  if (a.c.dim > 32) return mv_launch(paged_rows_kernel<kE4M3, kWrite, kMost / 2>, grid, dim3(kThreads), 0, st, a);
+  return mv_launch(paged_rows_kernel<kE4M3, kWrite, kMost / 4>, grid, dim3(kThreads), 0, st, a);
 }
 
 template <bool kWrite>
@@ -136,15 +190,19 @@ mv_status move_rows(const mv_rows& k, const mv_rows& v, int32_t n_rows, const in
   a.v = {static_cast<uint16_t*>(v.ptr), v.token_stride, v.head_stride};
   a.cu = cu;
   a.n_rows = n_rows;
-  a.tokens = 1;
+  // whole waves of CTAs with as many tokens each as share one round of lookups, which nothing hides
+  // (reads at most 16: they do better with more and smaller ones, 46 against 51 us for 234 MB; writes do not, 90 and 85 us
+  // for 340 MB)
+  const int64_t ctas = kResident * mv_sm_count(), most = kWrite ? kTokens : 16;
+  const int64_t waves = (n_rows + ctas * most - 1) / (ctas * most);
+  a.tokens = (int)((n_rows + ctas * waves - 1) / (ctas * waves));
+  a.look_lanes = 16;
+  while (a.look_lanes * a.tokens > kThreads) a.look_lanes /= 2;
   a.err = mv_error_word();
-  int lanes = 2;
-  while (lanes * 8 < a.c.dim) lanes *= 2;
   const dim3 grid((n_rows + a.tokens - 1) / a.tokens);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->dtype == MV_DTYPE_E4M3
-                            ? mv_launch(paged_rows_kernel<true, kWrite>, grid, dim3(kThreads), 0, st, a, lanes)
-                            : mv_launch(paged_rows_kernel<false, kWrite>, grid, dim3(kThreads), 0, st, a, lanes);
+  const cudaError_t e = cache->dtype == MV_DTYPE_E4M3 ? launch_rows<true, kWrite>(a, grid, st)
+                                                      : launch_rows<false, kWrite>(a, grid, st);
   return e == cudaSuccess ? mv_last_launch("paged_rows") : MV_ERR_CUDA;
 }
 

@@ -139,7 +139,7 @@ def test_prompt_attention_refusals():
 def test_binding_refuses_what_the_library_cannot_see():
     t = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
-        mv._rows(t, "q")                                      # not on a GPU
+        mv.prompt_attention(t, t, t, mv.PromptPlan([4]), 1.0, t)   # not on a GPU
     with pytest.raises(ValueError):
         mv.PagedKV(t, t)
     with pytest.raises(ValueError):
