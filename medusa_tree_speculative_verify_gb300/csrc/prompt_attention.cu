@@ -33,7 +33,7 @@ constexpr uint32_t kSite = 42;  // device error site
 struct PromptArgs {
   RowsArgs q, k, v, out;
   const int4* items;
-  int group, kv_heads, dim, head_major;
+  int group, kv_heads, dim, head_outer;  // head_outer: bit 0, 1, 2: q, k, v have the head as the outermost dimension
   float scale_log2;
   unsigned int* err;
 };
@@ -68,7 +68,11 @@ MV_DEV void add_specials(const PromptArgs& a, float (&o)[32], int d0, int t0, in
     }
 }
 
-constexpr int kThreads = 320;  // warps 0-3 and 4-7: softmax of sub-tile 0 and 1; warp 8: products; warp 9: copies
+// Warps 0-15: softmax, of sub-tile warp / 8 and of keys 64 (warp / 4 % 2) .. of a tile, for the rows of TMEM's lanes
+// 32 (warp % 4) ..; warp 16: products, warp 17: copies (18 and 19 fill up their warpgroup, whose registers go to the
+// softmax)
+constexpr int kSoftmaxWarps = 16, kThreads = 640;
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 4 * 104 + 64 <= 5 * 96, what a block of 640 threads starts with
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;  // move the exponent reference when the row maximum grows by more than this
 
@@ -82,12 +86,19 @@ struct Layout {
   static constexpr int kTile = kHalves * kRegion;
   static constexpr int kRing = kDim == 128 ? 5 : 10;
   static constexpr int kKV = 2 * kTile;
-  static constexpr int kBytes = kKV + kRing * kTile + 1024;
-  static_assert(kBytes <= 230 * 1024, "shared memory of one CTA");
+  static constexpr int kRest = kKV + kRing * kTile;
   // Tensor memory: S of the two sub-tiles, their O, and P (bf16, two keys a column). With 128-wide heads all 512
   // columns are taken and P lies over the S that it is computed from.
   static constexpr uint32_t kColS = 0, kColO = 256;
   static constexpr uint32_t kColP = kDim == 128 ? 0 : 384, kPStep = kDim == 128 ? 128 : 64;
+};
+
+// What follows the tiles in shared memory.
+struct Rest {
+  uint64_t qfull, full[10], empty[10], sfull[2], pfull[2], ofull[2], drain;
+  uint32_t tmem;
+  volatile int abort, special;
+  float half[2][2][kRows];  // [sub-tile][half]: what the two threads of a row tell each other
 };
 
 template <int kDim>
@@ -96,13 +107,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap vmap, const PromptArgs a) {
   using Ly = Layout<kDim>;
   constexpr uint32_t kIdS = tc_idesc(kRows, false), kIdO = tc_idesc(kDim, true);
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // All of the shared memory is this array, which starts on a multiple of 1024 bytes then: there is no room to round up
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + Ly::kKV;
-  __shared__ __align__(8) uint64_t qfull, full[Ly::kRing], empty[Ly::kRing], sfull[2], pfull[2], ofull[2], drain;
-  __shared__ uint32_t tmem_sh;
-  __shared__ volatile int s_abort, s_special;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Rest& sh = *reinterpret_cast<Rest*>(smem + Ly::kRest);
+  uint64_t &qfull = sh.qfull, (&full)[10] = sh.full, (&empty)[10] = sh.empty, (&sfull)[2] = sh.sfull,
+           (&pfull)[2] = sh.pfull, (&ofull)[2] = sh.ofull, &drain = sh.drain;
+  volatile int &s_abort = sh.abort, &s_special = sh.special;
+  if (smem_u32(smem) & 1023) {
+    if (threadIdx.x == 0) mv_set_error(a.err, kSite, MV_DEVERR_INDEX);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
   const int4 item = a.items[blockIdx.x / a.kv_heads];
   const int kh = blockIdx.x % a.kv_heads, t0 = item.x, len = item.y;
@@ -123,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sfull[s], 1);
-      mbar_init(&pfull[s], kRows);
+      mbar_init(&pfull[s], kSoftmaxWarps / 2);
       mbar_init(&ofull[s], 1);
     }
     mbar_init(&drain, 1);
@@ -131,106 +147,147 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_special = 0;
     mbar_fence_init();
   }
-  if (warp == 8) {
-    tc_alloc(&tmem_sh, kTmemCols);
+  if (warp == kSoftmaxWarps) {
+    tc_alloc(&sh.tmem, kTmemCols);
     tc_relinquish();
   }
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = tmem_sh;
+  const uint32_t tmem = sh.tmem;
   pdl_trigger();
   pdl_wait();
 
-  // a bounded wait that gives up at once after any other wait of this CTA gave up
+  // a bounded wait that also gives up once any other wait of this CTA has
   auto wait = [&](uint64_t* bar, int phase) {
-    if (s_abort) return false;
-    if (mbar_wait(bar, (uint32_t)(phase & 1))) return true;
-    s_abort = 1;
-    return false;
+    if (mbar_try_wait(bar, (uint32_t)(phase & 1))) return true;
+    const uint64_t t_start = mv_globaltimer();
+    while (!mbar_try_wait(bar, (uint32_t)(phase & 1)))
+      if (s_abort || mv_globaltimer() - t_start > MV_WAIT_LIMIT_NS) {
+        s_abort = 1;
+        return false;
+      }
+    return true;
   };
 
-  if (warp == 9) {
-    // ------------------------------------------------------------------ copies (one thread)
-    if (lane == 0) {
-      const int c1 = a.head_major;  // bit 0, 1, 2: q, k, v have the head as the outermost dimension
-      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int hm, int h, int row) {
+  if (warp >= kSoftmaxWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    int st = 0, phase = 0;  // place in the ring of the tile at hand
+    auto next = [&]() {
+      if (++st == Ly::kRing) {
+        st = 0;
+        phase ^= 1;
+      }
+    };
+    if (warp == kSoftmaxWarps + 1 && lane == 0) {
+      // ---------------------------------------------------------------- copies (one thread)
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head_outer, int h, int row) {
 #pragma unroll
         for (int hb = 0; hb < Ly::kHalves; ++hb)
-          tma_load_3d(dst + hb * Ly::kRegion, map, bar, hb * 64, hm ? row : h, hm ? h : row);
+          tma_load_3d(dst + hb * Ly::kRegion, map, bar, hb * 64, head_outer ? row : h, head_outer ? h : row);
       };
       mbar_arrive_expect_tx(&qfull, (uint32_t)((tiles[1] ? 2 : 1) * Ly::kTile));
-      load(smem, &qmap, &qfull, c1 & 1, head[0], t0 + block[0] * kRows);
-      if (tiles[1]) load(smem + Ly::kTile, &qmap, &qfull, c1 & 1, head[1], t0 + block[1] * kRows);
+      load(smem, &qmap, &qfull, a.head_outer & 1, head[0], t0 + block[0] * kRows);
+      if (tiles[1]) load(smem + Ly::kTile, &qmap, &qfull, a.head_outer & 1, head[1], t0 + block[1] * kRows);
       int n = 0;
-      for (; n < 2 * n_tiles; ++n) {  // K of tile 0, V of tile 0, K of tile 1, ...
-        const int st = n % Ly::kRing;
-        if (n >= Ly::kRing && !wait(&empty[st], n / Ly::kRing - 1)) break;
+      for (; n < 2 * n_tiles; ++n, next()) {  // K of tile 0, V of tile 0, K of tile 1, ...
+        if (n >= Ly::kRing && !wait(&empty[st], phase ^ 1)) break;
         mbar_arrive_expect_tx(&full[st], (uint32_t)Ly::kTile);
-        load(ring + st * Ly::kTile, n & 1 ? &vmap : &kmap, &full[st], n & 1 ? c1 & 4 : c1 & 2, kh, t0 + (n >> 1) * kRows);
+        load(ring + st * Ly::kTile, n & 1 ? &vmap : &kmap, &full[st], a.head_outer & (n & 1 ? 4 : 2), kh,
+             t0 + (n >> 1) * kRows);
       }
       // every copy has landed before the CTA may leave (they have, unless a wait gave up)
       if (s_abort) mbar_wait(&qfull, 0u);
       for (int i = max(0, n - Ly::kRing); i < n; ++i)
         if (!mbar_wait(&full[i % Ly::kRing], (uint32_t)((i / Ly::kRing) & 1))) break;
-    }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------------ products (one thread)
-    // S_s(j) = Q_s K(j)^T, O_s += P_s(j) V(j). S of the next tile goes right behind the P V that frees its place; the
-    // products of one sub-tile run while the other one's softmax works.
-    if (lane == 0) {
-      auto mma_s = [&](int s, int j) {
-        const uint32_t qb = smem_u32(smem) + s * Ly::kTile, kb = smem_u32(ring) + 2 * j % Ly::kRing * Ly::kTile;
+    } else if (warp == kSoftmaxWarps) {
+      // ---------------------------------------------------------------- products (one warp, an elected lane issues)
+      // S_s(j) = Q_s K(j)^T, O_s += P_s(j) V(j). S of the next tile goes right behind the P V that frees its place; the
+      // products of one sub-tile run while the other one's softmax works. The tensor cores take few products ahead, so what
+      // this warp spends between them is lost: descriptors and places are carried along, nothing is divided. (A warp
+      // for each sub-tile interleaves the two chains product by product: 550 us in place of 446 for 8192 tokens.)
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int n0 = __shfl_sync(0xffffffffu, tiles[0], 0), n1 = __shfl_sync(0xffffffffu, tiles[1], 0);
+      const int n_all = max(n0, n1);
+      const uint64_t q_desc = desc_kmajor(smem_u32(smem)), k_desc = desc_kmajor(smem_u32(ring)),
+                     v_desc = desc_mnmajor(smem_u32(ring), (uint32_t)Ly::kRegion);
+      auto all_wait = [&](uint64_t* bar, int ph) { return __all_sync(0xffffffffu, wait(bar, ph)) != 0; };
+      auto mma_s = [&](int s, int at) {
+        const uint64_t q = q_desc + (uint64_t)(s * (Ly::kTile >> 4)), k = k_desc + (uint64_t)(at * (Ly::kTile >> 4));
+        if (elect_one()) {
 #pragma unroll
-        for (int hb = 0; hb < Ly::kHalves; ++hb)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_f16(tmem + Ly::kColS + 128 * s, desc_kmajor(qb + hb * Ly::kRegion) + (uint64_t)(2 * k),
-                       desc_kmajor(kb + hb * Ly::kRegion) + (uint64_t)(2 * k), kIdS, (hb | k) ? 1u : 0u);
-        tc_commit_to(&sfull[s]);
-      };
-      auto mma_o = [&](int s, int j) {
-        const uint32_t vb = smem_u32(ring) + (2 * j + 1) % Ly::kRing * Ly::kTile;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)  // 16 keys each
-          tc_mma_f16_ta(tmem + Ly::kColO + kDim * s, tmem + Ly::kColP + Ly::kPStep * s + 8 * k,
-                        desc_mnmajor(vb + (uint32_t)(16 * k * 128), (uint32_t)Ly::kRegion), kIdO,
-                        (j > 0 || k > 0) ? 1u : 0u);
-      };
-      auto tile_in = [&](int n) { return wait(&full[n % Ly::kRing], n / Ly::kRing); };
-      bool ok = wait(&qfull, 0) && tile_in(0);
-      tc_after();
-      if (ok)
-        for (int s = 0; s < 2; ++s)
-          if (tiles[s]) mma_s(s, 0);
-      tc_commit_to(&empty[0]);
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        ok = tile_in(2 * j + 1) && (j + 1 == n_tiles || tile_in(2 * j + 2));
-        for (int s = 0; ok && s < 2; ++s) {
-          if (j >= tiles[s]) continue;
-          if (!(ok = wait(&pfull[s], j))) break;
-          tc_after();
-          mma_o(s, j);
-          if (j + 1 < tiles[s]) mma_s(s, j + 1);
-          else tc_commit_to(&ofull[s]);
+          for (int i = 0; i < kDim / 16; ++i)
+            tc_mma_f16(tm + Ly::kColS + 128 * s, q + (uint64_t)(i / 4 * (Ly::kRegion >> 4) + i % 4 * 2),
+                       k + (uint64_t)(i / 4 * (Ly::kRegion >> 4) + i % 4 * 2), kIdS, i ? 1u : 0u);
+          tc_commit_to(&sfull[s]);
         }
-        if (!ok) break;
-        tc_commit_to(&empty[(2 * j + 1) % Ly::kRing]);
-        if (j + 1 < n_tiles) tc_commit_to(&empty[(2 * j + 2) % Ly::kRing]);
+      };
+      auto mma_o = [&](int s, int at, bool first) {
+        const uint64_t v = v_desc + (uint64_t)(at * (Ly::kTile >> 4));
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)  // 16 keys each
+            tc_mma_f16_ta(tm + Ly::kColO + kDim * s, tm + Ly::kColP + Ly::kPStep * s + 8 * i,
+                          v + (uint64_t)(i * (16 * 128 >> 4)), kIdO, first && i == 0 ? 0u : 1u);
+        }
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc_commit_to(bar);
+      };
+      bool ok = all_wait(&qfull, 0) && all_wait(&full[0], 0);
+      tc_after();
+      if (ok) {
+        if (n0) mma_s(0, 0);
+        if (n1) mma_s(1, 0);
+      }
+      commit(&empty[0]);
+      next();
+      for (int j = 0; ok && j < n_all; ++j) {
+        const int v_st = st;
+        if (!(ok = all_wait(&full[st], phase))) break;  // V(j)
+        next();
+        if (j + 1 < n_all && !(ok = all_wait(&full[st], phase))) break;  // K(j + 1)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int n = s ? n1 : n0;
+          if (ok && j < n) {
+            ok = all_wait(&pfull[s], j);
+            if (!ok) continue;
+            tc_after();
+            mma_o(s, v_st, j == 0);
+            if (j + 1 < n) mma_s(s, st);
+            else commit(&ofull[s]);
+          }
+        }
+        if (j + 1 < n_all) {
+          commit(&empty[v_st]);
+          commit(&empty[st]);
+          next();
+        }
       }
       if (!ok) {  // every product issued finishes before the CTA's memory is let go
         mv_set_error(a.err, kSite, MV_DEVERR_TIMEOUT);
-        tc_commit_to(&drain);
+        commit(&drain);
         mbar_wait(&drain, 0u);
       }
     }
   } else {
-    // ------------------------------------------------------------------ softmax: one thread for each query row
-    const int s = warp >> 2, r = tid & (kRows - 1), n = tiles[s], i = block[s] * kRows + r;
+    // ------------------------------------------------------------------ softmax: two threads for each query row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int s = warp >> 3, half = (warp >> 2) & 1, r = tid & (kRows - 1), n = tiles[s], i = block[s] * kRows + r;
+    const int pair = 1 + (warp & 3) + 4 * s;  // named barrier of the two warps that share rows
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t at_s = lane_base + Ly::kColS + 128 * s, at_p = lane_base + Ly::kColP + Ly::kPStep * s,
-                   at_o = lane_base + Ly::kColO + kDim * s;
-    float m_ref = -INFINITY, l = 0.0f;  // exponent reference (log2 domain) and sum
+    const uint32_t at_s = lane_base + Ly::kColS + 128 * s + 64 * half;
+    const uint32_t at_p = lane_base + Ly::kColP + Ly::kPStep * s + 32 * half;
+    const uint32_t at_o = lane_base + Ly::kColO + kDim * s + kDim / 2 * half;  // this thread's half of the row's output
+    // what both threads of a row put in, in either's hand
+    // (the place is free again for the next tile: S of that comes after every warp's P of this)
+    auto exchange = [&](float mine) {
+      sh.half[s][half][r] = mine;
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+      return sh.half[s][half ^ 1][r];
+    };
+    float m_ref = -INFINITY, l = 0.0f;  // exponent reference (log2 domain, the same in both threads) and this half's sum
     for (int j = 0; j < n; ++j) {
       if (j == n - 1) {
         // The last tile holds keys after this row. Their weights are zero, but zero times a NaN or an infinity in V
@@ -241,14 +298,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4* v = reinterpret_cast<uint4*>(ring + (2 * j + 1) % Ly::kRing * Ly::kTile);
         uint32_t any = 0;
 #pragma unroll 4
-        for (int e = r; e < Ly::kTile / 16; e += kRows) {
+        for (int e = tid & (2 * kRows - 1); e < Ly::kTile / 16; e += 2 * kRows) {
           const uint4 w = v[e];
           any |= special2(w.x) | special2(w.y) | special2(w.z) | special2(w.w);
         }
         if (any) {
           s_special = 1;
           __threadfence_block();
-          for (int e = r; e < Ly::kTile / 16; e += kRows) {
+          for (int e = tid & (2 * kRows - 1); e < Ly::kTile / 16; e += 2 * kRows) {
             const uint4 w = v[e];
             v[e] = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
           }
@@ -258,16 +315,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(&sfull[s], j);
       __syncwarp();
       tc_after();
-      float x[kRows];
-      tc_ld128(at_s, x);
+      float x[64];
+      tc_ld64(at_s, x);
       if (j == n - 1) {
 #pragma unroll
-        for (int c = 0; c < kRows; ++c)
-          if (c > r) x[c] = -INFINITY;
+        for (int c = 0; c < 64; ++c)
+          if (64 * half + c > r) x[c] = -INFINITY;
       }
-      float top = x[0];
+      float tops[4] = {x[0], x[1], x[2], x[3]};  // chains short enough to issue without waiting
 #pragma unroll
-      for (int c = 1; c < kRows; ++c) top = fmaxf(top, x[c]);
+      for (int c = 4; c < 64; c += 2) tops[(c >> 1) & 3] = fmaxf(tops[(c >> 1) & 3], fmaxf(x[c], x[c + 1]));
+      float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+      top = fmaxf(top, exchange(top));  // both have read their S: P may be written over it
       const float m_new = fmaxf(m_ref, top * a.scale_log2);
       const bool move = m_new > m_ref + kRescaleLog2 || (m_ref == -INFINITY && m_new > -INFINITY);
       // O of this sub-tile is at rest: its last P V came before the S that was waited for
@@ -275,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = move ? fast_exp2(m_ref - m_new) : 1.0f;
         l *= f;
 #pragma unroll
-        for (int c = 0; c < kDim / 32; ++c) {
+        for (int c = 0; c < kDim / 64; ++c) {
           float o[32];
           tc_ld32(at_o + 32 * c, o);
 #pragma unroll
@@ -285,43 +344,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (move) m_ref = m_new;
       const float base = m_ref == -INFINITY ? 0.0f : m_ref;
-      float sum = 0.0f;
+      const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
+      uint64_t sums[4] = {};
+      uint32_t p[32];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t p[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float p0 = fast_exp2(fmaf(x[64 * half + 2 * e], a.scale_log2, -base));
-          const float p1 = fast_exp2(fmaf(x[64 * half + 2 * e + 1], a.scale_log2, -base));
-          sum += p0 + p1;
-          p[e] = pack_bf16x2(p0, p1);
-        }
-        tc_st32u(at_p + 32 * half, p);
+      for (int e = 0; e < 32; ++e) {
+        const float2 y = unpack2(fma2(pack2(x[2 * e], x[2 * e + 1]), scale2, base2));
+        const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
+        sums[e & 3] = add2(sums[e & 3], pack2(p0, p1));
+        p[e] = pack_bf16x2(p0, p1);
       }
-      l += sum;
+      tc_st32u(at_p, p);
+      const float2 sum = unpack2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+      l += sum.x + sum.y;
       tc_wait_st();
       tc_before();
-      mbar_arrive(&pfull[s]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pfull[s]);
     }
     if (n > 0) {
       const bool live = wait(&ofull[s], 0) && i < len;
+      l += exchange(l);
       __syncwarp();
       tc_after();
       const float inv = 1.0f / l;
       uint16_t* row = a.out.p + (int64_t)(t0 + i) * a.out.ts + (int64_t)head[s] * a.out.hs;
       const bool special = s_special;
 #pragma unroll
-      for (int c = 0; c < kDim / 32; ++c) {
+      for (int c = 0; c < kDim / 64; ++c) {
+        const int d0 = kDim / 2 * half + 32 * c;
         float o[32];
         tc_ld32(at_o + 32 * c, o);
         if (live) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if (special) add_specials(a, o, 32 * c, t0, i, kh, block);
+          if (special) add_specials(a, o, d0, t0, i, kh, block);
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            if (32 * c + e < a.dim)
-              *reinterpret_cast<uint4*>(row + 32 * c + e) =
+            if (d0 + e < a.dim)
+              *reinterpret_cast<uint4*>(row + d0 + e) =
                   make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
                              pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
         }
@@ -333,14 +394,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_after();
   if (s_abort && tid == 0) mv_set_error(a.err, kSite, MV_DEVERR_TIMEOUT);
-  if (warp == 8) tc_dealloc(tmem, kTmemCols);
+  if (warp == kSoftmaxWarps) tc_dealloc(tmem, kTmemCols);
 }
 
 template <int kDim>
 mv_status launch(const CUtensorMap (&maps)[3], const PromptArgs& a, int64_t grid, cudaStream_t stream) {
+  constexpr int kBytes = Layout<kDim>::kRest + (int)sizeof(Rest);
+  static_assert(kBytes <= 227 * 1024 && Layout<kDim>::kRing <= 10, "shared memory of one CTA");
   static int flags[64] = {};
-  if (!mv_set_smem_once((const void*)prompt_attn_kernel<kDim>, Layout<kDim>::kBytes, flags)) return MV_ERR_CUDA;
-  const cudaError_t e = mv_launch(prompt_attn_kernel<kDim>, dim3((unsigned)grid), dim3(kThreads), Layout<kDim>::kBytes,
+  if (!mv_set_smem_once((const void*)prompt_attn_kernel<kDim>, kBytes, flags)) return MV_ERR_CUDA;
+  // the warpgroups' shares come out of the registers that the block starts with: never launch with fewer
+  static const int regs = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, prompt_attn_kernel<kDim>) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs * kThreads < 128 * (kSoftmaxWarps / 4 * kSoftmaxRegs + kOtherRegs)) return MV_ERR_UNSUPPORTED;
+  const cudaError_t e = mv_launch(prompt_attn_kernel<kDim>, dim3((unsigned)grid), dim3(kThreads), kBytes,
                                   stream, maps[0], maps[1], maps[2], a);
   return e == cudaSuccess ? mv_last_launch("prompt_attention") : MV_ERR_CUDA;
 }
@@ -475,7 +544,7 @@ extern "C" mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n
   if (!rows_map(&maps[0], q, T, n_heads, head_dim, &hm[0]) || !rows_map(&maps[1], k, T, n_kv_heads, head_dim, &hm[1]) ||
       !rows_map(&maps[2], v, T, n_kv_heads, head_dim, &hm[2]))
     return MV_ERR_CUDA;
-  a.head_major = (hm[0] ? 1 : 0) | (hm[1] ? 2 : 0) | (hm[2] ? 4 : 0);
+  a.head_outer = (hm[0] ? 1 : 0) | (hm[1] ? 2 : 0) | (hm[2] ? 4 : 0);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return head_dim <= 64 ? launch<64>(maps, a, grid, st) : launch<128>(maps, a, grid, st);
 }
