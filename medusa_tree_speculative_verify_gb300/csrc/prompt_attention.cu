@@ -69,8 +69,8 @@ MV_DEV void add_specials(const PromptArgs& a, float (&o)[32], int d0, int t0, in
 }
 
 // Warps 0-15: softmax, of sub-tile warp / 8 and of keys 64 (warp / 4 % 2) .. of a tile, for the rows of TMEM's lanes
-// 32 (warp % 4) ..; warp 16: products, warp 17: copies (18 and 19 fill up their warpgroup, whose registers go to the
-// softmax)
+// 32 (warp % 4) ..; warp 16: products, warp 17: copies, warp 18 tells when both operands are there (19 fills up
+// the warpgroup, whose registers go to the softmax)
 constexpr int kSoftmaxWarps = 16, kThreads = 640;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 4 * 104 + 64 <= 5 * 96, what a block of 640 threads starts with
 constexpr uint32_t kTmemCols = 512;
@@ -95,7 +95,7 @@ struct Layout {
 
 // What follows the tiles in shared memory.
 struct Rest {
-  uint64_t qfull, full[10], empty[10], sfull[2], pfull[2], ofull[2], drain;
+  uint64_t qfull, full[10], freed[8], sfull[2], pfull[2], ofull[2], drain;
   uint32_t tmem;
   volatile int abort, special;
   float half[2][2][kRows];  // [sub-tile][half]: what the two threads of a row tell each other
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + Ly::kKV;
   Rest& sh = *reinterpret_cast<Rest*>(smem + Ly::kRest);
-  uint64_t &qfull = sh.qfull, (&full)[10] = sh.full, (&empty)[10] = sh.empty, (&sfull)[2] = sh.sfull,
+  uint64_t &qfull = sh.qfull, (&full)[10] = sh.full, (&freed)[8] = sh.freed, (&sfull)[2] = sh.sfull,
            (&pfull)[2] = sh.pfull, (&ofull)[2] = sh.ofull, &drain = sh.drain;
   volatile int &s_abort = sh.abort, &s_special = sh.special;
   if (smem_u32(smem) & 1023) {
@@ -133,13 +133,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     mbar_init(&qfull, 1);
-    for (int i = 0; i < Ly::kRing; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
-    }
+    for (int i = 0; i < Ly::kRing; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&freed[i], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sfull[s], 1);
-      mbar_init(&pfull[s], kSoftmaxWarps / 2);
+      mbar_init(&pfull[s], kSoftmaxWarps / 2 + 1);
       mbar_init(&ofull[s], 1);
     }
     mbar_init(&drain, 1);
@@ -172,13 +170,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    int st = 0, phase = 0;  // place in the ring of the tile at hand
-    auto next = [&]() {
-      if (++st == Ly::kRing) {
-        st = 0;
-        phase ^= 1;
-      }
-    };
     if (warp == kSoftmaxWarps + 1 && lane == 0) {
       // ---------------------------------------------------------------- copies (one thread)
       auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head_outer, int h, int row) {
@@ -190,8 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       load(smem, &qmap, &qfull, a.head_outer & 1, head[0], t0 + block[0] * kRows);
       if (tiles[1]) load(smem + Ly::kTile, &qmap, &qfull, a.head_outer & 1, head[1], t0 + block[1] * kRows);
       int n = 0;
-      for (; n < 2 * n_tiles; ++n, next()) {  // K of tile 0, V of tile 0, K of tile 1, ...
-        if (n >= Ly::kRing && !wait(&empty[st], phase ^ 1)) break;
+      for (int st = 0; n < 2 * n_tiles; ++n, st = st + 1 == Ly::kRing ? 0 : st + 1) {  // K(0), V(0), K(1), V(1), ...
+        // what was there: K(i) or V(i - 1), freed as the i-th (at most five are outstanding: eight barriers in turn)
+        const int i = (n - Ly::kRing + 1) >> 1;
+        if (n >= Ly::kRing && !wait(&freed[i & 7], i >> 3)) break;
         mbar_arrive_expect_tx(&full[st], (uint32_t)Ly::kTile);
         load(ring + st * Ly::kTile, n & 1 ? &vmap : &kmap, &full[st], a.head_outer & (n & 1 ? 4 : 2), kh,
              t0 + (n >> 1) * kRows);
@@ -203,15 +196,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kSoftmaxWarps) {
       // ---------------------------------------------------------------- products (one warp, an elected lane issues)
       // S_s(j) = Q_s K(j)^T, O_s += P_s(j) V(j). S of the next tile goes right behind the P V that frees its place; the
-      // products of one sub-tile run while the other one's softmax works. The tensor cores take few products ahead, so what
-      // this warp spends between them is lost: descriptors and places are carried along, nothing is divided. (A warp
-      // for each sub-tile interleaves the two chains product by product: 550 us in place of 446 for 8192 tokens.)
+      // products of one sub-tile run while the other one's softmax works. The tensor cores take only one or two products
+      // ahead, so what this warp spends between them is lost: one wait for each sub-tile and tile (pfull: P is written and
+      // K and V have come), nothing divided, no flag carried along. (A warp for each sub-tile interleaves the two chains
+      // product by product: 550 us in place of 446 for 8192 tokens.)
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const int n0 = __shfl_sync(0xffffffffu, tiles[0], 0), n1 = __shfl_sync(0xffffffffu, tiles[1], 0);
       const int n_all = max(n0, n1);
       const uint64_t q_desc = desc_kmajor(smem_u32(smem)), k_desc = desc_kmajor(smem_u32(ring)),
                      v_desc = desc_mnmajor(smem_u32(ring), (uint32_t)Ly::kRegion);
-      auto all_wait = [&](uint64_t* bar, int ph) { return __all_sync(0xffffffffu, wait(bar, ph)) != 0; };
       auto mma_s = [&](int s, int at) {
         const uint64_t q = q_desc + (uint64_t)(s * (Ly::kTile >> 4)), k = k_desc + (uint64_t)(at * (Ly::kTile >> 4));
         if (elect_one()) {
@@ -231,44 +224,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                           v + (uint64_t)(i * (16 * 128 >> 4)), kIdO, first && i == 0 ? 0u : 1u);
         }
       };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) tc_commit_to(bar);
-      };
-      bool ok = all_wait(&qfull, 0) && all_wait(&full[0], 0);
+      wait(&qfull, 0);
+      wait(&full[0], 0);
+      __syncwarp();
       tc_after();
-      if (ok) {
-        if (n0) mma_s(0, 0);
-        if (n1) mma_s(1, 0);
-      }
-      commit(&empty[0]);
-      next();
-      for (int j = 0; ok && j < n_all; ++j) {
-        const int v_st = st;
-        if (!(ok = all_wait(&full[st], phase))) break;  // V(j)
-        next();
-        if (j + 1 < n_all && !(ok = all_wait(&full[st], phase))) break;  // K(j + 1)
+      if (n0) mma_s(0, 0);
+      if (n1) mma_s(1, 0);
+      if (elect_one()) tc_commit_to(&freed[0]);
+      int v_at = 1, k_at = 2;  // places in the ring of V(j) and K(j + 1)
+      for (int j = 0; j < n_all; ++j) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int n = s ? n1 : n0;
-          if (ok && j < n) {
-            ok = all_wait(&pfull[s], j);
-            if (!ok) continue;
-            tc_after();
-            mma_o(s, v_st, j == 0);
-            if (j + 1 < n) mma_s(s, st);
-            else commit(&ofull[s]);
-          }
+          if (j >= n) continue;
+          wait(&pfull[s], j);
+          __syncwarp();
+          tc_after();
+          mma_o(s, v_at, j == 0);
+          if (j + 1 < n) mma_s(s, k_at);
+          else if (elect_one()) tc_commit_to(&ofull[s]);
         }
-        if (j + 1 < n_all) {
-          commit(&empty[v_st]);
-          commit(&empty[st]);
-          next();
-        }
+        if (j + 1 < n_all && elect_one()) tc_commit_to(&freed[(j + 1) & 7]);
+        v_at = v_at + 2 >= Ly::kRing ? v_at + 2 - Ly::kRing : v_at + 2;
+        k_at = k_at + 2 >= Ly::kRing ? k_at + 2 - Ly::kRing : k_at + 2;
       }
-      if (!ok) {  // every product issued finishes before the CTA's memory is let go
-        mv_set_error(a.err, kSite, MV_DEVERR_TIMEOUT);
-        commit(&drain);
+      if (s_abort) {  // every product issued finishes before the CTA's memory is let go
+        if (elect_one()) tc_commit_to(&drain);
         mbar_wait(&drain, 0u);
+      }
+    } else if (warp == kSoftmaxWarps + 2 && lane == 0) {
+      // ---------------------------------------------------------------- V(j) and K(j + 1) have come: the last arrival at pfull
+      int st = 0, phase = 0;
+      auto next = [&]() {
+        if (++st == Ly::kRing) {
+          st = 0;
+          phase ^= 1;
+        }
+      };
+      for (int j = 0; j < n_tiles; ++j) {
+        next();
+        wait(&full[st], phase);
+        if (j + 1 < n_tiles) {
+          next();
+          wait(&full[st], phase);
+        }
+        for (int s = 0; s < 2; ++s) {
+          if (j >= tiles[s]) continue;
+          if (j > 0) wait(&pfull[s], j - 1);  // not twice in one phase
+          mbar_arrive(&pfull[s]);
+        }
       }
     }
   } else {
