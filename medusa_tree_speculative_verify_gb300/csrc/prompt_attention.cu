@@ -337,28 +337,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j > 0 && __any_sync(0xffffffffu, move)) {
         const float f = move ? fast_exp2(m_ref - m_new) : 1.0f;
         l *= f;
+#pragma unroll 1
+        for (int c = 0; c < kDim / 2; c += 16) {  // seldom: a few registers at a time, the row of S stays in its own
+          uint32_t o[16];
+          tc_ld16u(at_o + c, o);
 #pragma unroll
-        for (int c = 0; c < kDim / 64; ++c) {
-          float o[32];
-          tc_ld32(at_o + 32 * c, o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= f;
-          tc_st32(at_o + 32 * c, o);
+          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tc_st16u(at_o + c, o);
         }
       }
       if (move) m_ref = m_new;
       const float base = m_ref == -INFINITY ? 0.0f : m_ref;
       const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
       uint64_t sums[4] = {};
-      uint32_t p[32];
 #pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const float2 y = unpack2(fma2(pack2(x[2 * e], x[2 * e + 1]), scale2, base2));
-        const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
-        sums[e & 3] = add2(sums[e & 3], pack2(p0, p1));
-        p[e] = pack_bf16x2(p0, p1);
+      for (int q = 0; q < 2; ++q) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 y = unpack2(fma2(pack2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), scale2, base2));
+          const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
+          sums[e & 3] = add2(sums[e & 3], pack2(p0, p1));
+          p[e] = pack_bf16x2(p0, p1);
+        }
+        tc_st16u(at_p + 16 * q, p);
       }
-      tc_st32u(at_p, p);
       const float2 sum = unpack2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
       l += sum.x + sum.y;
       tc_wait_st();
