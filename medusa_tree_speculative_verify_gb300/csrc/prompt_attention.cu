@@ -91,11 +91,13 @@ struct Layout {
   // columns are taken and P lies over the S that it is computed from.
   static constexpr uint32_t kColS = 0, kColO = 256;
   static constexpr uint32_t kColP = kDim == 128 ? 0 : 384, kPStep = kDim == 128 ? 128 : 64;
+  // 64-wide heads: P has its own place, so S of the next tile may be computed as soon as this one's has been read
+  static constexpr bool kEarly = kDim == 64;
 };
 
 // What follows the tiles in shared memory.
 struct Rest {
-  uint64_t qfull, full[10], freed[8], sfull[2], pfull[2], ofull[2], drain;
+  uint64_t qfull, full[10], freed[8], sfull[2], sread[2], pfull[2], ofull[2], drain;
   uint32_t tmem;
   volatile int abort, special;
   float half[2][2][kRows];  // [sub-tile][half]: what the two threads of a row tell each other
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = smem + Ly::kKV;
   Rest& sh = *reinterpret_cast<Rest*>(smem + Ly::kRest);
   uint64_t &qfull = sh.qfull, (&full)[10] = sh.full, (&freed)[8] = sh.freed, (&sfull)[2] = sh.sfull,
-           (&pfull)[2] = sh.pfull, (&ofull)[2] = sh.ofull, &drain = sh.drain;
+           (&sread)[2] = sh.sread, (&pfull)[2] = sh.pfull, (&ofull)[2] = sh.ofull, &drain = sh.drain;
   volatile int &s_abort = sh.abort, &s_special = sh.special;
   if (smem_u32(smem) & 1023) {
     if (threadIdx.x == 0) mv_set_error(a.err, kSite, MV_DEVERR_INDEX);
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 8; ++i) mbar_init(&freed[i], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sfull[s], 1);
+      mbar_init(&sread[s], kSoftmaxWarps / 2 + 1);
       mbar_init(&pfull[s], kSoftmaxWarps / 2 + 1);
       mbar_init(&ofull[s], 1);
     }
@@ -233,6 +236,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) tc_commit_to(&freed[0]);
       int v_at = 1, k_at = 2;  // places in the ring of V(j) and K(j + 1)
       for (int j = 0; j < n_all; ++j) {
+        if (Ly::kEarly) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (j + 1 >= (s ? n1 : n0)) continue;
+            wait(&sread[s], j);
+            __syncwarp();
+            tc_after();
+            mma_s(s, k_at);
+          }
+        }
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const int n = s ? n1 : n0;
@@ -241,8 +254,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tc_after();
           mma_o(s, v_at, j == 0);
-          if (j + 1 < n) mma_s(s, k_at);
-          else if (elect_one()) tc_commit_to(&ofull[s]);
+          if (Ly::kEarly || j + 1 == n) {
+            if (elect_one()) tc_commit_to(&ofull[s]);
+          } else {
+            mma_s(s, k_at);
+          }
         }
         if (j + 1 < n_all && elect_one()) tc_commit_to(&freed[(j + 1) & 7]);
         v_at = v_at + 2 >= Ly::kRing ? v_at + 2 - Ly::kRing : v_at + 2;
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(&drain, 0u);
       }
     } else if (warp == kSoftmaxWarps + 2 && lane == 0) {
-      // ---------------------------------------------------------------- V(j) and K(j + 1) have come: the last arrival at pfull
+      // ---------------------------------------------------------------- V(j) and K(j + 1) have come: the last arrival at pfull (sread)
       int st = 0, phase = 0;
       auto next = [&]() {
         if (++st == Ly::kRing) {
@@ -270,7 +286,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
           if (j >= tiles[s]) continue;
-          if (j > 0) wait(&pfull[s], j - 1);  // not twice in one phase
+          if (Ly::kEarly) {
+            if (j > 0) wait(&sread[s], j - 1);  // not twice in one phase
+            mbar_arrive(&sread[s]);
+          }
+          if (j > 0) wait(&pfull[s], j - 1);
           mbar_arrive(&pfull[s]);
         }
       }
@@ -321,6 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_after();
       float x[64];
       tc_ld64(at_s, x);
+      if (Ly::kEarly) {
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sread[s]);
+      }
       if (j == n - 1) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
@@ -333,7 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       top = fmaxf(top, exchange(top));  // both have read their S: P may be written over it
       const float m_new = fmaxf(m_ref, top * a.scale_log2);
       const bool move = m_new > m_ref + kRescaleLog2 || (m_ref == -INFINITY && m_new > -INFINITY);
-      // O of this sub-tile is at rest: its last P V came before the S that was waited for
+      // O of this sub-tile has to be at rest, and P be read: the last P V came before the S that was waited for, or is
+      // waited for itself
+      if (Ly::kEarly && j > 0) {
+        wait(&ofull[s], j - 1);
+        __syncwarp();
+        tc_after();
+      }
       if (j > 0 && __any_sync(0xffffffffu, move)) {
         const float f = move ? fast_exp2(m_ref - m_new) : 1.0f;
         l *= f;
@@ -370,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&pfull[s]);
     }
     if (n > 0) {
-      const bool live = wait(&ofull[s], 0) && i < len;
+      const bool live = wait(&ofull[s], Ly::kEarly ? n - 1 : 0) && i < len;
       l += exchange(l);
       __syncwarp();
       tc_after();
