@@ -163,12 +163,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](uint64_t* bar, int phase) {
     if (mbar_try_wait(bar, (uint32_t)(phase & 1))) return true;
     const uint64_t t_start = mv_globaltimer();
-    while (!mbar_try_wait(bar, (uint32_t)(phase & 1)))
-      if (s_abort || mv_globaltimer() - t_start > MV_WAIT_LIMIT_NS) {
-        s_abort = 1;
-        return false;
-      }
-    return true;
+    while (!s_abort) {
+      if (mbar_try_wait(bar, (uint32_t)(phase & 1))) return true;
+      if (mv_globaltimer() - t_start > MV_WAIT_LIMIT_NS) s_abort = 1;
+    }
+    return false;
   };
 
   if (warp >= kSoftmaxWarps) {
@@ -264,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         v_at = v_at + 2 >= Ly::kRing ? v_at + 2 - Ly::kRing : v_at + 2;
         k_at = k_at + 2 >= Ly::kRing ? k_at + 2 - Ly::kRing : k_at + 2;
       }
-      if (s_abort) {  // every product issued finishes before the CTA's memory is let go
+      if (__any_sync(0xffffffffu, s_abort)) {  // every product issued finishes before the CTA's memory is let go
         if (elect_one()) tc_commit_to(&drain);
         mbar_wait(&drain, 0u);
       }

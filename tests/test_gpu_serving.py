@@ -118,6 +118,23 @@ def test_prompt_long():
     check_prompt(q, k, v, out, lens, scale)
 
 
+@pytest.mark.parametrize("hq,hk", [(8, 8), (12, 4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_many_items(hq, hk, d):
+    """Several times more work items than SMs, of every length up to five key tiles, a NaN in one of the prompts."""
+    r = np.random.default_rng(d)
+    lens = [int(x) for x in np.concatenate([r.integers(1, 130, 40), r.integers(100, 640, 30), [0, 1, 128, 129, 640]])]
+    q, k, v, out, scale = run_prompt(lens, hq, hk, d, seed=d)
+    check_prompt(q, k, v, out, lens, scale)
+    at = sum(lens[:50]) + lens[50] // 2
+    v[at, 0, 5] = float("nan")
+    bad = torch.empty_like(out)
+    mv.prompt_attention(q, k, v, mv.PromptPlan(lens, hq // hk), scale, bad)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[at:sum(lens[:51]), : hq // hk, 5] = True
+    assert torch.equal(bad[~hit], out[~hit]) and torch.isnan(bad[hit]).all()
+
+
 def test_prompt_leaves_rows_behind_the_plan():
     lens = [130, 20]
     q, k, v, out, scale = run_prompt(lens, 2, 2, 64, extra=45)
