@@ -44,6 +44,7 @@ struct AttnArgs {
   RowsArgs q, out;
   int group, parts;  // query heads of a kv head, units of a kv head
   int short_keys;    // sequences of at most so many keys go a unit to each warp
+  int box_tiles;     // 16-key tiles of a copy: 1, 2 or 4, never over a page's end
   float scale_log2;
   unsigned int* count;  // [kMaxCtas]
   float* part;          // [CTAs][2] partial results
@@ -58,10 +59,9 @@ struct Layout {
   static constexpr int kRegion = 16 * kBox;              // bytes of one
   static constexpr int kSub = 256 / kRow;                // 16-key tiles of a warp's step: 8 KB
   static constexpr int kKeys = 16 * kSub;                // keys of a warp's step
-  static constexpr int kTile = 32 * kRow;                // bytes of 16 keys, K then V
-  static constexpr int kStage = kSub * kTile;
+  // a step: for each box of the row the regions of its kSub tiles, K, then the same of V
+  static constexpr int kV = kBoxes * kSub * kRegion, kStage = 2 * kV;
   static constexpr int kExps = kE4M3 ? 32 * kSub : 0;    // bytes of their exponents
-  static constexpr int kOps = kSub * (2 * kBoxes + (kE4M3 ? 2 : 0));  // copies of a step, one lane each
   static constexpr int kVPiece = kRow / 8 < 16 ? 8 : 16; // bytes a lane reads of a value row at once
   static constexpr int kMT = kDim / 16;                  // 16-row tiles of O^T
   static constexpr int kHeads = 8 * kNT;
@@ -72,7 +72,7 @@ struct Layout {
   static constexpr int kJoin = (8 * kMaxCtas + 8 * kThreads) * 4;
   static constexpr int kMerge = 4 * kSlot * 4 > kJoin ? 4 * kSlot * 4 : kJoin;
   static constexpr int kExpsAt = kQueue, kMergeAt = kExpsAt + kWarps * kStages * kExps, kPreAt = kMergeAt + kMerge;
-  static_assert(kStage == 8192 && kOps <= 32 && kMergeAt % 16 == 0, "");
+  static_assert(kStage == 8192 && kSub * 2 * kBoxes <= 16 && 2 * kSub <= 16 && kMergeAt % 16 == 0, "");
   static int bytes(int n_seq) { return 1024 + kPreAt + (2 * n_seq + 1) * 4; }
 };
 
@@ -91,11 +91,13 @@ MV_DEV uint32_t lds_byte(uint32_t a) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-// 16 bytes of global memory to shared memory, counted on `bar`
-MV_DEV void bulk16(uint32_t dst, const void* src, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 16, [%2];" ::"r"(dst),
-               "l"(src), "r"(smem_u32(bar))
-               : "memory");
+// 16 bytes of global memory to shared memory by this thread
+MV_DEV void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// arrives at `bar` once this thread's cp_async16 so far have come
+MV_DEV void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 template <bool kF16>
 MV_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -135,7 +137,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
-  __shared__ float s_ml[kWarps][3][8];
+  __shared__ float s_ml[kWarps][3][8];  // references of x and y, sum
+  __shared__ float s_fin[4][8];         // all warps': factor of the output, the two references, sum
   __shared__ int s_scan[kWarps];
   struct Split {
     int b, head0, n_heads, u0, n;  // u0, n: first place and steps of the unit; n = 0: none
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], kE4M3 ? 33 : 1);  // the copies' bytes, and each lane's exponents
     mbar_fence_init();
   }
   pdl_wait();
@@ -199,7 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   const int total = carry, ctas = min((int)gridDim.x, total), cta = blockIdx.x;
   if (cta >= ctas) return;
-  auto piece = [&](int c) { return (int)((int64_t)total * c / ctas); };
+  // the first `rest` pieces are one longer
+  const int each = total / ctas, rest = total - each * ctas;
+  auto piece = [&](int c) { return c * each + min(c, rest); };
   const int s_first = piece(cta), s_end = piece(cta + 1);
   // A place on the line: step `step` of the `n` of an entry, which is unit `idx` of sequence b for all warps (a step is
   // kWarps tiles in turn) or, `one`, units kWarps * idx .. of a short sequence, one for each warp.
@@ -246,17 +251,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (s_begin >= s_end) return;
   Place here = ahead;
 
-  // ---- this warp's queue. Each of the first kOps lanes does one of a step's copies: its 16-key tile u, K or V, a box of
-  // the row or the exponents. Page and tile in it are carried along: a step is kWarps * kSub tiles after the one before.
+  // ---- this warp's queue. A lane is there for one of a step's copies (its tiles from my_u on, a box of K or V; from lane
+  // 16 on: the exponents of one tile's K or V). Page and tile in it are carried along: a step is kWarps * kSub tiles after
+  // the one before. The table's entries are asked for two steps before their copies.
   const uint32_t queue = smem_u32(smem) + warp * kStages * Ly::kStage;
   const uint32_t exps = smem_u32(smem) + Ly::kExpsAt + warp * kStages * Ly::kExps;
-  const int page16 = a.c.page_size >> 4;
-  const int my_u = lane % Ly::kSub, my_op = lane / Ly::kSub;  // op: K boxes, V boxes, K and V exponents
-  const bool my_v = my_op >= 2 * Ly::kBoxes ? my_op & 1 : my_op >= Ly::kBoxes;
+  const int page16 = a.c.page_size >> 4, box_groups = Ly::kSub / a.box_tiles;
+  const bool my_exp = lane >= 16;
+  const int my_u = my_exp ? (lane - 16) >> 1 : lane % box_groups * a.box_tiles;
+  const int my_op = my_exp ? lane & 1 : lane / box_groups;  // K boxes, then V boxes
+  const bool my_v = my_exp ? my_op : my_op >= Ly::kBoxes;
+  const bool mine_any = my_exp ? kE4M3 && my_u < Ly::kSub : my_op < 2 * Ly::kBoxes;
   const int page_add = kWarps * Ly::kSub / page16, tile_add = kWarps * Ly::kSub % page16;
   const int page_one = Ly::kSub / page16, tile_one = Ly::kSub % page16;
-  int s_ahead = s_begin, page, tile, entry = 0;  // entry: the table's, of the step that is copied next
-  int key_ahead, h_ahead;                        // its first key here (past the end: nothing to do) and kv head
+  int s_ahead = s_begin, page, tile;  // of the step that is looked up next
+  int key_ahead, h_ahead;             // its first key here (past the end: nothing to do) and kv head
   bool more = true;
   auto enter_copy = [&]() {
     const int first = (ahead.one ? ahead.step : ahead.step * kWarps + warp) * Ly::kSub;
@@ -266,31 +275,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     page = (first + my_u) / page16;
     tile = first + my_u - page * page16;
   };
-  auto look_up = [&]() {
-    if (key_ahead + 16 * my_u < ahead.len) entry = __ldcg(a.c.table + (int64_t)ahead.b * a.c.ld_table + page);
-  };
   enter_copy();
-  auto copy_step = [&](int slot) {
+  struct Next {
+    int entry, row;  // this lane's page and first row in it
+    bool has, valid;
+  };
+  auto look_up = [&]() {
+    Next x = {0, 0, false, more};
     if (more) {
-      const int left = ahead.len - key_ahead;  // keys that are left from here
-      const bool has = lane < Ly::kOps && 16 * my_u < left;
-      const bool bad = has && (entry < 0 || entry >= a.c.n_pages);
-      if (bad) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)entry);
-      const uint32_t bytes = !has || bad ? 0u : (my_op >= 2 * Ly::kBoxes ? 16u : (uint32_t)Ly::kRegion);
-      const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);  // also: every lane is done with the slot
-      uint64_t* bar = &s_full[warp][slot];
-      if (lane == 0) mbar_arrive_expect_tx(bar, sum);
-      if (bytes) {
-        const int row = h_ahead * a.c.page_size + tile * 16;  // of the page
-        if (my_op >= 2 * Ly::kBoxes) {
-          const uint8_t* src = (my_v ? a.c.v_exp : a.c.k_exp) + (int64_t)entry * a.c.heads * a.c.page_size + row;
-          bulk16(exps + slot * Ly::kExps + (2 * my_u + my_v) * 16, src, bar);
-        } else {
-          const int box = my_v ? my_op - Ly::kBoxes : my_op;
-          uint8_t* dst = smem + (warp * kStages + slot) * Ly::kStage + my_u * Ly::kTile + my_op * Ly::kRegion;
-          tma_load_3d(dst, my_v ? &vmap : &kmap, bar, box * (kE4M3 ? Ly::kBox : Ly::kBox / 2), row, entry);
-        }
-      }
+      x.has = mine_any && key_ahead + 16 * my_u < ahead.len;
+      x.row = h_ahead * a.c.page_size + tile * 16;
+      if (x.has) x.entry = __ldcg(a.c.table + (int64_t)ahead.b * a.c.ld_table + page);
       ++s_ahead;
       if (++ahead.step < ahead.n) {
         more = ahead.one || s_ahead < s_end;
@@ -309,10 +304,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           enter_copy();
         }
       }
-      if (more) look_up();
     }
+    return x;
   };
-  look_up();
+  Next next = look_up(), then = look_up();
+  int copied = 0, used = 0;  // steps
+  auto copy_step = [&](int slot) {
+    if (next.valid) {
+      const bool bad = next.has && (next.entry < 0 || next.entry >= a.c.n_pages);
+      if (bad) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)next.entry);
+      const bool go = next.has && !bad;
+      const uint32_t bytes = go && !my_exp ? (uint32_t)(a.box_tiles * Ly::kRegion) : 0u;
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);  // also: every lane is done with the slot
+      uint64_t* bar = &s_full[warp][slot];
+      if (lane == 0) mbar_arrive_expect_tx(bar, sum);
+      if (bytes) {
+        const int box = my_v ? my_op - Ly::kBoxes : my_op;
+        uint8_t* dst = smem + (warp * kStages + slot) * Ly::kStage + (my_op * Ly::kSub + my_u) * Ly::kRegion;
+        tma_load_3d(dst, my_v ? &vmap : &kmap, bar, box * (kE4M3 ? Ly::kBox : Ly::kBox / 2), next.row, next.entry);
+      }
+      if (kE4M3) {
+        if (go && my_exp)
+          cp_async16(exps + slot * Ly::kExps + (lane - 16) * 16,
+                     (my_v ? a.c.v_exp : a.c.k_exp) + (int64_t)next.entry * a.c.heads * a.c.page_size + next.row);
+        cp_async_arrive(bar);
+      }
+      ++copied;
+    }
+    next = then;
+    then = look_up();
+  };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) copy_step(i);
   // where this lane reads in a 16-row region: its piece of key row g (row g + 8: + 8 rows), of value row 2 t and 2 t + 1
@@ -408,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     for (int i = 0; i < steps; ++i, key0 += key_add) {
       copy_step(slot == 0 ? kStages - 1 : slot - 1);
-      if (s + i < s_ahead && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase))) {
-        more = false;  // nothing more is copied; what is on its way is still waited for
+      if (used++ < copied && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase))) {
+        more = next.valid = then.valid = false;  // nothing more is copied; what is on its way is still waited for
         mv_set_error(a.err, kPagedAttnSite, MV_DEVERR_TIMEOUT);
       }
       const uint32_t at = queue + slot * Ly::kStage, ex_at = exps + slot * Ly::kExps;
@@ -437,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = 0; u < Ly::kSub; ++u)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            kw[u][r] = lds16(at + u * Ly::kTile + (i2 >> 1) * Ly::kRegion + (k_off ^ (i2 & 1) * 64) + r * 8 * Ly::kBox);
+            kw[u][r] = lds16(at + ((i2 >> 1) * Ly::kSub + u) * Ly::kRegion + (k_off ^ (i2 & 1) * 64) + r * 8 * Ly::kBox);
 #pragma unroll
         for (int j = 0; j < (kE4M3 ? 4 : 2); ++j)
 #pragma unroll
@@ -555,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int u = 0; u < Ly::kSub; ++u) {
         if (u > 0 && key0 + 16 * u >= len) break;
-        const uint32_t vt = at + u * Ly::kTile + Ly::kBoxes * Ly::kRegion;
+        const uint32_t vt = at + Ly::kV + u * Ly::kRegion;
         const int left = len - key0 - 16 * u;
         constexpr int kPieces = Ly::kBoxes, kWords = Ly::kVPiece / 4;
 #pragma unroll
@@ -563,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t w[4][4];  // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const uint32_t src = vt + i2 * Ly::kRegion + v_off[r & 1] + (r >> 1) * 8 * Ly::kBox;
+            const uint32_t src = vt + i2 * Ly::kSub * Ly::kRegion + v_off[r & 1] + (r >> 1) * 8 * Ly::kBox;
             if (kWords == 4) {
               const uint4 v = lds16(src);
               w[r][0] = v.x;
@@ -660,19 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s_ml[warp][2][2 * t + e] = l[n][e];
         }
       }
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][1][2 * t + e]);
-        const float f = weight(my[n][e], top);
-#pragma unroll
-        for (int m = 0; m < Ly::kMT; ++m) {
-          o[n][m][e] *= f;
-          o[n][m][2 + e] *= f;
-        }
-      }
+      // warps 4-7 leave their output, 0-3 add it to theirs, then the four sums; warp 4 meanwhile what all have in common
       float* mine = s_merge + (warp & 3) * Ly::kSlot + lane;
       if (warp >= 4) {
 #pragma unroll
@@ -682,10 +691,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncthreads();
       if (warp < 4) {
+        float f[2], f4[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][1][2 * t + e]);
+          f[e] = weight(my[n][e], top);
+          f4[e] = weight(s_ml[warp + 4][1][2 * t + e], top);
+        }
 #pragma unroll
         for (int m = 0; m < Ly::kMT; ++m)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mine[(4 * m + e) * 32] += o[n][m][e];
+          for (int e = 0; e < 4; ++e) mine[(4 * m + e) * 32] = o[n][m][e] * f[e & 1] + mine[(4 * m + e) * 32] * f4[e & 1];
+      } else if (warp == 4 && lane < 8) {
+        float tx = -INFINITY, ty = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          tx = fmaxf(tx, s_ml[w][0][lane]);
+          ty = fmaxf(ty, s_ml[w][1][lane]);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += s_ml[w][2][lane] * weight(s_ml[w][0][lane], tx);
+        s_fin[0][lane] = len > 0 ? (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum : 0.0f;
+        s_fin[1][lane] = tx;
+        s_fin[2][lane] = ty;
+        s_fin[3][lane] = sum;
       }
       __syncthreads();
       // thread: one head of the tile, 8 consecutive dims
@@ -698,17 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float* src = s_merge + ((4 * (4 * i2 + (k >> 1))) + 2 * (k & 1) + odd) * 32 + ln;
           v[k] = (src[0] + src[Ly::kSlot]) + (src[2 * Ly::kSlot] + src[3 * Ly::kSlot]);
         }
-        float tx = -INFINITY, ty = -INFINITY, sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          tx = fmaxf(tx, s_ml[w][0][hh]);
-          ty = fmaxf(ty, s_ml[w][1][hh]);
-        }
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += s_ml[w][2][hh] * weight(s_ml[w][0][hh], tx);
         if (h >= n_heads) continue;
         if (whole) {
-          const float f = len > 0 ? (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum : 0.0f;
+          const float f = s_fin[0][hh];
           if (d < a.c.dim)
             *reinterpret_cast<uint4*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)(head0 + h) * a.out.hs + d) =
                 make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
@@ -717,7 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float* dst = a.part + (int64_t)(2 * cta + part) * Ly::kPart;
           *reinterpret_cast<float4*>(dst + h * kDim + d) = make_float4(v[0], v[1], v[2], v[3]);
           *reinterpret_cast<float4*>(dst + h * kDim + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
-          if (d == 0) *reinterpret_cast<float4*>(dst + Ly::kHeads * kDim + 4 * h) = make_float4(tx, ty, sum, 0.0f);
+          if (d == 0) *reinterpret_cast<float4*>(dst + Ly::kHeads * kDim + 4 * h) =
+                make_float4(s_fin[1][hh], s_fin[2][hh], s_fin[3][hh], 0.0f);
         }
       }
       __syncthreads();
@@ -727,10 +751,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- units over several CTAs: the last one to come joins the partial results in the order of the line
   __syncthreads();
   auto cta_of = [&](int place) {  // the CTA whose piece holds a place
-    int c = (int)((int64_t)place * ctas / total);
-    while (piece(c + 1) <= place) ++c;
-    while (piece(c) > place) --c;
-    return c;
+    const int longer = rest * (each + 1);
+    return place < longer ? place / (each + 1) : rest + (place - longer) / each;
   };
   if (tid < 2) {
     bool last = false;
@@ -739,8 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c0 = cta_of(sp.u0 + kUnitCost), c1 = cta_of(sp.u0 + kUnitCost + sp.n - 1);
       __threadfence();
       last = atomicAdd(a.count + c0, 1u) == (unsigned int)(c1 - c0);
-      if (last) atomicExch(a.count + c0, 0u);
-      __threadfence();
+      if (last) {
+        atomicExch(a.count + c0, 0u);
+        __threadfence();
+      }
     }
     s_last[tid] = last;
   }
@@ -835,11 +859,13 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   const int grid = (int)std::min<int64_t>(most, std::min(mv_sm_count(), kMaxCtas));
   AttnArgs a = args;
   a.short_keys = std::min(kShortSteps, 2 * (a.c.n_seq * a.c.heads * a.parts / grid)) * Ly::kKeys;
-  // a pool as (dim, row of the page, page), boxes of 16 rows; dims behind the head's are filled with zeros
+  const int page16 = a.c.page_size / 16;
+  a.box_tiles = page16 % Ly::kSub == 0 ? Ly::kSub : Ly::kSub == 4 && page16 % 2 == 0 ? 2 : 1;
+  // a pool as (dim, row of the page, page), boxes of box_tiles * 16 rows; dims behind the head's are filled with zeros
   CUtensorMap maps[2];
   const uint64_t row = (uint64_t)a.c.dim * (kE4M3 ? 1 : 2), rows = (uint64_t)a.c.heads * a.c.page_size;
   const uint64_t dims[3] = {(uint64_t)a.c.dim, rows, (uint64_t)a.c.n_pages}, strides[2] = {row, row * rows};
-  const uint32_t box[3] = {(uint32_t)(kE4M3 ? Ly::kBox : Ly::kBox / 2), 16, 1};
+  const uint32_t box[3] = {(uint32_t)(kE4M3 ? Ly::kBox : Ly::kBox / 2), 16u * a.box_tiles, 1};
   for (int i = 0; i < 2; ++i)
     if (!mv_encode_tmap(&maps[i], kE4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                         i ? a.c.v : a.c.k, dims, strides, box,
