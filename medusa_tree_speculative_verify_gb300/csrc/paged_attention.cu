@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStages = 3;       // steps of a warp's queue
-constexpr int kUnitCost = 1;     // what a unit costs beside its steps, in steps
+constexpr int kUnitCost = 2;     // what a unit costs beside its steps, in steps (128 sequences of up to 2000 keys: 30 us, with 1: 35)
 constexpr int kShortSteps = 16;  // steps of one warp up to which a sequence may go a unit to each warp
 constexpr int kMaxCtas = 160;    // counters at the start of the workspace; CTAs of a launch
 constexpr int kChunkSeq = 1024;  // sequences of one launch
@@ -45,6 +45,10 @@ struct AttnArgs {
   int group, parts;  // query heads of a kv head, units of a kv head
   int short_keys;    // sequences of at most so many keys go a unit to each warp
   int box_tiles;     // 16-key tiles of a copy: 1, 2 or 4, never over a page's end
+  // divisions by a page's 16-key tiles, done once on the host: of a tile number n by n * page_inv >> 36; pages and tiles in
+  // them from a step to the next of all warps and of one (a division takes a hundred cycles and more of a call's start)
+  uint64_t page_inv;
+  int page_add, tile_add, page_one, tile_one, groups_log2;  // 2^groups_log2 copies for K or V's tiles of a step
   float scale_log2;
   unsigned int* count;  // [kMaxCtas]
   float* part;          // [CTAs][2] partial results
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int total = carry, ctas = min((int)gridDim.x, total), cta = blockIdx.x;
   if (cta >= ctas) return;
   // the first `rest` pieces are one longer
-  const int each = total / ctas, rest = total - each * ctas;
+  const int each = (unsigned)total / (unsigned)ctas, rest = total - each * ctas;
   auto piece = [&](int c) { return c * each + min(c, rest); };
   const int s_first = piece(cta), s_end = piece(cta + 1);
   // A place on the line: step `step` of the `n` of an entry, which is unit `idx` of sequence b for all warps (a step is
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     enter(ahead, lo);
     const int in_b = s_first - s_pre[lo], width = kUnitCost + ahead.n;
-    ahead.idx = in_b / width;
+    ahead.idx = (unsigned)in_b / (unsigned)width;
     const int at = in_b - ahead.idx * width;
     ahead.step = max(0, at - kUnitCost);
     s_begin = s_first - at + kUnitCost + ahead.step;
@@ -250,20 +254,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (s_begin >= s_end) return;
   Place here = ahead;
+  auto head_of = [&](int unit) { return a.parts == 1 ? unit : (int)((unsigned)unit / (unsigned)a.parts); };
 
   // ---- this warp's queue. A lane is there for one of a step's copies (its tiles from my_u on, a box of K or V; from lane
   // 16 on: the exponents of one tile's K or V). Page and tile in it are carried along: a step is kWarps * kSub tiles after
   // the one before. The table's entries are asked for two steps before their copies.
   const uint32_t queue = smem_u32(smem) + warp * kStages * Ly::kStage;
   const uint32_t exps = smem_u32(smem) + Ly::kExpsAt + warp * kStages * Ly::kExps;
-  const int page16 = a.c.page_size >> 4, box_groups = Ly::kSub / a.box_tiles;
+  const int page16 = a.c.page_size >> 4, box_groups = 1 << a.groups_log2;
   const bool my_exp = lane >= 16;
-  const int my_u = my_exp ? (lane - 16) >> 1 : lane % box_groups * a.box_tiles;
-  const int my_op = my_exp ? lane & 1 : lane / box_groups;  // K boxes, then V boxes
+  const int my_u = my_exp ? (lane - 16) >> 1 : (lane & (box_groups - 1)) * a.box_tiles;
+  const int my_op = my_exp ? lane & 1 : lane >> a.groups_log2;  // K boxes, then V boxes
   const bool my_v = my_exp ? my_op : my_op >= Ly::kBoxes;
   const bool mine_any = my_exp ? kE4M3 && my_u < Ly::kSub : my_op < 2 * Ly::kBoxes;
-  const int page_add = kWarps * Ly::kSub / page16, tile_add = kWarps * Ly::kSub % page16;
-  const int page_one = Ly::kSub / page16, tile_one = Ly::kSub % page16;
   int s_ahead = s_begin, page, tile;  // of the step that is looked up next
   int key_ahead, h_ahead;             // its first key here (past the end: nothing to do) and kv head
   bool more = true;
@@ -271,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int first = (ahead.one ? ahead.step : ahead.step * kWarps + warp) * Ly::kSub;
     const int unit = ahead.one ? ahead.idx * kWarps + warp : ahead.idx;
     key_ahead = unit < units ? 16 * first : ahead.len;
-    h_ahead = unit / a.parts;
-    page = (first + my_u) / page16;
+    h_ahead = head_of(unit);
+    page = (int)((uint64_t)(first + my_u) * a.page_inv >> 36);
     tile = first + my_u - page * page16;
   };
   enter_copy();
@@ -290,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++ahead.step < ahead.n) {
         more = ahead.one || s_ahead < s_end;
         key_ahead = key_ahead < ahead.len ? key_ahead + (ahead.one ? Ly::kKeys : kStepKeys) : ahead.len;
-        page += ahead.one ? page_one : page_add;
-        tile += ahead.one ? tile_one : tile_add;
+        page += ahead.one ? a.page_one : a.page_add;
+        tile += ahead.one ? a.tile_one : a.tile_add;
         if (tile >= page16) {
           tile -= page16;
           ++page;
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t q_raw[kNT][kDim / 8];
   auto load_q = [&](const Place& p) {
     constexpr int kWords = kE4M3 ? 8 : 4;  // words of Q for a piece of K
-    const int unit = p.one ? p.idx * kWarps + warp : p.idx, kh = unit / a.parts;
+    const int unit = p.one ? p.idx * kWarps + warp : p.idx, kh = head_of(unit);
     const int head0 = kh * a.group + (unit - kh * a.parts) * Ly::kHeads;
     const int n_heads = unit < units ? min(Ly::kHeads, (kh + 1) * a.group - head0) : 0;
 #pragma unroll
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b = here.b, len = here.len, nb = here.n, step0 = here.step;
     const bool one = here.one;
     const int steps = one ? nb : min(nb - step0, s_end - s);  // of this entry, here
-    const int unit = one ? here.idx * kWarps + warp : here.idx, kh = unit / a.parts;
+    const int unit = one ? here.idx * kWarps + warp : here.idx, kh = head_of(unit);
     const int head0 = kh * a.group + (unit - kh * a.parts) * Ly::kHeads;
     const int n_heads = unit < units ? min(Ly::kHeads, (kh + 1) * a.group - head0) : 0;
     // this warp's first key, and from step to step
@@ -750,9 +753,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- units over several CTAs: the last one to come joins the partial results in the order of the line
   __syncthreads();
-  auto cta_of = [&](int place) {  // the CTA whose piece holds a place
-    const int longer = rest * (each + 1);
-    return place < longer ? place / (each + 1) : rest + (place - longer) / each;
+  auto cta_of = [&](int place) {  // the CTA whose piece holds a place: guessed, and put right
+    int c = min(ctas - 1, (int)((float)place / (float)each));
+    while (piece(c) > place) --c;
+    while (piece(c + 1) <= place) ++c;
+    return c;
   };
   if (tid < 2) {
     bool last = false;
@@ -776,6 +781,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *s_w = s_merge, *s_sum = s_merge + 8 * kMaxCtas;
     auto part_of = [&](int c) { return a.part + (int64_t)(2 * c + (c == c0 && u0 > piece(c0) ? 1 : 0)) * Ly::kPart; };
     for (int n = 0; n < kNT && 8 * n < n_heads; ++n) {
+      // thread: one head, 8 dims, every kSets-th part (the first kAhead are asked for at once); then the sets
+      constexpr int kSets = kThreads / kDim, kAhead = 4;
+      const int e = tid % kDim, hh = e / (kDim / 8), d = e % (kDim / 8) * 8, first = c0 + tid / kDim;
+      float4 lo[kAhead], hi[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int c = first + i * kSets;
+        if (c <= c1 && 8 * n + hh < n_heads) {
+          const float* src = part_of(c) + (8 * n + hh) * kDim + d;
+          lo[i] = __ldcg(reinterpret_cast<const float4*>(src));
+          hi[i] = __ldcg(reinterpret_cast<const float4*>(src + 4));
+        }
+      }
       // a warp for each head: the references' maxima, the parts' weights, the sum
       const int h = 8 * n + warp;
       const float4 none = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
@@ -805,25 +823,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
       if (lane == 0) s_ml[0][0][warp] = (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum;
       __syncthreads();
-      // thread: one head, 8 dims, every kSets-th part; then the sets
-      constexpr int kSets = kThreads / kDim;
-      const int e = tid % kDim, hh = e / (kDim / 8), d = e % (kDim / 8) * 8;
       float v[8] = {};
+      auto add = [&](const float4& lo, const float4& hi, float f) {
+        v[0] += lo.x * f;
+        v[1] += lo.y * f;
+        v[2] += lo.z * f;
+        v[3] += lo.w * f;
+        v[4] += hi.x * f;
+        v[5] += hi.y * f;
+        v[6] += hi.z * f;
+        v[7] += hi.w * f;
+      };
       if (8 * n + hh < n_heads) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (first + i * kSets <= c1) add(lo[i], hi[i], s_w[hh * kMaxCtas + first + i * kSets - c0]);
 #pragma unroll 4
-        for (int c = c0 + tid / kDim; c <= c1; c += kSets) {
+        for (int c = first + kAhead * kSets; c <= c1; c += kSets) {
           const float* src = part_of(c) + (8 * n + hh) * kDim + d;
-          const float4 lo = __ldcg(reinterpret_cast<const float4*>(src));
-          const float4 hi = __ldcg(reinterpret_cast<const float4*>(src + 4));
-          const float f = s_w[hh * kMaxCtas + c - c0];
-          v[0] += lo.x * f;
-          v[1] += lo.y * f;
-          v[2] += lo.z * f;
-          v[3] += lo.w * f;
-          v[4] += hi.x * f;
-          v[5] += hi.y * f;
-          v[6] += hi.z * f;
-          v[7] += hi.w * f;
+          add(__ldcg(reinterpret_cast<const float4*>(src)), __ldcg(reinterpret_cast<const float4*>(src + 4)),
+              s_w[hh * kMaxCtas + c - c0]);
         }
       }
 #pragma unroll
@@ -861,6 +880,12 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   a.short_keys = std::min(kShortSteps, 2 * (a.c.n_seq * a.c.heads * a.parts / grid)) * Ly::kKeys;
   const int page16 = a.c.page_size / 16;
   a.box_tiles = page16 % Ly::kSub == 0 ? Ly::kSub : Ly::kSub == 4 && page16 % 2 == 0 ? 2 : 1;
+  a.groups_log2 = Ly::kSub / a.box_tiles == 4 ? 2 : Ly::kSub / a.box_tiles == 2 ? 1 : 0;
+  a.page_inv = (uint64_t(1) << 36) / page16 + 1;  // exact for tile numbers below 2^27: 2^27 * 64 < 2^36
+  a.page_add = kWarps * Ly::kSub / page16;
+  a.tile_add = kWarps * Ly::kSub % page16;
+  a.page_one = Ly::kSub / page16;
+  a.tile_one = Ly::kSub % page16;
   // a pool as (dim, row of the page, page), boxes of box_tiles * 16 rows; dims behind the head's are filled with zeros
   CUtensorMap maps[2];
   const uint64_t row = (uint64_t)a.c.dim * (kE4M3 ? 1 : 2), rows = (uint64_t)a.c.heads * a.c.page_size;
