@@ -26,6 +26,7 @@
 // short sequences takes no longer than one of a long one. A unit within one CTA is done there; one that crosses pieces leaves partial results (reference, sum, output in fp32) in the workspace, and the CTA that adds
 // the last one joins all of them in the order of the line, so the result does not depend on who comes last.
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.cuh"
 #include "paged.cuh"
@@ -38,11 +39,13 @@ constexpr int kUnitCost = 2;     // what a unit costs beside its steps, in steps
 constexpr int kShortSteps = 16;  // steps of one warp up to which a sequence may go a unit to each warp
 constexpr int kMaxCtas = 160;    // counters at the start of the workspace; CTAs of a launch
 constexpr int kChunkSeq = 1024;  // sequences of one launch
+constexpr int kClusterMost = 16;
 
 struct AttnArgs {
   PagedArgs c;
   RowsArgs q, out;
   int group, parts;  // query heads of a kv head, units of a kv head
+  int cluster;       // CTAs of a cluster
   int short_keys;    // sequences of at most so many keys go a unit to each warp
   int box_tiles;     // 16-key tiles of a copy: 1, 2 or 4, never over a page's end
   // divisions by a page's 16-key tiles, done once on the host: of a tile number n by n * page_inv >> 36; pages and tiles in
@@ -134,7 +137,8 @@ MV_DEV float ex2(float x) {
 // 2^(a - b) where both may be -inf (then the weight of nothing: 0)
 MV_DEV float weight(float a, float b) { return a == -INFINITY ? 0.0f : exp2f(a - b); }
 
-template <int kDim, bool kE4M3, int kNT>
+// kCluster: one sequence, a cluster of CTAs for each unit (see launch).
+template <int kDim, bool kE4M3, int kNT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
   using Ly = Layout<kDim, kE4M3, kNT>;
@@ -167,49 +171,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   pdl_wait();
 
-  // ---- the line: for every unit kUnitCost places that stand for its start and end, then its steps (one for an empty
-  // sequence: its zeros are written). A sequence of a bad length has none.
-  int carry = 0;
-  for (int base = 0; base < n_seq; base += kThreads) {
-    const int b = base + tid;
-    int steps = 0;
-    if (b < n_seq) {
-      int len = __ldcg(a.c.seq_lens + b);
+  int total = 0;
+  if (kCluster) {
+    if (tid == 0) {
+      const int len = __ldcg(a.c.seq_lens);
       const bool bad = len < 0 || len > a.c.max_pages * a.c.page_size;
-      if (bad && blockIdx.x == 0) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)b);
-      const bool one = len <= a.short_keys;
-      steps = bad ? 0
-                  : (kUnitCost + max(1, one ? (len + Ly::kKeys - 1) / Ly::kKeys : (len + kStepKeys - 1) / kStepKeys)) *
-                        (one ? groups : units);
-      s_len[b] = bad ? 0 : len;
+      if (bad && blockIdx.x == 0) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, 0u);
+      s_len[0] = bad ? -1 : len;
     }
-    int incl = steps;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
-    }
-    if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    int before = carry, all = carry;
+    if (s_len[0] < 0) return;  // the whole grid
+  } else {
+    // ---- the line: for every unit kUnitCost places that stand for its start and end, then its steps (one for an empty
+    // sequence: its zeros are written). A sequence of a bad length has none.
+    int carry = 0;
+    for (int base = 0; base < n_seq; base += kThreads) {
+      const int b = base + tid;
+      int steps = 0;
+      if (b < n_seq) {
+        int len = __ldcg(a.c.seq_lens + b);
+        const bool bad = len < 0 || len > a.c.max_pages * a.c.page_size;
+        if (bad && blockIdx.x == 0) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)b);
+        const bool one = len <= a.short_keys;
+        steps = bad ? 0
+                    : (kUnitCost + max(1, one ? (len + Ly::kKeys - 1) / Ly::kKeys : (len + kStepKeys - 1) / kStepKeys)) *
+                          (one ? groups : units);
+        s_len[b] = bad ? 0 : len;
+      }
+      int incl = steps;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_scan[w];
-      all += s_scan[w];
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 31) s_scan[warp] = incl;
+      __syncthreads();
+      int before = carry, all = carry;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_scan[w];
+        all += s_scan[w];
+      }
+      if (b < n_seq) s_pre[b] = before + incl - steps;
+      carry = all;
+      __syncthreads();
     }
-    if (b < n_seq) s_pre[b] = before + incl - steps;
-    carry = all;
+    if (tid == 0) s_pre[n_seq] = carry;
+    if (tid < 2) s_split[tid].n = 0;
     __syncthreads();
+    total = carry;
   }
-  if (tid == 0) s_pre[n_seq] = carry;
-  if (tid < 2) s_split[tid].n = 0;
-  __syncthreads();
-  const int total = carry, ctas = min((int)gridDim.x, total), cta = blockIdx.x;
-  if (cta >= ctas) return;
+  const int ctas = kCluster ? 1 : min((int)gridDim.x, total), cta = blockIdx.x;
+  if (!kCluster && cta >= ctas) return;
   // the first `rest` pieces are one longer
   const int each = (unsigned)total / (unsigned)ctas, rest = total - each * ctas;
   auto piece = [&](int c) { return c * each + min(c, rest); };
-  const int s_first = piece(cta), s_end = piece(cta + 1);
+  const int s_first = kCluster ? 0 : piece(cta);
+  int s_end = kCluster ? 0 : piece(cta + 1);
   // A place on the line: step `step` of the `n` of an entry, which is unit `idx` of sequence b for all warps (a step is
   // kWarps tiles in turn) or, `one`, units kWarps * idx .. of a short sequence, one for each warp.
   struct Place {
@@ -219,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto enter = [&](Place& p, int b) {
     p.b = b;
     p.len = s_len[b];
-    p.one = p.len <= a.short_keys;
+    p.one = !kCluster && p.len <= a.short_keys;
     p.n = max(1, p.one ? (p.len + Ly::kKeys - 1) / Ly::kKeys : (p.len + kStepKeys - 1) / kStepKeys);
   };
   // to the next entry, whose first place is s < total
@@ -234,7 +252,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   Place ahead;
   int s_begin;  // the first step at or after s_first that this CTA does
-  {
+  const int c_rank = kCluster ? (int)cluster_rank() : 0, c_size = kCluster ? a.cluster : 1;
+  if (kCluster) {  // an equal share of the unit's steps, possibly none; places counted from 0
+    enter(ahead, 0);
+    ahead.idx = cta / c_size;
+    ahead.step = (int)((int64_t)ahead.n * c_rank / c_size);
+    s_begin = 0;
+    s_end = (int)((int64_t)ahead.n * (c_rank + 1) / c_size) - ahead.step;
+  } else {
     int lo = 0, hi = n_seq;  // the last b with pre[b] <= s_first: one with places
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -252,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s_begin < s_end) next_entry(ahead, s_begin - kUnitCost);
     }
   }
-  if (s_begin >= s_end) return;
+  if (!kCluster && s_begin >= s_end) return;
   Place here = ahead;
   auto head_of = [&](int unit) { return a.parts == 1 ? unit : (int)((unsigned)unit / (unsigned)a.parts); };
 
@@ -269,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool mine_any = my_exp ? kE4M3 && my_u < Ly::kSub : my_op < 2 * Ly::kBoxes;
   int s_ahead = s_begin, page, tile;  // of the step that is looked up next
   int key_ahead, h_ahead;             // its first key here (past the end: nothing to do) and kv head
-  bool more = true;
+  bool more = s_begin < s_end;
   auto enter_copy = [&]() {
     const int first = (ahead.one ? ahead.step : ahead.step * kWarps + warp) * Ly::kSub;
     const int unit = ahead.one ? ahead.idx * kWarps + warp : ahead.idx;
@@ -380,8 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- unit after unit
   int s = s_begin, slot = 0, phase = 0;
+  bool once = kCluster;  // a CTA of a cluster puts its results together even where it has no step
   load_q(here);
-  while (s < s_end) {
+  while (s < s_end || once) {
+    once = false;
     const int b = here.b, len = here.len, nb = here.n, step0 = here.step;
     const bool one = here.one;
     const int steps = one ? nb : min(nb - step0, s_end - s);  // of this entry, here
@@ -641,10 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // ---- the entry's results: the warps' together, 8 heads at a time
-    const bool whole = steps == nb;
+    const bool whole = !kCluster && steps == nb;
     const int u0 = s - step0 - kUnitCost;                       // the unit's first place
     const int part = u0 <= s_first ? 0 : 1;                     // this CTA's partial result of it
-    if (!whole && tid == 0) s_split[part] = {b, head0, n_heads, u0, nb};
+    if (!kCluster && !whole && tid == 0) s_split[part] = {b, head0, n_heads, u0, nb};
     s += steps + kUnitCost;
     if (s < s_end) {  // the next entry's Q is on its way while this one's results are put together
       next_entry(here, s - kUnitCost);
@@ -740,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
                            pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
         } else {
-          float* dst = a.part + (int64_t)(2 * cta + part) * Ly::kPart;
+          float* dst = kCluster ? reinterpret_cast<float*>(smem) : a.part + (int64_t)(2 * cta + part) * Ly::kPart;
           *reinterpret_cast<float4*>(dst + h * kDim + d) = make_float4(v[0], v[1], v[2], v[3]);
           *reinterpret_cast<float4*>(dst + h * kDim + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
           if (d == 0) *reinterpret_cast<float4*>(dst + Ly::kHeads * kDim + 4 * h) =
@@ -749,6 +776,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncthreads();
     }
+  }
+
+  if (kCluster) {
+    // ---- the cluster's partial results lie where the copies went; each CTA joins some heads' dims, in the order of ranks
+    cluster_sync_all();
+    const int kh = head_of(here.idx), head0 = kh * a.group + (here.idx - kh * a.parts) * Ly::kHeads;
+    const int n_heads = min(Ly::kHeads, (kh + 1) * a.group - head0);
+    const uint32_t base = smem_u32(smem);
+    for (int e = c_rank + c_size * tid; e < Ly::kHeads * kDim / 8; e += c_size * kThreads) {
+      const int h = e / (kDim / 8), d = e % (kDim / 8) * 8;
+      if (h >= n_heads || d >= a.c.dim) continue;
+      float4 ml[kClusterMost];
+      float tx = -INFINITY, ty = -INFINITY, sum = 0.0f, v[8] = {};
+#pragma unroll
+      for (int c = 0; c < kClusterMost; ++c) {
+        if (c >= c_size) break;
+        ml[c] = ld_cluster_f4(map_rank(base + (Ly::kHeads * kDim + 4 * h) * 4, c));
+        tx = fmaxf(tx, ml[c].x);
+        ty = fmaxf(ty, ml[c].y);
+      }
+#pragma unroll
+      for (int c = 0; c < kClusterMost; ++c) {
+        if (c >= c_size) break;
+        const uint32_t src = map_rank(base + (h * kDim + d) * 4, c);
+        const float4 lo = ld_cluster_f4(src), hi = ld_cluster_f4(src + 16);
+        const float f = weight(ml[c].y, ty), x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        sum += ml[c].z * weight(ml[c].x, tx);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += x[k] * f;
+      }
+      const float f = here.len > 0 ? (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum : 0.0f;
+      *reinterpret_cast<uint4*>(a.out.p + (int64_t)(head0 + h) * a.out.hs + d) =
+          make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f), pack_bf16x2(v[4] * f, v[5] * f),
+                     pack_bf16x2(v[6] * f, v[7] * f));
+    }
+    cluster_sync_all();  // nobody leaves while its results are read
+    return;
   }
 
   // ---- units over several CTAs: the last one to come joins the partial results in the order of the line
@@ -866,18 +930,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Clusters of `size` CTAs of the kernel that the device holds at once (found once for each device and size).
+template <int kDim, bool kE4M3, int kNT>
+int most_clusters(int size, int bytes) {
+  static std::atomic<int> found[64][5];  // 0: not asked yet, else one more
+  const int dev = mv_device(), log2 = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : size == 8 ? 3 : 4;
+  if (dev < 0 || dev >= 64) return 0;
+  int n = found[dev][log2].load();
+  if (!n) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim = {(unsigned)size, 1, 1};
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, paged_attn_kernel<kDim, kE4M3, kNT, true>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    found[dev][log2].store(++n);
+  }
+  return n - 1;
+}
+
 template <int kDim, bool kE4M3, int kNT>
 mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   using Ly = Layout<kDim, kE4M3, kNT>;
-  static int flags[64] = {};
+  static int flags[64] = {}, c_flags[64] = {}, c_wide[64] = {};
   const int bytes = Ly::bytes(args.c.n_seq);
-  if (!mv_set_smem_once((const void*)paged_attn_kernel<kDim, kE4M3, kNT>, Ly::bytes(kChunkSeq), flags)) return MV_ERR_CUDA;
-  const int64_t most = (int64_t)args.c.n_seq * args.c.heads * args.parts *
-                       (((int64_t)args.c.max_pages * args.c.page_size + kWarps * Ly::kKeys - 1) / (kWarps * Ly::kKeys) + kUnitCost + kShortSteps);
+  if (!mv_set_smem_once((const void*)paged_attn_kernel<kDim, kE4M3, kNT, false>, Ly::bytes(kChunkSeq), flags))
+    return MV_ERR_CUDA;
+  const int units = args.c.heads * args.parts, sms = std::min(mv_sm_count(), kMaxCtas), step = kWarps * Ly::kKeys;
+  const int64_t most = (int64_t)args.c.n_seq * units *
+                       (((int64_t)args.c.max_pages * args.c.page_size + step - 1) / step + kUnitCost + kShortSteps);
   if (most > 0x7fffffff) return MV_ERR_SHAPE;
-  const int grid = (int)std::min<int64_t>(most, std::min(mv_sm_count(), kMaxCtas));
+  const int grid = (int)std::min<int64_t>(most, sms);
   AttnArgs a = args;
-  a.short_keys = std::min(kShortSteps, 2 * (a.c.n_seq * a.c.heads * a.parts / grid)) * Ly::kKeys;
+  // Sequences short enough for one warp to a unit: while there are units for every warp, up to kShortSteps of its steps
+  a.short_keys = std::min(kShortSteps, 2 * (a.c.n_seq * units / grid)) * Ly::kKeys;
   const int page16 = a.c.page_size / 16;
   a.box_tiles = page16 % Ly::kSub == 0 ? Ly::kSub : Ly::kSub == 4 && page16 % 2 == 0 ? 2 : 1;
   a.groups_log2 = Ly::kSub / a.box_tiles == 4 ? 2 : Ly::kSub / a.box_tiles == 2 ? 1 : 0;
@@ -896,8 +989,40 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
                         i ? a.c.v : a.c.k, dims, strides, box,
                         Ly::kBox == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
       return MV_ERR_CUDA;
+
+  // One sequence: its units are alike, and a cluster for each, joined over distributed shared memory, is sooner done than
+  // pieces of a line that are joined through the workspace (32 heads, 1027 keys: 7.9 and 10.2 us) as long as the clusters fill
+  // most of the SMs.
+  if (a.c.n_seq == 1) {
+    int size = kClusterMost;
+    while (size > 1 && units * size > sms) size /= 2;
+    const void* fn = (const void*)paged_attn_kernel<kDim, kE4M3, kNT, true>;
+    if (units * size <= sms && 4 * units * size >= 3 * sms && mv_set_smem_once(fn, Ly::bytes(1), c_flags)) {
+      const int dev = mv_device();
+      if (size > 8 && !c_wide[dev])
+        c_wide[dev] = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess ? 1 : -1;
+      if (size > 8 && c_wide[dev] < 0) cudaGetLastError();
+      if ((size <= 8 || c_wide[dev] > 0) && most_clusters<kDim, kE4M3, kNT>(size, Ly::bytes(1)) >= units) {
+        a.cluster = size;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(units * size);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Ly::bytes(1);
+        cfg.stream = stream;
+        cudaLaunchAttribute at[2];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim = {(unsigned)size, 1, 1};
+        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = mv_pdl_enabled() ? 2 : 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<kDim, kE4M3, kNT, true>, maps[0], maps[1], a);
+        return e == cudaSuccess ? mv_last_launch("paged_attention") : MV_ERR_CUDA;
+      }
+    }
+  }
   const cudaError_t e =
-      mv_launch(paged_attn_kernel<kDim, kE4M3, kNT>, dim3(grid), dim3(kThreads), bytes, stream, maps[0], maps[1], a);
+      mv_launch(paged_attn_kernel<kDim, kE4M3, kNT, false>, dim3(grid), dim3(kThreads), bytes, stream, maps[0], maps[1], a);
   return e == cudaSuccess ? mv_last_launch("paged_attention") : MV_ERR_CUDA;
 }
 

@@ -471,6 +471,22 @@ def test_paged_attention_long_and_many(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n", [0, 1, 15, 130, 1000, 2300])
+@pytest.mark.parametrize("hq,hk,d", [(32, 32, 128), (64, 8, 64), (16, 8, 128), (128, 128, 64), (64, 64, 32), (144, 9, 128)])
+def test_paged_attention_of_one_sequence(dtype, n, hq, hk, d):
+    """One sequence over one to sixteen CTAs for each unit, with fewer steps than CTAs among them."""
+    pool = Pool([n], hk, d, 48, dtype).fill(n)
+    q = normal(3, 1, hq, d)
+    out = run_paged(pool, q, d ** -0.5)
+    check_paged(pool, q, out, d ** -0.5)
+    assert n or (out == 0).all()
+    if n == 130:
+        bad = run_paged(pool, q, 0.1, lens=i32([-1]))
+        take_error(41)
+        assert (bad == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
 @pytest.mark.parametrize("scale,std", [(0.0, 1.0), (1.0, 3.0)])
 def test_paged_attention_scales(dtype, scale, std):
     pool = Pool([400, 50], 2, 64, 16, dtype).fill(1, std)
