@@ -471,6 +471,16 @@ def test_paged_attention_long_and_many(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n_seq", [1025, 2500])
+def test_paged_attention_of_more_sequences_than_a_launch_takes(dtype, n_seq):
+    lens = [int(x) for x in np.random.default_rng(n_seq).integers(0, 40, n_seq)]
+    pool = Pool(lens, 1, 32, 16, dtype).fill(1)
+    q = normal(3, n_seq, 2, 32)
+    out = run_paged(pool, q, 0.2)
+    check_paged(pool, q, out, 0.2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
 @pytest.mark.parametrize("n", [0, 1, 15, 130, 1000, 2300])
 @pytest.mark.parametrize("hq,hk,d", [(32, 32, 128), (64, 8, 64), (16, 8, 128), (128, 128, 64), (64, 64, 32), (144, 9, 128)])
 def test_paged_attention_of_one_sequence(dtype, n, hq, hk, d):
@@ -480,6 +490,14 @@ def test_paged_attention_of_one_sequence(dtype, n, hq, hk, d):
     out = run_paged(pool, q, d ** -0.5)
     check_paged(pool, q, out, d ** -0.5)
     assert n or (out == 0).all()
+    if n == 1000:                                             # captured, replayed at another length
+        ws = torch.zeros(mv.paged_attention_workspace(1, hq, hk, d), dtype=torch.uint8, device="cuda")
+        g, got, cur = torch.cuda.CUDAGraph(), torch.empty_like(q), i32([1])
+        with torch.cuda.graph(g):
+            mv.paged_attention(q, pool.cache, pool.d_table, cur, d ** -0.5, got, ws)
+        cur.fill_(n)
+        g.replay()
+        assert torch.equal(got, out)
     if n == 130:
         bad = run_paged(pool, q, 0.1, lens=i32([-1]))
         take_error(41)
@@ -581,6 +599,28 @@ def test_paged_attention_of_no_sequences():
     q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     ws = torch.zeros(mv.paged_attention_workspace(0, 4, 2, 64), dtype=torch.uint8, device="cuda")
     mv.paged_attention(q, c, i32(np.zeros((0, 3))), i32([]), 1.0, torch.empty_like(q), ws)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with a workspace each, among them both kinds of split, give what they give alone."""
+    cases = []
+    for lens, hq, hk, dtype in (([3000, 5], 8, 2, E4M3), ([2000], 32, 32, BF16), ([900] * 7, 6, 2, BF16)):
+        pool = Pool(lens, hk, 64, 16, dtype).fill(len(lens))
+        q = normal(3, len(lens), hq, 64)
+        cases.append((pool, q, run_paged(pool, q, 0.1), torch.empty_like(q), torch.zeros(
+            mv.paged_attention_workspace(len(lens), hq, hk, 64), dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+    lens = [300, 40, 500]
+    q, k, v, want, scale = run_prompt(lens, 4, 2, 64, seed=8)
+    plan, got, side = mv.PromptPlan(lens, 2), torch.empty_like(want), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for pool, x, _, out, ws, stream in cases:
+            mv.paged_attention(x, pool.cache, pool.d_table, pool.d_lens, 0.1, out, ws, stream=stream)
+        mv.prompt_attention(q, k, v, plan, scale, got, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    for _, _, alone, out, _, _ in cases:
+        assert torch.equal(out, alone)
 
 
 def test_decode_loop_captured_once_and_replayed():
