@@ -125,6 +125,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
+  pdl_trigger();
+  if (warp == kSoftmaxWarps + 1 && lane == 0) {
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
   const int4 item = a.items[blockIdx.x / a.kv_heads];
   const int kh = blockIdx.x % a.kv_heads, t0 = item.x, len = item.y;
   int block[2], head[2], tiles[2];  // row block of 128 tokens, query head, key tiles (0: no such sub-tile)
@@ -136,9 +142,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int n_tiles = max(tiles[0], tiles[1]);
 
-  if (tid == 0) {
-    mbar_init(&qfull, 1);
-    for (int i = 0; i < Ly::kRing; ++i) mbar_init(&full[i], 1);
+  auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head_outer, int h, int row) {
+#pragma unroll
+    for (int hb = 0; hb < Ly::kHalves; ++hb)
+      tma_load_3d(dst + hb * Ly::kRegion, map, bar, hb * 64, head_outer ? row : h, head_outer ? h : row);
+  };
+  auto load_tile = [&](int n, int st) {  // K(0), V(0), K(1), V(1), ...
+    mbar_arrive_expect_tx(&full[st], (uint32_t)Ly::kTile);
+    load(ring + st * Ly::kTile, n & 1 ? &vmap : &kmap, &full[st], a.head_outer & (n & 1 ? 4 : 2), kh,
+         t0 + (n >> 1) * kRows);
+  };
+  if (warp == kSoftmaxWarps + 1) {
+    // the copies start while the rest of the CTA is being set up: Q, and as many tiles as there are places
+    if (lane == 0) {
+      mbar_init(&qfull, 1);
+      for (int i = 0; i < Ly::kRing; ++i) mbar_init(&full[i], 1);
+      mbar_fence_init();
+      pdl_wait();
+      mbar_arrive_expect_tx(&qfull, (uint32_t)((tiles[1] ? 2 : 1) * Ly::kTile));
+      load(smem, &qmap, &qfull, a.head_outer & 1, head[0], t0 + block[0] * kRows);
+      load_tile(0, 0);
+      if (tiles[1]) load(smem + Ly::kTile, &qmap, &qfull, a.head_outer & 1, head[1], t0 + block[1] * kRows);
+      for (int n = 1; n < min(Ly::kRing, 2 * n_tiles); ++n) load_tile(n, n);
+    }
+    __syncwarp();
+  } else if (warp == kSoftmaxWarps) {
+    tc_alloc(&sh.tmem, kTmemCols);
+    tc_relinquish();
+  } else if (tid == 0) {
     for (int i = 0; i < 8; ++i) mbar_init(&freed[i], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sfull[s], 1);
@@ -152,15 +183,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_special = 0;
     mbar_fence_init();
   }
-  if (warp == kSoftmaxWarps) {
-    tc_alloc(&sh.tmem, kTmemCols);
-    tc_relinquish();
-  }
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = sh.tmem;
-  pdl_trigger();
   pdl_wait();
 
   // a bounded wait that also gives up once any other wait of this CTA has
@@ -178,22 +204,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSoftmaxWarps + 1 && lane == 0) {
       // ---------------------------------------------------------------- copies (one thread)
-      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head_outer, int h, int row) {
-#pragma unroll
-        for (int hb = 0; hb < Ly::kHalves; ++hb)
-          tma_load_3d(dst + hb * Ly::kRegion, map, bar, hb * 64, head_outer ? row : h, head_outer ? h : row);
-      };
-      mbar_arrive_expect_tx(&qfull, (uint32_t)((tiles[1] ? 2 : 1) * Ly::kTile));
-      load(smem, &qmap, &qfull, a.head_outer & 1, head[0], t0 + block[0] * kRows);
-      if (tiles[1]) load(smem + Ly::kTile, &qmap, &qfull, a.head_outer & 1, head[1], t0 + block[1] * kRows);
-      int n = 0;
-      for (int st = 0; n < 2 * n_tiles; ++n, st = st + 1 == Ly::kRing ? 0 : st + 1) {  // K(0), V(0), K(1), V(1), ...
+      int n = min(Ly::kRing, 2 * n_tiles);  // those are on their way
+      for (int st = 0; n < 2 * n_tiles; ++n, st = st + 1 == Ly::kRing ? 0 : st + 1) {
         // what was there: K(i) or V(i - 1), freed as the i-th (at most five are outstanding: eight barriers in turn)
         const int i = (n - Ly::kRing + 1) >> 1;
-        if (n >= Ly::kRing && !wait(&freed[i & 7], i >> 3)) break;
-        mbar_arrive_expect_tx(&full[st], (uint32_t)Ly::kTile);
-        load(ring + st * Ly::kTile, n & 1 ? &vmap : &kmap, &full[st], a.head_outer & (n & 1 ? 4 : 2), kh,
-             t0 + (n >> 1) * kRows);
+        if (!wait(&freed[i & 7], i >> 3)) break;
+        load_tile(n, st);
       }
       // every copy has landed before the CTA may leave (they have, unless a wait gave up)
       if (s_abort) mbar_wait(&qfull, 0u);
@@ -354,7 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sread[s]);
       }
-      if (j == n - 1) {
+      // the last tile: keys after the row's own are masked (warps whose rows see all of their 64 keys have nothing to do)
+      if (j == n - 1 && 64 * half + 63 > (r & ~31)) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (64 * half + c > r) x[c] = -INFINITY;
@@ -411,30 +428,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       l += sum.x + sum.y;
     }
     if (n > 0) {
-      const bool live = wait(&ofull[s], Ly::kEarly ? n - 1 : 0) && i < len;
+      wait(&ofull[s], Ly::kEarly ? n - 1 : 0);
       l += exchange(l);
       __syncwarp();
       tc_after();
+      // The row, normalised, through the sub-tile's Q (every product with it is done) so that whole rows are stored by
+      // neighbouring lanes: pieces of 16 bytes, their place within eight turned by the row.
+      constexpr int kRowBytes = 2 * kDim, kPieces = kRowBytes / 16;
+      uint8_t* stage = smem + s * Ly::kTile;
       const float inv = 1.0f / l;
-      uint16_t* row = a.out.p + (int64_t)(t0 + i) * a.out.ts + (int64_t)head[s] * a.out.hs;
       const bool special = s_special;
 #pragma unroll
       for (int c = 0; c < kDim / 64; ++c) {
         const int d0 = kDim / 2 * half + 32 * c;
         float o[32];
         tc_ld32(at_o + 32 * c, o);
-        if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if (special) add_specials(a, o, d0, t0, i, kh, block);
+        for (int e = 0; e < 32; ++e) o[e] *= inv;
+        if (special && i < len) add_specials(a, o, d0, t0, i, kh, block);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            if (d0 + e < a.dim)
-              *reinterpret_cast<uint4*>(row + d0 + e) =
-                  make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
-                             pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
-        }
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4*>(stage + r * kRowBytes + ((((d0 + e) >> 3) ^ (r & 7)) << 4)) =
+              make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
+                         pack_bf16x2(o[e + 6], o[e + 7]));
         __syncwarp();
+      }
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");  // both halves of the 32 rows are there
+      uint16_t* out = a.out.p + (int64_t)(t0 + block[s] * kRows) * a.out.ts + (int64_t)head[s] * a.out.hs;
+      const int piece = lane & (kPieces - 1), rows_left = len - block[s] * kRows;
+#pragma unroll
+      for (int e = 0; e < 16; e += 32 / kPieces) {  // 16 of them by each warp
+        const int row = (r & ~31) + 16 * half + e + lane / kPieces;
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + row * kRowBytes + ((piece ^ (row & 7)) << 4));
+        if (row < rows_left && 8 * piece < a.dim) *reinterpret_cast<uint4*>(out + (int64_t)row * a.out.ts + 8 * piece) = w;
       }
     }
   }
