@@ -3,10 +3,15 @@
 // S = Q K^T and O += P V run as tcgen05.mma with S, P and O in tensor memory, 128 query rows by 128 keys at a time. A CTA
 // takes two sub-tiles (128 tokens of one head each) of one prompt and kv head: with grouped heads two heads of the
 // same tokens, else two neighbouring row blocks, so one copy of a K and V tile serves both and the products of one run
-// while the other's softmax works. One thread owns one row: it reads the row of S, updates the running maximum, writes
-// the weights as bf16 for the second product and sums them in fp32. The reference of the exponentials moves only when
-// the row maximum has grown by more than 2^8; then the thread rescales its row of O in place. Weights are rounded to bf16
-// since both operands of a product have one type; the sums stay in fp32.
+// while the other's softmax works. Two threads own a row, 64 keys of a tile each: they read S, update the running maximum
+// together, write the weights as bf16 for the second product and sum them in fp32. The reference of the exponentials moves
+// only when the row maximum has grown by more than 2^8; then they rescale their row of O in place. Weights are rounded to
+// bf16 since both operands of a product have one type; the sums stay in fp32.
+//
+// 8192 tokens of 32 heads of 128 over 8: 318 us, 1.73 PFLOP/s; of 64: 250 us, 1.1 PFLOP/s. With 128-wide heads the products,
+// their issue and the softmax's chain (read S, maximum, exponentials, write P) bound it alike; with 64-wide ones the softmax,
+// which has as many exponentials for half the products. Short prompts (24 of up to 300 tokens, 32 heads: 21 us) are bound by
+// that chain's latency, of which an item has two or three tiles in a row.
 #include <math.h>
 
 #include <algorithm>
@@ -78,15 +83,15 @@ constexpr float kRescaleLog2 = 8.0f;  // move the exponent reference when the ro
 
 // kDim: head_dim rounded up to 64 or 128 (the copies fill the rest with zeros). Shared memory from a 1024-byte aligned
 // base: Q of both sub-tiles, then a ring of kRing tiles of 128 keys, K and V of a tile in turn; each as kDim / 64
-// regions of [128 rows][64] bf16 with the 128-byte swizzle.
+// regions of [128 rows][64] bf16 with the 128-byte swizzle. Then 2 KB for each softmax warp, through which its output goes.
 template <int kDim>
 struct Layout {
   static constexpr int kHalves = kDim / 64;
   static constexpr int kRegion = kRows * 128;
   static constexpr int kTile = kHalves * kRegion;
-  static constexpr int kRing = kDim == 128 ? 5 : 10;
+  static constexpr int kRing = kDim == 128 ? 4 : 8;
   static constexpr int kKV = 2 * kTile;
-  static constexpr int kRest = kKV + kRing * kTile;
+  static constexpr int kStage = kKV + kRing * kTile, kRest = kStage + kSoftmaxWarps * 2048;
   // Tensor memory: S of the two sub-tiles, their O, and P (bf16, two keys a column). With 128-wide heads all 512
   // columns are taken and P lies over the S that it is computed from.
   static constexpr uint32_t kColS = 0, kColO = 256;
@@ -98,14 +103,53 @@ struct Layout {
   static constexpr int kParts = kDim == 128 ? 2 : 1;
 };
 
+// Cluster launch control: asks for a block of this grid that has not started yet, which then will not start; the answer
+// (16 bytes, counted on `bar`) names it or says that there is none. After a "none" nothing more may be asked.
+MV_DEV void clc_request(uint4* answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(answer)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// blockIdx.x of the block taken over, -1 for none
+MV_DEV int clc_block(const uint4* answer) {
+  uint32_t any, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(any), "=r"(x)
+      : "r"(smem_u32(answer))
+      : "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // read before the next answer is written
+  return any ? (int)x : -1;
+}
+
+// A work item of one kv head: two sub-tiles of a prompt.
+struct Work {
+  int t0, len, kh;                  // the prompt's first token and length, kv head
+  int block[2], head[2], tiles[2];  // row block of 128 tokens, query head, key tiles (0: no such sub-tile)
+  int n;                            // key tiles of the longer one; 0: there is no more work
+};
+
 // What follows the tiles in shared memory.
 struct Rest {
-  uint64_t qfull, full[10], freed[8], sfull[2], sread[2], pfull[2][2], ofull[2], drain;
+  uint64_t qfull, qfree, full[8], freed[16], sfull[2], sread[2], pfull[2][2], ofull[2], drain;
+  uint64_t wfull[2], wempty[2], cfull;
+  uint4 cancel;   // the answer to a request for another block's work
+  Work work[2];   // the CTA's items in turn
+  int used[8];    // the event that frees each place of the ring
   uint32_t tmem;
   volatile int abort, special;
   float half[2][2][kRows];  // [sub-tile][half]: what the two threads of a row tell each other
 };
 
+// A block for each item, longest first; but a CTA that has an item's copies under way takes over the next block that has
+// not started (cluster launch control), so that the SMs stay evenly loaded and no item waits for a CTA to be set up. The
+// copying thread deals the items out; each role goes through them on its own, counting the barriers' phases on from item to
+// item: while the softmax warps write an item's output, the next one's Q, K and V come and its first S is computed.
+// With a CTA set up for each item, 8192 tokens take 336 us (320 so), 12 prompts of up to 2048 tokens 57 (50), 24 of up to
+// 300 28 (21).
 template <int kDim>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -116,72 +160,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + Ly::kKV;
   Rest& sh = *reinterpret_cast<Rest*>(smem + Ly::kRest);
-  uint64_t &qfull = sh.qfull, (&full)[10] = sh.full, (&freed)[8] = sh.freed, (&sfull)[2] = sh.sfull,
-           (&sread)[2] = sh.sread, (&pfull)[2][2] = sh.pfull, (&ofull)[2] = sh.ofull, &drain = sh.drain;
   volatile int &s_abort = sh.abort, &s_special = sh.special;
   if (smem_u32(smem) & 1023) {
     if (threadIdx.x == 0) mv_set_error(a.err, kSite, MV_DEVERR_INDEX);
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-
   pdl_trigger();
-  if (warp == kSoftmaxWarps + 1 && lane == 0) {
-    tma_prefetch_desc(&qmap);
-    tma_prefetch_desc(&kmap);
-    tma_prefetch_desc(&vmap);
-  }
-  const int4 item = a.items[blockIdx.x / a.kv_heads];
-  const int kh = blockIdx.x % a.kv_heads, t0 = item.x, len = item.y;
-  int block[2], head[2], tiles[2];  // row block of 128 tokens, query head, key tiles (0: no such sub-tile)
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    block[s] = (item.z + s) / a.group;
-    head[s] = kh * a.group + (item.z + s) % a.group;
-    tiles[s] = block[s] * kRows < len ? block[s] + 1 : 0;
-  }
-  const int n_tiles = max(tiles[0], tiles[1]);
-
-  auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head_outer, int h, int row) {
-#pragma unroll
-    for (int hb = 0; hb < Ly::kHalves; ++hb)
-      tma_load_3d(dst + hb * Ly::kRegion, map, bar, hb * 64, head_outer ? row : h, head_outer ? h : row);
-  };
-  auto load_tile = [&](int n, int st) {  // K(0), V(0), K(1), V(1), ...
-    mbar_arrive_expect_tx(&full[st], (uint32_t)Ly::kTile);
-    load(ring + st * Ly::kTile, n & 1 ? &vmap : &kmap, &full[st], a.head_outer & (n & 1 ? 4 : 2), kh,
-         t0 + (n >> 1) * kRows);
-  };
-  if (warp == kSoftmaxWarps + 1) {
-    // the copies start while the rest of the CTA is being set up: Q, and as many tiles as there are places
-    if (lane == 0) {
-      mbar_init(&qfull, 1);
-      for (int i = 0; i < Ly::kRing; ++i) mbar_init(&full[i], 1);
-      mbar_fence_init();
-      pdl_wait();
-      mbar_arrive_expect_tx(&qfull, (uint32_t)((tiles[1] ? 2 : 1) * Ly::kTile));
-      load(smem, &qmap, &qfull, a.head_outer & 1, head[0], t0 + block[0] * kRows);
-      load_tile(0, 0);
-      if (tiles[1]) load(smem + Ly::kTile, &qmap, &qfull, a.head_outer & 1, head[1], t0 + block[1] * kRows);
-      for (int n = 1; n < min(Ly::kRing, 2 * n_tiles); ++n) load_tile(n, n);
-    }
-    __syncwarp();
-  } else if (warp == kSoftmaxWarps) {
+  if (warp == kSoftmaxWarps) {
     tc_alloc(&sh.tmem, kTmemCols);
     tc_relinquish();
   } else if (tid == 0) {
-    for (int i = 0; i < 8; ++i) mbar_init(&freed[i], 1);
+    mbar_init(&sh.qfull, 1);
+    mbar_init(&sh.qfree, 1);
+    for (int i = 0; i < Ly::kRing; ++i) mbar_init(&sh.full[i], 1);
+    for (int i = 0; i < 16; ++i) mbar_init(&sh.freed[i], 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sfull[s], 1);
-      mbar_init(&sread[s], kSoftmaxWarps / 2 + 1);
-      mbar_init(&pfull[s][0], kSoftmaxWarps / 2 + 1);
-      mbar_init(&pfull[s][1], kSoftmaxWarps / 2);
-      mbar_init(&ofull[s], 1);
+      mbar_init(&sh.sfull[s], 1);
+      mbar_init(&sh.sread[s], kSoftmaxWarps / 2 + 1);
+      mbar_init(&sh.pfull[s][0], kSoftmaxWarps / 2 + 1);
+      mbar_init(&sh.pfull[s][1], kSoftmaxWarps / 2);
+      mbar_init(&sh.ofull[s], 1);
+      mbar_init(&sh.wfull[s], 1);
+      mbar_init(&sh.wempty[s], kSoftmaxWarps + 2);
     }
-    mbar_init(&drain, 1);
+    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.cfull, 1);
     s_abort = 0;
     s_special = 0;
     mbar_fence_init();
+  } else if (warp == kSoftmaxWarps + 1 && lane == 0) {
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
   }
   tc_before();
   __syncthreads();
@@ -199,32 +210,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return false;
   };
+  // The r-th item, or that there is none. The copying thread always ends the list, whatever was given up on, and within a few
+  // time limits: all roles have to see the same items (the two warps of a row meet at barriers), so this waits on
+  // regardless of the others, and counts attempts, which a CTA that is not running does not use up.
+  auto work_in = [&](int r) -> const Work* {
+    for (unsigned int i = 0; i < 1u << 30; ++i)
+      if (mbar_try_wait(&sh.wfull[r & 1], (uint32_t)((r >> 1) & 1))) return sh.work[r & 1].n ? &sh.work[r & 1] : nullptr;
+    s_abort = 1;
+    return nullptr;
+  };
 
   if (warp >= kSoftmaxWarps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSoftmaxWarps + 1 && lane == 0) {
-      // ---------------------------------------------------------------- copies (one thread)
-      int n = min(Ly::kRing, 2 * n_tiles);  // those are on their way
-      for (int st = 0; n < 2 * n_tiles; ++n, st = st + 1 == Ly::kRing ? 0 : st + 1) {
-        // what was there: K(i) or V(i - 1), freed as the i-th (at most five are outstanding: eight barriers in turn)
-        const int i = (n - Ly::kRing + 1) >> 1;
-        if (!wait(&freed[i & 7], i >> 3)) break;
-        load_tile(n, st);
+      // ---------------------------------------------------------------- items and copies (one thread)
+      // Tile g of the CTA (K(0), V(0), K(1), .. of its first item, then of the next) has place g % kRing of the ring. An item
+      // frees its tiles in n + 1 events: K(0); V(j) and K(j + 1); V(n - 1). Event e is phase e / 16 of barrier e % 16: never
+      // more than the ring's tiles are outstanding.
+      int g = 0, event = 0, r = 0, q = 0;  // tiles, events, items, copies of Q so far
+      for (int next = (int)blockIdx.x;; ++r) {
+        Work w = {};
+        if (next >= 0) {
+          const int4 item = a.items[next / a.kv_heads];
+          w.kh = next % a.kv_heads;
+          w.t0 = item.x;
+          w.len = item.y;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            w.block[s] = (item.z + s) / a.group;
+            w.head[s] = w.kh * a.group + (item.z + s) % a.group;
+            w.tiles[s] = w.block[s] * kRows < w.len ? w.block[s] + 1 : 0;
+          }
+          w.n = max(w.tiles[0], w.tiles[1]);
+        }
+        if (r >= 2) mbar_wait(&sh.wempty[r & 1], (uint32_t)(((r - 2) >> 1) & 1), 4 * MV_WAIT_LIMIT_NS);
+        sh.work[r & 1] = w;
+        mbar_arrive(&sh.wfull[r & 1]);
+        if (next < 0) break;
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head_outer, int h, int row) {
+#pragma unroll
+          for (int hb = 0; hb < Ly::kHalves; ++hb)
+            tma_load_3d(dst + hb * Ly::kRegion, map, bar, hb * 64, head_outer ? row : h, head_outer ? h : row);
+        };
+        next = -1;
+        if (r > 0 && !wait(&sh.qfree, r - 1)) continue;
+        ++q;
+        mbar_arrive_expect_tx(&sh.qfull, (uint32_t)((w.tiles[1] ? 2 : 1) * Ly::kTile));
+        load(smem, &qmap, &sh.qfull, a.head_outer & 1, w.head[0], w.t0 + w.block[0] * kRows);
+        if (w.tiles[1]) load(smem + Ly::kTile, &qmap, &sh.qfull, a.head_outer & 1, w.head[1], w.t0 + w.block[1] * kRows);
+        bool ok = true;
+        for (int m = 0; m < 2 * w.n; ++m, ++g) {
+          const int st = g & (Ly::kRing - 1);
+          if (g >= Ly::kRing && !(ok = wait(&sh.freed[sh.used[st] & 15], sh.used[st] >> 4))) break;
+          sh.used[st] = event + ((m + 1) >> 1);
+          mbar_arrive_expect_tx(&sh.full[st], (uint32_t)Ly::kTile);
+          load(ring + st * Ly::kTile, m & 1 ? &vmap : &kmap, &sh.full[st], a.head_outer & (m & 1 ? 4 : 2), w.kh,
+               w.t0 + (m >> 1) * kRows);
+        }
+        event += w.n + 1;
+        if (!ok) continue;
+        mbar_arrive_expect_tx(&sh.cfull, 16);
+        clc_request(&sh.cancel, &sh.cfull);
+        if (mbar_wait(&sh.cfull, (uint32_t)(r & 1)))
+          next = clc_block(&sh.cancel);
+        else
+          s_abort = 1;
       }
-      // every copy has landed before the CTA may leave (they have, unless a wait gave up)
-      if (s_abort) mbar_wait(&qfull, 0u);
-      for (int i = max(0, n - Ly::kRing); i < n; ++i)
-        if (!mbar_wait(&full[i % Ly::kRing], (uint32_t)((i / Ly::kRing) & 1))) break;
+      if (s_abort) {  // every copy has landed before the CTA may leave (else they have)
+        for (int i = max(0, g - Ly::kRing); i < g; ++i)
+          if (!mbar_wait(&sh.full[i & (Ly::kRing - 1)], (uint32_t)((i / Ly::kRing) & 1))) break;
+        if (q > 0) mbar_wait(&sh.qfull, (uint32_t)((q - 1) & 1));
+      }
     } else if (warp == kSoftmaxWarps) {
       // ---------------------------------------------------------------- products (one warp, an elected lane issues)
       // S_s(j) = Q_s K(j)^T, O_s += P_s(j) V(j). S of the next tile goes right behind the P V that frees its place; the
       // products of one sub-tile run while the other one's softmax works. The tensor cores take only one or two products
-      // ahead, so what this warp spends between them is lost: one wait for each sub-tile and tile (pfull: P is written and
-      // K and V have come), nothing divided, no flag carried along. (A warp for each sub-tile interleaves the two chains
-      // product by product: 550 us in place of 446 for 8192 tokens.)
+      // ahead, so what this warp spends between them is lost: few waits (pfull: P is written and K and V have come),
+      // nothing divided, no flag carried along. (A warp for each sub-tile interleaves the two chains product by product:
+      // 550 us in place of 446 for 8192 tokens.) elect_one is for whole warps: only under conditions that all lanes share.
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const int n0 = __shfl_sync(0xffffffffu, tiles[0], 0), n1 = __shfl_sync(0xffffffffu, tiles[1], 0);
-      const int n_all = max(n0, n1);
       const uint64_t q_desc = desc_kmajor(smem_u32(smem)), k_desc = desc_kmajor(smem_u32(ring)),
                      v_desc = desc_mnmajor(smem_u32(ring), (uint32_t)Ly::kRegion);
       auto mma_s = [&](int s, int at) {
@@ -234,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kDim / 16; ++i)
             tc_mma_f16(tm + Ly::kColS + 128 * s, q + (uint64_t)(i / 4 * (Ly::kRegion >> 4) + i % 4 * 2),
                        k + (uint64_t)(i / 4 * (Ly::kRegion >> 4) + i % 4 * 2), kIdS, i ? 1u : 0u);
-          tc_commit_to(&sfull[s]);
+          tc_commit_to(&sh.sfull[s]);
         }
       };
       auto mma_o = [&](int s, int at, bool first, int part) {
@@ -248,81 +312,96 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
-      wait(&qfull, 0);
-      wait(&full[0], 0);
-      __syncwarp();
-      tc_after();
-      if (n0) mma_s(0, 0);
-      if (n1) mma_s(1, 0);
-      if (elect_one()) tc_commit_to(&freed[0]);
-      int v_at = 1, k_at = 2;  // places in the ring of V(j) and K(j + 1)
-      for (int j = 0; j < n_all; ++j) {
-        if (Ly::kEarly) {
+      auto wait_for = [&](uint64_t* bar, int phase) {
+        wait(bar, phase);
+        __syncwarp();
+        tc_after();
+      };
+      int event = 0, tile = 0, c0 = 0, c1 = 0;  // next event and tile, tiles of each sub-tile in the items before
+      for (int r = 0;; ++r) {
+        const Work* w = work_in(r);
+        if (!__any_sync(0xffffffffu, w != nullptr)) break;
+        const int n0 = __shfl_sync(0xffffffffu, w->tiles[0], 0), n1 = __shfl_sync(0xffffffffu, w->tiles[1], 0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.wempty[r & 1]);
+        const int n_all = max(n0, n1);
+        wait(&sh.qfull, r);
+        wait_for(&sh.full[tile & (Ly::kRing - 1)], tile / Ly::kRing);
+        mma_s(0, tile & (Ly::kRing - 1));
+        if (n1) mma_s(1, tile & (Ly::kRing - 1));
+        if (elect_one()) {
+          tc_commit_to(&sh.freed[event & 15]);
+          if (n_all == 1) tc_commit_to(&sh.qfree);
+        }
+        for (int j = 0; j < n_all; ++j) {
+          const int v_at = (tile + 1) & (Ly::kRing - 1), k_at = (tile + 2) & (Ly::kRing - 1);
+          tile += 2;
+          ++event;
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
-            if (j + 1 >= (s ? n1 : n0)) continue;
-            wait(&sread[s], j);
-            __syncwarp();
-            tc_after();
-            mma_s(s, k_at);
+            const int n = s ? n1 : n0;
+            if (j >= n) continue;
+            if (Ly::kEarly && j + 1 < n) {
+              wait_for(&sh.sread[s], (s ? c1 : c0) + j);
+              mma_s(s, k_at);
+            }
+#pragma unroll
+            for (int part = 0; part < Ly::kParts; ++part) {
+              wait_for(&sh.pfull[s][part], (s ? c1 : c0) + j);
+              mma_o(s, v_at, j == 0, part);
+            }
+            if (Ly::kEarly || j + 1 == n) {
+              if (elect_one()) tc_commit_to(&sh.ofull[s]);
+            } else {
+              mma_s(s, k_at);
+            }
+          }
+          if (elect_one()) {
+            tc_commit_to(&sh.freed[event & 15]);
+            if (j + 2 == n_all) tc_commit_to(&sh.qfree);  // the item's last S has been issued
           }
         }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int n = s ? n1 : n0;
-          if (j >= n) continue;
-#pragma unroll
-          for (int part = 0; part < Ly::kParts; ++part) {
-            wait(&pfull[s][part], j);
-            __syncwarp();
-            tc_after();
-            mma_o(s, v_at, j == 0, part);
-          }
-          if (Ly::kEarly || j + 1 == n) {
-            if (elect_one()) tc_commit_to(&ofull[s]);
-          } else {
-            mma_s(s, k_at);
-          }
-        }
-        if (j + 1 < n_all && elect_one()) tc_commit_to(&freed[(j + 1) & 7]);
-        v_at = v_at + 2 >= Ly::kRing ? v_at + 2 - Ly::kRing : v_at + 2;
-        k_at = k_at + 2 >= Ly::kRing ? k_at + 2 - Ly::kRing : k_at + 2;
+        ++event;
+        c0 += n0;
+        c1 += n1;
       }
-      if (__any_sync(0xffffffffu, s_abort)) {  // every product issued finishes before the CTA's memory is let go
-        if (elect_one()) tc_commit_to(&drain);
-        mbar_wait(&drain, 0u);
-      }
+      // Every product issued, and with them the last commits' arrivals, are over before the CTA's memory is let go
+      if (elect_one()) tc_commit_to(&sh.drain);
+      mbar_wait(&sh.drain, 0u);
     } else if (warp == kSoftmaxWarps + 2 && lane == 0) {
       // ---------------------------------------------------------------- V(j) and K(j + 1) have come: the last arrival at pfull (sread)
-      int st = 0, phase = 0;
-      auto next = [&]() {
-        if (++st == Ly::kRing) {
-          st = 0;
-          phase ^= 1;
-        }
-      };
-      for (int j = 0; j < n_tiles; ++j) {
-        next();
-        wait(&full[st], phase);
-        if (j + 1 < n_tiles) {
-          next();
-          wait(&full[st], phase);
-        }
-        for (int s = 0; s < 2; ++s) {
-          if (j >= tiles[s]) continue;
-          if (Ly::kEarly) {
-            if (j > 0) wait(&sread[s], j - 1);  // not twice in one phase
-            mbar_arrive(&sread[s]);
+      int tile = 0, c[2] = {0, 0};
+      for (int r = 0;; ++r) {
+        const Work* w = work_in(r);
+        if (!w) break;
+        const int n[2] = {w->tiles[0], w->tiles[1]}, n_all = w->n;
+        mbar_arrive(&sh.wempty[r & 1]);
+        for (int j = 0; j < n_all; ++j) {
+          // the phases before are over: one arrival in each, and all of K that came before has been waited for
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (j >= n[s] || c[s] == 0) continue;
+            if (Ly::kEarly) wait(&sh.sread[s], c[s] - 1);
+            wait(&sh.pfull[s][0], c[s] - 1);
           }
-          if (j > 0) wait(&pfull[s][0], j - 1);
-          mbar_arrive(&pfull[s][0]);
+          ++tile;
+          wait(&sh.full[tile & (Ly::kRing - 1)], tile / Ly::kRing);
+          ++tile;
+          if (j + 1 < n_all) wait(&sh.full[tile & (Ly::kRing - 1)], tile / Ly::kRing);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (j >= n[s]) continue;
+            if (Ly::kEarly) mbar_arrive(&sh.sread[s]);
+            mbar_arrive(&sh.pfull[s][0]);
+            ++c[s];
+          }
         }
       }
     }
   } else {
     // ------------------------------------------------------------------ softmax: two threads for each query row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int s = warp >> 3, half = (warp >> 2) & 1, r = tid & (kRows - 1), n = tiles[s], i = block[s] * kRows + r;
+    const int s = warp >> 3, half = (warp >> 2) & 1, r = tid & (kRows - 1);
     const int pair = 1 + (warp & 3) + 4 * s;  // named barrier of the two warps that share rows
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t at_s = lane_base + Ly::kColS + 128 * s + 64 * half;
@@ -335,133 +414,147 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
       return sh.half[s][half ^ 1][r];
     };
-    float m_ref = -INFINITY, l = 0.0f;  // exponent reference (log2 domain, the same in both threads) and this half's sum
-    for (int j = 0; j < n; ++j) {
-      if (j == n - 1) {
-        // The last tile holds keys after this row. Their weights are zero, but zero times a NaN or an infinity in V
-        // is a NaN, so such elements become zeros here (usually there is none) and reach the rows that see them at
-        // the end. A tile is looked through by each sub-tile that ends with it; what one of them has cleared the
-        // other does not find, so the mark is the CTA's.
-        wait(&full[(2 * j + 1) % Ly::kRing], (2 * j + 1) / Ly::kRing);
-        uint4* v = reinterpret_cast<uint4*>(ring + (2 * j + 1) % Ly::kRing * Ly::kTile);
-        uint32_t any = 0;
+    int c = 0, o_phase = 0, tile = 0;  // tiles and items of this sub-tile, tiles of the ring, before this item
+    for (int round = 0;; ++round) {
+      const Work* w = work_in(round);
+      if (!__any_sync(0xffffffffu, w != nullptr)) break;
+      const int n = __shfl_sync(0xffffffffu, w->tiles[s], 0);
+      float m_ref = -INFINITY, l = 0.0f;  // exponent reference (log2 domain, the same in both threads) and this half's sum
+      for (int left = n; left > 0; --left, ++c, tile += 2) {
+        wait(&sh.sfull[s], c);
+        if (left == 1) {
+          // The last tile holds keys after this row-> Their weights are zero, but zero times a NaN or an infinity in V
+          // is a NaN, so such elements become zeros here (usually there is none) and reach the rows that see them at
+          // the end. A tile is looked through by each sub-tile that ends with it; what one of them has cleared the
+          // other does not find, so the mark is the CTA's. (Only here, behind the wait for S, is the tile's barrier at
+          // most one phase away.)
+          const int at = tile + 1;
+          wait(&sh.full[at & (Ly::kRing - 1)], at / Ly::kRing);
+          uint4* v = reinterpret_cast<uint4*>(ring + (at & (Ly::kRing - 1)) * Ly::kTile);
+          uint32_t any = 0;
 #pragma unroll 4
-        for (int e = tid & (2 * kRows - 1); e < Ly::kTile / 16; e += 2 * kRows) {
-          const uint4 w = v[e];
-          any |= special2(w.x) | special2(w.y) | special2(w.z) | special2(w.w);
-        }
-        if (any) {
-          s_special = 1;
-          __threadfence_block();
           for (int e = tid & (2 * kRows - 1); e < Ly::kTile / 16; e += 2 * kRows) {
-            const uint4 w = v[e];
-            v[e] = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+            const uint4 x = v[e];
+            any |= special2(x.x) | special2(x.y) | special2(x.z) | special2(x.w);
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (any) {
+            s_special = 1;
+            __threadfence_block();
+            for (int e = tid & (2 * kRows - 1); e < Ly::kTile / 16; e += 2 * kRows) {
+              const uint4 x = v[e];
+              v[e] = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
         }
-      }
-      wait(&sfull[s], j);
-      __syncwarp();
-      tc_after();
-      float x[64];
-      tc_ld64(at_s, x);
-      if (Ly::kEarly) {
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sread[s]);
-      }
-      // the last tile: keys after the row's own are masked (warps whose rows see all of their 64 keys have nothing to do)
-      if (j == n - 1 && 64 * half + 63 > (r & ~31)) {
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (64 * half + c > r) x[c] = -INFINITY;
-      }
-      float tops[4] = {x[0], x[1], x[2], x[3]};  // chains short enough to issue without waiting
-#pragma unroll
-      for (int c = 4; c < 64; c += 2) tops[(c >> 1) & 3] = fmaxf(tops[(c >> 1) & 3], fmaxf(x[c], x[c + 1]));
-      float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-      top = fmaxf(top, exchange(top));  // both have read their S: P may be written over it
-      const float m_new = fmaxf(m_ref, top * a.scale_log2);
-      const bool move = m_new > m_ref + kRescaleLog2 || (m_ref == -INFINITY && m_new > -INFINITY);
-      // O of this sub-tile has to be at rest, and P be read: the last P V came before the S that was waited for, or is
-      // waited for itself
-      if (Ly::kEarly && j > 0) {
-        wait(&ofull[s], j - 1);
         __syncwarp();
         tc_after();
-      }
-      if (j > 0 && __any_sync(0xffffffffu, move)) {
-        const float f = move ? fast_exp2(m_ref - m_new) : 1.0f;
-        l *= f;
-#pragma unroll 1
-        for (int c = 0; c < kDim / 2; c += 16) {  // seldom: a few registers at a time, the row of S stays in its own
-          uint32_t o[16];
-          tc_ld16u(at_o + c, o);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tc_st16u(at_o + c, o);
-        }
-      }
-      if (move) m_ref = m_new;
-      const float base = m_ref == -INFINITY ? 0.0f : m_ref;
-      const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
-      uint64_t sums[4] = {};
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t p[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 y = unpack2(fma2(pack2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), scale2, base2));
-          const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
-          sums[e & 3] = add2(sums[e & 3], pack2(p0, p1));
-          p[e] = pack_bf16x2(p0, p1);
-        }
-        tc_st16u(at_p + 16 * q, p);
-        if (Ly::kParts == 2 || q == 1) {
-          tc_wait_st();
+        float x[64];
+        tc_ld64(at_s, x);
+        if (Ly::kEarly) {
           tc_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&pfull[s][Ly::kParts == 2 ? q : 0]);
+          if (lane == 0) mbar_arrive(&sh.sread[s]);
         }
+        // the last tile: keys after the row's own are masked (warps whose rows see all of their 64 keys have nothing to do)
+        if (left == 1 && 64 * half + 63 > (r & ~31)) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (64 * half + e > r) x[e] = -INFINITY;
+        }
+        float tops[4] = {x[0], x[1], x[2], x[3]};  // chains short enough to issue without waiting
+#pragma unroll
+        for (int e = 4; e < 64; e += 2) tops[(e >> 1) & 3] = fmaxf(tops[(e >> 1) & 3], fmaxf(x[e], x[e + 1]));
+        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        top = fmaxf(top, exchange(top));  // both have read their S: P may be written over it
+        const float m_new = fmaxf(m_ref, top * a.scale_log2);
+        const bool move = m_new > m_ref + kRescaleLog2 || (m_ref == -INFINITY && m_new > -INFINITY);
+        // O of this sub-tile has to be at rest, and P be read: the last P V came before the S that was waited for, or is
+        // waited for itself
+        if (Ly::kEarly && c > 0) {
+          wait(&sh.ofull[s], c - 1);
+          __syncwarp();
+          tc_after();
+        }
+        if (__any_sync(0xffffffffu, move && m_ref > -INFINITY)) {
+          const float f = move ? fast_exp2(m_ref - m_new) : 1.0f;
+          l *= f;
+#pragma unroll 1
+          for (int e0 = 0; e0 < kDim / 2; e0 += 16) {  // seldom: a few registers at a time, the row of S stays in its own
+            uint32_t o[16];
+            tc_ld16u(at_o + e0, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tc_st16u(at_o + e0, o);
+          }
+        }
+        if (move) m_ref = m_new;
+        const float base = m_ref == -INFINITY ? 0.0f : m_ref;
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
+        uint64_t sums[4] = {};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = unpack2(fma2(pack2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]), scale2, base2));
+            const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
+            sums[e & 3] = add2(sums[e & 3], pack2(p0, p1));
+            p[e] = pack_bf16x2(p0, p1);
+          }
+          tc_st16u(at_p + 16 * q, p);
+          if (Ly::kParts == 2 || q == 1) {
+            tc_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.pfull[s][Ly::kParts == 2 ? q : 0]);
+          }
+        }
+        const float2 sum = unpack2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
+        l += sum.x + sum.y;
       }
-      const float2 sum = unpack2(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])));
-      l += sum.x + sum.y;
-    }
-    if (n > 0) {
-      wait(&ofull[s], Ly::kEarly ? n - 1 : 0);
-      l += exchange(l);
+      if (n > 0) {
+        wait(&sh.ofull[s], Ly::kEarly ? c - 1 : o_phase);
+        ++o_phase;
+        l += exchange(l);
+        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");  // the other has it: free for the next item
+        tc_after();
+        // The row, normalised, in 32 columns at a time through the warp's own 2 KB, so that whole sectors are stored by
+        // neighbouring lanes: pieces of 16 bytes, their place within four turned by the row->
+        uint8_t* stage = smem + Ly::kStage + warp * 2048;
+        const float inv = 1.0f / l;
+        const int block = w->block[s], i = block * kRows + r, len = w->len;
+        const int row0 = block * kRows + (r & ~31) + (lane >> 2), piece = lane & 3;
+        uint16_t* out = a.out.p + (int64_t)(w->t0 + row0) * a.out.ts + (int64_t)w->head[s] * a.out.hs;
+        const bool special = s_special;
+#pragma unroll
+        for (int e0 = 0; e0 < kDim / 2; e0 += 32) {
+          const int d0 = kDim / 2 * half + e0;
+          float o[32];
+          tc_ld32(at_o + e0, o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          if (special && i < len) add_specials(a, o, d0, w->t0, i, w->kh, w->block);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                           pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            const int row = e + (lane >> 2);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
+            if (row0 + e < len && d0 + 8 * piece < a.dim)
+              *reinterpret_cast<uint4*>(out + (int64_t)e * a.out.ts + d0 + 8 * piece) = x;
+          }
+          __syncwarp();
+        }
+        tc_before();  // before the next item's first P, and with it the product that writes O anew
+      }
+      tile += 2 * (w->n - n);
       __syncwarp();
-      tc_after();
-      // The row, normalised, through the sub-tile's Q (every product with it is done) so that whole rows are stored by
-      // neighbouring lanes: pieces of 16 bytes, their place within eight turned by the row.
-      constexpr int kRowBytes = 2 * kDim, kPieces = kRowBytes / 16;
-      uint8_t* stage = smem + s * Ly::kTile;
-      const float inv = 1.0f / l;
-      const bool special = s_special;
-#pragma unroll
-      for (int c = 0; c < kDim / 64; ++c) {
-        const int d0 = kDim / 2 * half + 32 * c;
-        float o[32];
-        tc_ld32(at_o + 32 * c, o);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= inv;
-        if (special && i < len) add_specials(a, o, d0, t0, i, kh, block);
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(stage + r * kRowBytes + ((((d0 + e) >> 3) ^ (r & 7)) << 4)) =
-              make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
-                         pack_bf16x2(o[e + 6], o[e + 7]));
-        __syncwarp();
-      }
-      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");  // both halves of the 32 rows are there
-      uint16_t* out = a.out.p + (int64_t)(t0 + block[s] * kRows) * a.out.ts + (int64_t)head[s] * a.out.hs;
-      const int piece = lane & (kPieces - 1), rows_left = len - block[s] * kRows;
-#pragma unroll
-      for (int e = 0; e < 16; e += 32 / kPieces) {  // 16 of them by each warp
-        const int row = (r & ~31) + 16 * half + e + lane / kPieces;
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + row * kRowBytes + ((piece ^ (row & 7)) << 4));
-        if (row < rows_left && 8 * piece < a.dim) *reinterpret_cast<uint4*>(out + (int64_t)row * a.out.ts + 8 * piece) = w;
-      }
+      if (lane == 0) mbar_arrive(&sh.wempty[round & 1]);
     }
   }
   tc_before();
@@ -474,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int kDim>
 mv_status launch(const CUtensorMap (&maps)[3], const PromptArgs& a, int64_t grid, cudaStream_t stream) {
   constexpr int kBytes = Layout<kDim>::kRest + (int)sizeof(Rest);
-  static_assert(kBytes <= 227 * 1024 && Layout<kDim>::kRing <= 10, "shared memory of one CTA");
+  static_assert(kBytes <= 227 * 1024 && Layout<kDim>::kRing <= 8, "shared memory of one CTA");
   static int flags[64] = {};
   if (!mv_set_smem_once((const void*)prompt_attn_kernel<kDim>, kBytes, flags)) return MV_ERR_CUDA;
   // the warpgroups' shares come out of the registers that the block starts with: never launch with fewer
