@@ -8,7 +8,7 @@
 // only when the row maximum has grown by more than 2^8; then they rescale their row of O in place. Weights are rounded to
 // bf16 since both operands of a product have one type; the sums stay in fp32.
 //
-// 8192 tokens of 32 heads of 128 over 8: 318 us, 1.73 PFLOP/s; of 64: 250 us, 1.1 PFLOP/s. With 128-wide heads the products,
+// 8192 tokens of 32 heads of 128 over 8: 309 us, 1.78 PFLOP/s; of 64: 250 us, 1.1 PFLOP/s. With 128-wide heads the products,
 // their issue and the softmax's chain (read S, maximum, exponentials, write P) bound it alike; with 64-wide ones the softmax,
 // which has as many exponentials for half the products. Short prompts (24 of up to 300 tokens, 32 heads: 21 us) are bound by
 // that chain's latency, of which an item has two or three tiles in a row.
@@ -420,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__any_sync(0xffffffffu, w != nullptr)) break;
       const int n = __shfl_sync(0xffffffffu, w->tiles[s], 0);
       float m_ref = -INFINITY, l = 0.0f;  // exponent reference (log2 domain, the same in both threads) and this half's sum
+      // (two tiles at a time where P shares its place with S: 316 -> 309 us for 8192 tokens; 64-wide 251 -> 261)
+#pragma unroll (Ly::kEarly ? 1 : 2)
       for (int left = n; left > 0; --left, ++c, tile += 2) {
         wait(&sh.sfull[s], c);
         if (left == 1) {
