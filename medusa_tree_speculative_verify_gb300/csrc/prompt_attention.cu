@@ -8,9 +8,9 @@
 // only when the row maximum has grown by more than 2^8; then they rescale their row of O in place. Weights are rounded to
 // bf16 since both operands of a product have one type; the sums stay in fp32.
 //
-// 8192 tokens of 32 heads of 128 over 8: 309 us, 1.78 PFLOP/s; of 64: 250 us, 1.1 PFLOP/s. With 128-wide heads the products,
+// 8192 tokens of 32 heads of 128 over 8: 308 us, 1.78 PFLOP/s; of 64: 238 us, 1.16 PFLOP/s. With 128-wide heads the products,
 // their issue and the softmax's chain (read S, maximum, exponentials, write P) bound it alike; with 64-wide ones the softmax,
-// which has as many exponentials for half the products. Short prompts (24 of up to 300 tokens, 32 heads: 21 us) are bound by
+// which has as many exponentials for half the products. Short prompts (24 of up to 300 tokens, 32 heads: 19 us) are bound by
 // that chain's latency, of which an item has two or three tiles in a row.
 #include <math.h>
 
@@ -74,11 +74,14 @@ MV_DEV void add_specials(const PromptArgs& a, float (&o)[32], int d0, int t0, in
 }
 
 // Warps 0-15: softmax, of sub-tile warp / 8 and of keys 64 (warp / 4 % 2) .. of a tile, for the rows of TMEM's lanes
-// 32 (warp % 4) ..; warp 16: products, warp 17: copies, warp 18 tells when both operands are there (19 fills up
-// the warpgroup, whose registers go to the softmax)
+// 32 (warp % 4) ..; warp 16: products, warp 17: copies, warp 18 tells when both operands are there, and looks
+// through V (19 fills up the warpgroup, whose registers go to the softmax)
 constexpr int kSoftmaxWarps = 16, kThreads = 640;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 4 * 104 + 64 <= 5 * 96, what a block of 640 threads starts with
 constexpr uint32_t kTmemCols = 512;
+// The descriptor d with its address moved on, in units of 16 bytes, within the field: one 32-bit addition (8192 tokens of
+// 64-wide heads 250 -> 238 us; what the issuing warp computes between products is lost)
+MV_DEV uint64_t desc_plus(uint64_t d, uint32_t by) { return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + by); }
 constexpr float kRescaleLog2 = 8.0f;  // move the exponent reference when the row maximum grows by more than this
 
 // kDim: head_dim rounded up to 64 or 128 (the copies fill the rest with zeros). Shared memory from a 1024-byte aligned
@@ -148,7 +151,7 @@ struct Rest {
 // not started (cluster launch control), so that the SMs stay evenly loaded and no item waits for a CTA to be set up. The
 // copying thread deals the items out; each role goes through them on its own, counting the barriers' phases on from item to
 // item: while the softmax warps write an item's output, the next one's Q, K and V come and its first S is computed.
-// With a CTA set up for each item, 8192 tokens take 336 us (320 so), 12 prompts of up to 2048 tokens 57 (50), 24 of up to
+// With a CTA set up for each item 8192 tokens took 336 us (320 so), 12 prompts of up to 2048 tokens 57 (50), 24 of up to
 // 300 28 (21).
 template <int kDim>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -292,23 +295,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q_desc = desc_kmajor(smem_u32(smem)), k_desc = desc_kmajor(smem_u32(ring)),
                      v_desc = desc_mnmajor(smem_u32(ring), (uint32_t)Ly::kRegion);
       auto mma_s = [&](int s, int at) {
-        const uint64_t q = q_desc + (uint64_t)(s * (Ly::kTile >> 4)), k = k_desc + (uint64_t)(at * (Ly::kTile >> 4));
+        const uint64_t q = desc_plus(q_desc, s * (Ly::kTile >> 4)), k = desc_plus(k_desc, at * (Ly::kTile >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < kDim / 16; ++i)
-            tc_mma_f16(tm + Ly::kColS + 128 * s, q + (uint64_t)(i / 4 * (Ly::kRegion >> 4) + i % 4 * 2),
-                       k + (uint64_t)(i / 4 * (Ly::kRegion >> 4) + i % 4 * 2), kIdS, i ? 1u : 0u);
+            tc_mma_f16(tm + Ly::kColS + 128 * s, desc_plus(q, i / 4 * (Ly::kRegion >> 4) + i % 4 * 2),
+                       desc_plus(k, i / 4 * (Ly::kRegion >> 4) + i % 4 * 2), kIdS, i ? 1u : 0u);
           tc_commit_to(&sh.sfull[s]);
         }
       };
       auto mma_o = [&](int s, int at, bool first, int part) {
-        const uint64_t v = v_desc + (uint64_t)(at * (Ly::kTile >> 4));
+        uint32_t col = tm;
+        asm volatile("" : "+r"(col));  // taken anew each time: hoisted out of the loops these operands would spill
+        const uint64_t v = desc_plus(v_desc, at * (Ly::kTile >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int e = 0; e < 8 / Ly::kParts; ++e) {  // 16 keys each
             const int i = Ly::kParts == 1 ? e : (e & 1) + 4 * (e >> 1) + 2 * part;
-            tc_mma_f16_ta(tm + Ly::kColO + kDim * s, tm + Ly::kColP + Ly::kPStep * s + 8 * i,
-                          v + (uint64_t)(i * (16 * 128 >> 4)), kIdO, first && i == 0 ? 0u : 1u);
+            tc_mma_f16_ta(col + Ly::kColO + kDim * s, col + Ly::kColP + Ly::kPStep * s + 8 * i,
+                          desc_plus(v, i * (16 * 128 >> 4)), kIdO, first && i == 0 ? 0u : 1u);
           }
         }
       };
@@ -368,14 +373,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Every product issued, and with them the last commits' arrivals, are over before the CTA's memory is let go
       if (elect_one()) tc_commit_to(&sh.drain);
       mbar_wait(&sh.drain, 0u);
-    } else if (warp == kSoftmaxWarps + 2 && lane == 0) {
+    } else if (warp == kSoftmaxWarps + 2) {
       // ---------------------------------------------------------------- V(j) and K(j + 1) have come: the last arrival at pfull (sread)
+      // The last tile of a sub-tile holds keys after its rows. Their weights are zero, but zero times a NaN or an infinity
+      // in V is a NaN, so such elements become zeros here (usually there is none), before any product of that tile, and
+      // reach the rows that see them at the end. (One look for both sub-tiles, while their S is computed: by the softmax
+      // warps themselves, behind the wait for S, 12 prompts of up to 2048 tokens take 51 us, 47 so.)
       int tile = 0, c[2] = {0, 0};
       for (int r = 0;; ++r) {
         const Work* w = work_in(r);
-        if (!w) break;
-        const int n[2] = {w->tiles[0], w->tiles[1]}, n_all = w->n;
-        mbar_arrive(&sh.wempty[r & 1]);
+        if (!__any_sync(0xffffffffu, w != nullptr)) break;
+        const int n[2] = {__shfl_sync(0xffffffffu, w->tiles[0], 0), __shfl_sync(0xffffffffu, w->tiles[1], 0)};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.wempty[r & 1]);
+        const int n_all = max(n[0], n[1]);
         for (int j = 0; j < n_all; ++j) {
           // the phases before are over: one arrival in each, and all of K that came before has been waited for
 #pragma unroll
@@ -384,15 +395,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (Ly::kEarly) wait(&sh.sread[s], c[s] - 1);
             wait(&sh.pfull[s][0], c[s] - 1);
           }
-          ++tile;
-          wait(&sh.full[tile & (Ly::kRing - 1)], tile / Ly::kRing);
-          ++tile;
+          const int at = tile + 1;
+          tile += 2;
+          wait(&sh.full[at & (Ly::kRing - 1)], at / Ly::kRing);
+          if (j + 1 == n[0] || j + 1 == n[1]) {
+            uint4* v = reinterpret_cast<uint4*>(ring + (at & (Ly::kRing - 1)) * Ly::kTile);
+            uint32_t any = 0;
+#pragma unroll 8
+            for (int e = lane; e < Ly::kTile / 16; e += 32) {
+              const uint4 x = v[e];
+              any |= special2(x.x) | special2(x.y) | special2(x.z) | special2(x.w);
+            }
+            if (any) {
+              s_special = 1;
+              for (int e = lane; e < Ly::kTile / 16; e += 32) {
+                const uint4 x = v[e];
+                v[e] = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+          }
           if (j + 1 < n_all) wait(&sh.full[tile & (Ly::kRing - 1)], tile / Ly::kRing);
+          __syncwarp();
 #pragma unroll
           for (int s = 0; s < 2; ++s) {
             if (j >= n[s]) continue;
-            if (Ly::kEarly) mbar_arrive(&sh.sread[s]);
-            mbar_arrive(&sh.pfull[s][0]);
+            if (Ly::kEarly && lane == 0) mbar_arrive(&sh.sread[s]);
+            if (lane == 0) mbar_arrive(&sh.pfull[s][0]);
             ++c[s];
           }
         }
@@ -414,41 +443,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
       return sh.half[s][half ^ 1][r];
     };
-    int c = 0, o_phase = 0, tile = 0;  // tiles and items of this sub-tile, tiles of the ring, before this item
+    int c = 0, o_phase = 0;  // tiles and items of this sub-tile so far
     for (int round = 0;; ++round) {
       const Work* w = work_in(round);
       if (!__any_sync(0xffffffffu, w != nullptr)) break;
       const int n = __shfl_sync(0xffffffffu, w->tiles[s], 0);
       float m_ref = -INFINITY, l = 0.0f;  // exponent reference (log2 domain, the same in both threads) and this half's sum
-      // (two tiles at a time where P shares its place with S: 316 -> 309 us for 8192 tokens; 64-wide 251 -> 261)
-#pragma unroll (Ly::kEarly ? 1 : 2)
-      for (int left = n; left > 0; --left, ++c, tile += 2) {
+      for (int left = n; left > 0; --left, ++c) {
         wait(&sh.sfull[s], c);
-        if (left == 1) {
-          // The last tile holds keys after this row-> Their weights are zero, but zero times a NaN or an infinity in V
-          // is a NaN, so such elements become zeros here (usually there is none) and reach the rows that see them at
-          // the end. A tile is looked through by each sub-tile that ends with it; what one of them has cleared the
-          // other does not find, so the mark is the CTA's. (Only here, behind the wait for S, is the tile's barrier at
-          // most one phase away.)
-          const int at = tile + 1;
-          wait(&sh.full[at & (Ly::kRing - 1)], at / Ly::kRing);
-          uint4* v = reinterpret_cast<uint4*>(ring + (at & (Ly::kRing - 1)) * Ly::kTile);
-          uint32_t any = 0;
-#pragma unroll 4
-          for (int e = tid & (2 * kRows - 1); e < Ly::kTile / 16; e += 2 * kRows) {
-            const uint4 x = v[e];
-            any |= special2(x.x) | special2(x.y) | special2(x.z) | special2(x.w);
-          }
-          if (any) {
-            s_special = 1;
-            __threadfence_block();
-            for (int e = tid & (2 * kRows - 1); e < Ly::kTile / 16; e += 2 * kRows) {
-              const uint4 x = v[e];
-              v[e] = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          }
-        }
         __syncwarp();
         tc_after();
         float x[64];
@@ -554,7 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_before();  // before the next item's first P, and with it the product that writes O anew
       }
-      tile += 2 * (w->n - n);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.wempty[round & 1]);
     }
