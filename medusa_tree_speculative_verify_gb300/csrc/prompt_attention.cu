@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");  // the other has it: free for the next item
         tc_after();
         // The row, normalised, in 32 columns at a time through the warp's own 2 KB, so that whole sectors are stored by
-        // neighbouring lanes: pieces of 16 bytes, their place within four turned by the row->
+        // neighbouring lanes: pieces of 16 bytes, their place within four turned by the row.
         uint8_t* stage = smem + Ly::kStage + warp * 2048;
         const float inv = 1.0f / l;
         const int block = w->block[s], i = block * kRows + r, len = w->len;
