@@ -135,6 +135,31 @@ def test_prompt_many_items(hq, hk, d):
     assert torch.equal(bad[~hit], out[~hit]) and torch.isnan(bad[hit]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompts_of_many_items_at_once(d):
+    """Calls that each fill the GPU several times over, on streams of both priorities and replayed from a graph beside them,
+    give what each gives alone: a CTA takes over further items of its own call only, each item once."""
+    cases = []
+    for seed, (n, most, hq, hk) in enumerate([(60, 400, 8, 8), (9, 2000, 8, 2), (150, 130, 12, 4)]):
+        lens = [int(x) for x in np.random.default_rng(seed).integers(1, most, n)]
+        q, k, v, want, scale = run_prompt(lens, hq, hk, d, seed=seed)
+        plan = mv.PromptPlan(lens, hq // hk)
+        cases.append((q, k, v, plan, scale, want, torch.empty_like(want), torch.cuda.Stream(priority=-(seed % 2))))
+    g, graphed = torch.cuda.CUDAGraph(), torch.zeros_like(cases[0][5])
+    with torch.cuda.graph(g):
+        for _ in range(2):
+            mv.prompt_attention(*cases[0][:5], graphed)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for q, k, v, plan, scale, _, out, stream in cases:
+            mv.prompt_attention(q, k, v, plan, scale, out, stream=stream)
+        g.replay()
+    torch.cuda.synchronize()
+    for *_, want, out, _ in cases:
+        assert torch.equal(out, want)
+    assert torch.equal(graphed, cases[0][5])
+
+
 def test_prompt_leaves_rows_behind_the_plan():
     lens = [130, 20]
     q, k, v, out, scale = run_prompt(lens, 2, 2, 64, extra=45)
