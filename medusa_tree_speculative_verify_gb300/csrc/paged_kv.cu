@@ -1,7 +1,6 @@
 // Rows of keys and values written into a paged cache, and read back.
 //
-// A row is one token's head_dim values of one kv head. A group of kLanes threads moves one row, 16 bytes of the
-// pool a thread. Writing e4m3: the group's largest |x| gives the exponent e, the smallest with max|x| <=
+// A row is one token's head_dim values of one kv head. A group of kLanes threads moves one row, 16 elements a thread. Writing e4m3: the group's largest |x| gives the exponent e, the smallest with max|x| <=
 // 448 * 2^e: with max|x| = 1.m * 2^(E-127), 448 = 1.75 * 2^8, that is e = E - 135, one more when 1.m > 1.75. The
 // product with 2^-e is exact (short of underflow), so the row is rounded once, by the conversion, and what it stands
 // for is exact in bf16 again.
@@ -25,8 +24,34 @@ struct MoveArgs {
   RowsArgs k, v;
   const int32_t* cu;
   int n_rows, tokens, look_lanes;  // tokens of a CTA, threads that look one of them up
+  bool wide;                       // all bf16 rows start on a multiple of 32 bytes
   unsigned int* err;
 };
+
+// 32 bytes at once where they start on a multiple of 32: whole sectors, which two halves in turn ask for twice (e4m3 rows of
+// 38 k tokens x 8 heads read 46.8 -> 41.0 us, 8294 tokens written and read back 27.6 -> 24.5)
+MV_DEV void load32(const uint8_t* p, uint32_t (&x)[8], bool wide) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                 : "l"(p));
+    return;
+  }
+  const uint4 lo = reinterpret_cast<const uint4*>(p)[0], hi = reinterpret_cast<const uint4*>(p)[1];
+  const uint32_t both[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = both[j];
+}
+MV_DEV void store32(uint8_t* p, const uint32_t (&x)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "l"(p)
+                 : "memory");
+    return;
+  }
+  reinterpret_cast<uint4*>(p)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<uint4*>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+}
 
 // Where token t of the packed rows lies: page and slot; page -1 for a row behind the last sequence, -2 when the table,
 // the lengths or cu are out of range. By n = 2^k consecutive lanes, which narrow the sequences down to an n-th at a time.
@@ -56,11 +81,11 @@ MV_DEV int2 place_of(const MoveArgs& a, int t, int n) {
 // kLanes threads a row, the power of two from dim / kEl up
 template <bool kE4M3, bool kWrite, int kLanes>
 __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const MoveArgs a) {
-  constexpr int kEl = kE4M3 ? 16 : 8;              // elements of a thread
-  // Rows on their way, K and V in turn: 64 to 96 bytes a thread, what its registers hold (bf16 with four: 31 against 26.6 us
-  // for 8294 tokens x 8 heads written and read back; e4m3 written with four, read with six: 29.5 against 27.8)
-  constexpr int kAhead = !kE4M3 ? 6 : kWrite ? 2 : 4;
-  constexpr int kWords = kE4M3 && kWrite ? 8 : 4;
+  constexpr int kEl = 16;  // elements of a thread
+  // Rows on their way, K and V in turn: as many as a thread's registers hold (8294 tokens x 8 heads written and read back:
+  // bf16 with two 35 us, with four 26; e4m3 written with four 29, with two 28)
+  constexpr int kAhead = kE4M3 && kWrite ? 2 : 4;
+  constexpr int kWords = kE4M3 && !kWrite ? 4 : 8;
   __shared__ int2 s_place[kTokens];
   pdl_trigger();
   pdl_wait();
@@ -108,14 +133,15 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
           uint8_t* held = (is_v ? a.c.v : a.c.k) + held_at;
           to[i + is_v] = kWrite ? held : row;
           if (kE4M3) exp[i + is_v] = (is_v ? a.c.v_exp : a.c.k_exp) + prow;
-          const uint4* from = reinterpret_cast<const uint4*>(kWrite ? row : held);
-#pragma unroll
-          for (int j = 0; j < kWords / 4; ++j) {
-            const uint4 w = from[j];
-            x[i + is_v][4 * j] = w.x;
-            x[i + is_v][4 * j + 1] = w.y;
-            x[i + is_v][4 * j + 2] = w.z;
-            x[i + is_v][4 * j + 3] = w.w;
+          const uint8_t* from = kWrite ? row : held;
+          if constexpr (kWords == 8) {
+            load32(from, x[i + is_v], a.wide);
+          } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(from);
+            x[i + is_v][0] = w.x;
+            x[i + is_v][1] = w.y;
+            x[i + is_v][2] = w.z;
+            x[i + is_v][3] = w.w;
           }
           if (kE4M3 && !kWrite) byte[i + is_v] = *exp[i + is_v];
         }
@@ -130,7 +156,9 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (!kE4M3) {
-        if (to[i]) *reinterpret_cast<uint4*>(to[i]) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+        if constexpr (kWords == 8) {
+          if (to[i]) store32(to[i], x[i], a.wide);
+        }
       } else if (kWrite) {
         float f[16], top = 0.0f;
 #pragma unroll
@@ -163,8 +191,7 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
           const float2 f = half2_to_float2(e4m3x2_to_half2((uint16_t)(x[i][j >> 1] >> (16 * (j & 1)))));
           o[j] = pack_bf16x2(f.x * s, f.y * s);
         }
-        reinterpret_cast<uint4*>(to[i])[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<uint4*>(to[i])[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        store32(to[i], o, a.wide);
       }
     }
   }
@@ -172,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
 
 template <bool kE4M3, bool kWrite>
 cudaError_t launch_rows(const MoveArgs& a, dim3 grid, cudaStream_t st) {
-  constexpr int kMost = kE4M3 ? 8 : 16;
+  constexpr int kMost = 8;
   if (a.c.dim > 64) return mv_launch(paged_rows_kernel<kE4M3, kWrite, kMost>, grid, dim3(kThreads), 0, st, a);
   if (a.c.dim > 32) return mv_launch(paged_rows_kernel<kE4M3, kWrite, kMost / 2>, grid, dim3(kThreads), 0, st, a);
   return mv_launch(paged_rows_kernel<kE4M3, kWrite, kMost / 4>, grid, dim3(kThreads), 0, st, a);
@@ -193,6 +220,12 @@ mv_status move_rows(const mv_rows& k, const mv_rows& v, int32_t n_rows, const in
   a.k = {static_cast<uint16_t*>(k.ptr), k.token_stride, k.head_stride};
   a.v = {static_cast<uint16_t*>(v.ptr), v.token_stride, v.head_stride};
   a.cu = cu;
+  const auto whole = [](const mv_rows& r) {
+    return !((reinterpret_cast<uintptr_t>(r.ptr) | (uint64_t)r.token_stride * 2 | (uint64_t)r.head_stride * 2) & 31);
+  };
+  a.wide = whole(k) && whole(v) &&
+           (cache->dtype == MV_DTYPE_E4M3 ||
+            !((reinterpret_cast<uintptr_t>(cache->k) | reinterpret_cast<uintptr_t>(cache->v)) & 31));
   a.n_rows = n_rows;
   // whole waves of CTAs with as many tokens each as share one round of lookups, which nothing hides
   // (reads at most 16: they do better with more and smaller ones, 46 against 51 us for 234 MB; writes do not, 90 and 85 us

@@ -381,6 +381,51 @@ def test_rows_with_strides_into_a_session_layout(dtype):
         assert np.array_equal(f64(y), want)
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("d", [16, 48, 64, 80, 128])
+@pytest.mark.parametrize("off", ["k", "v", "heads", "tokens", "pool"])
+def test_rows_on_any_multiple_of_16_bytes(dtype, d, off):
+    """Rows of the caller's or of the pool that start on odd multiples of 16 bytes move like those on multiples of 32."""
+    lens, hk, page = [37, 1, 70], 3, 16
+    n, cu = sum(lens), i32(np.cumsum([0] + lens))
+    aligned = Pool(lens, hk, d, page, dtype, seed=d)
+    k, v = normal(1, n, hk, d), normal(2, n, hk, d)
+    mv.paged_kv_append(k, v, cu, aligned.cache, aligned.d_table, aligned.d_lens)
+
+    def rows(which):
+        """[n, hk, d] in memory filled with 7, moved by 8 elements where asked"""
+        skip, gap_h, gap_t = 8 * (off == which), 8 * (off == "heads"), 8 * (off == "tokens")
+        ts = hk * (d + gap_h) + gap_t
+        flat = torch.full((skip + n * ts,), 7.0, dtype=torch.bfloat16, device="cuda")
+        return flat, flat.as_strided((n, hk, d), (ts, d + gap_h, 1), skip)
+
+    pool = Pool(lens, hk, d, page, dtype, seed=d)
+    c = pool.cache
+    if off == "pool":
+        def moved(x):
+            by = 16 // x.element_size()
+            return torch.zeros(x.numel() + by, dtype=torch.uint8 if dtype == E4M3 else x.dtype,
+                               device="cuda").view(x.dtype)[by:].view(x.shape)
+        c = mv.PagedKV(moved(c.k), moved(c.v), c.k_exp, c.v_exp)
+        pool.cache = c
+    (_, k1), (_, v1) = rows("k"), rows("v")
+    k1.copy_(k)
+    v1.copy_(v)
+    mv.paged_kv_append(k1, v1, cu, c, pool.d_table, pool.d_lens)
+    assert same_bits(pool.bits(), aligned.bits())
+    (fk, ko), (fv, vo) = rows("k"), rows("v")
+    want = [torch.empty_like(k) for _ in range(2)]
+    mv.paged_kv_read(aligned.cache, aligned.d_table, aligned.d_lens, cu, *want)
+    mv.paged_kv_read(c, pool.d_table, pool.d_lens, cu, ko, vo)
+    torch.cuda.synchronize()
+    for x, src, flat, got in ((want[0], k, fk, ko), (want[1], v, fv, vo)):
+        assert torch.equal(got, x)
+        ref = f64(src) if dtype == BF16 else serving.stored_value(*serving.quantise(f64(src)))
+        assert np.array_equal(f64(x), ref)
+        got.fill_(7.0)
+        assert (flat == 7.0).all()                            # nothing between the rows
+
+
 def take_error(site):
     st, code = mv.get_error()
     assert st == 6 and code >> 16 == site and code & 0xffff == 2
