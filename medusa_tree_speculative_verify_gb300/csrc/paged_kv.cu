@@ -227,10 +227,13 @@ mv_status move_rows(const mv_rows& k, const mv_rows& v, int32_t n_rows, const in
            (cache->dtype == MV_DTYPE_E4M3 ||
             !((reinterpret_cast<uintptr_t>(cache->k) | reinterpret_cast<uintptr_t>(cache->v)) & 31));
   a.n_rows = n_rows;
-  // whole waves of CTAs with as many tokens each as share one round of lookups, which nothing hides
-  // (reads at most 16: they do better with more and smaller ones, 46 against 51 us for 234 MB; writes do not, 90 and 85 us
-  // for 340 MB)
-  const int64_t ctas = kResident * mv_sm_count(), most = kWrite ? kTokens : 16;
+  // Whole waves of CTAs with as many tokens each as share one round of lookups, which nothing hides. Reads do better with
+  // more and smaller CTAs (38 k tokens x 8 heads of 128: 41 us with up to 16, 43 with up to 32; x 32 heads: 142 with up to 8,
+  // 147 with up to 16), down to two rounds of copies for each thread (23 k tokens x 4 heads of 64: 10 us with up to 64, 20
+  // with up to 16). Writes do not (120 prompts 78 us with up to 64, 83 with up to 16).
+  const int groups = kThreads / (a.c.dim > 64 ? 8 : a.c.dim > 32 ? 4 : 2);
+  const int64_t ctas = kResident * mv_sm_count();
+  const int64_t most = kWrite ? kTokens : std::max(8, std::min(kTokens, 4 * groups / a.c.heads));
   const int64_t waves = (n_rows + ctas * most - 1) / (ctas * most);
   a.tokens = (int)((n_rows + ctas * waves - 1) / (ctas * waves));
   a.look_lanes = 16;
