@@ -52,7 +52,7 @@ MV_DEV uint32_t finite2(uint32_t w) {
 }
 
 // Adds to o (elements d0 .. d0 + 31 of query row i) the NaNs and infinities of V that the row sees in the last key
-// tiles of the CTA's two sub-tiles. Added once more they change nothing, so it does not matter which of them the
+// tiles of the item's two sub-tiles. Added once more they change nothing, so it does not matter which of them the
 // products have met already.
 MV_DEV void add_specials(const PromptArgs& a, float (&o)[32], int d0, int t0, int i, int kh, const int (&block)[2]) {
   for (int s = 0; s < 2; ++s)
@@ -79,9 +79,11 @@ MV_DEV void add_specials(const PromptArgs& a, float (&o)[32], int d0, int t0, in
 constexpr int kSoftmaxWarps = 16, kThreads = 640;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 4 * 104 + 64 <= 5 * 96, what a block of 640 threads starts with
 constexpr uint32_t kTmemCols = 512;
+
 // The descriptor d with its address moved on, in units of 16 bytes, within the field: one 32-bit addition (8192 tokens of
 // 64-wide heads 250 -> 238 us; what the issuing warp computes between products is lost)
 MV_DEV uint64_t desc_plus(uint64_t d, uint32_t by) { return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + by); }
+
 constexpr float kRescaleLog2 = 8.0f;  // move the exponent reference when the row maximum grows by more than this
 
 // kDim: head_dim rounded up to 64 or 128 (the copies fill the rest with zeros). Shared memory from a 1024-byte aligned

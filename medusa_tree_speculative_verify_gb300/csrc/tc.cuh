@@ -160,9 +160,9 @@ MV_DEV uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// One lane of a converged warp (all 32 lanes have to come here, or none goes on). The instructions of tcgen05 take their operands from uniform registers: where a whole warp
-// computes them and one elected lane issues, they stay there; under a branch on a lane number each is moved there again
-// for every instruction, about 100 cycles a product.
+// One lane of a converged warp (all 32 lanes have to come here, or none goes on). The instructions of tcgen05 take their
+// operands from uniform registers: where a whole warp computes them and one elected lane issues, they stay there; under a
+// branch on a lane number each is moved there again for every instruction, about 100 cycles a product.
 MV_DEV bool elect_one() {
   uint32_t one;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
