@@ -38,6 +38,7 @@ constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStages = 3;       // steps of a warp's queue
 constexpr int kUnitCost = 2;     // what a unit costs beside its steps, in steps (128 sequences of up to 2000 keys: 30 us, with 1: 35)
 constexpr int kShortSteps = 16;  // steps of one warp up to which a sequence may go a unit to each warp
+constexpr unsigned int kEvenMost = 20;  // places of a piece up to which all have one length
 constexpr int kMaxCtas = 160;    // counters at the start of the workspace; CTAs of a launch
 constexpr int kChunkSeq = 1024;  // sequences of one launch
 constexpr int kClusterMost = 16;
@@ -222,11 +223,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     total = carry;
   }
-  const int ctas = kCluster ? 1 : min((int)gridDim.x, total), cta = blockIdx.x;
+  // Pieces of one length, the least that the grid can do them in: with the places spread over all CTAs none would be done
+  // sooner, and units would have more parts (12 sequences of up to 38 k keys, 16 heads of one kv head: 17 us, spread 21; 4 of
+  // 2000, 8 kv heads: 12 and 14.5). Long pieces are spread, the first `rest` of them one longer: there the last few SMs count
+  // for their bandwidth (64 sequences of up to 8191 keys, 33 places a piece: 38.7 us, of one length 39.9).
+  const unsigned int all = (unsigned)total, least = (all + gridDim.x - 1) / gridDim.x;
+  const bool even = least <= kEvenMost;
+  const int each = kCluster ? 1 : max(1, (int)(even ? least : all / gridDim.x)), rest = even ? 0 : total - each * (int)gridDim.x;
+  const int ctas = kCluster ? 1 : even ? (int)((all + each - 1) / (unsigned)each) : (int)gridDim.x, cta = blockIdx.x;
   if (!kCluster && cta >= ctas) return;
-  // the first `rest` pieces are one longer
-  const int each = (unsigned)total / (unsigned)ctas, rest = total - each * ctas;
-  auto piece = [&](int c) { return c * each + min(c, rest); };
+  auto piece = [&](int c) { return (int)min((unsigned)c * (unsigned)each + min(c, rest), all); };
   const int s_first = kCluster ? 0 : piece(cta);
   int s_end = kCluster ? 0 : piece(cta + 1);
   // A place on the line: step `step` of the `n` of an entry, which is unit `idx` of sequence b for all warps (a step is
@@ -819,9 +825,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- units over several CTAs: the last one to come joins the partial results in the order of the line
   __syncthreads();
   auto cta_of = [&](int place) {  // the CTA whose piece holds a place: guessed, and put right
-    int c = min(ctas - 1, (int)((float)place / (float)each));
+    int c = min(ctas - 1, (int)((unsigned)place / (unsigned)each));
     while (piece(c) > place) --c;
-    while (piece(c + 1) <= place) ++c;
     return c;
   };
   if (tid < 2) {
