@@ -106,6 +106,7 @@ struct Layout {
   // 128-wide heads: P is handed over in two parts (keys 0-31 and 64-95 of a tile, then the rest), so that its product
   // starts while the second exponentials are taken: 345 -> 341 us for 8192 tokens; for 64-wide ones 259 -> 282
   static constexpr int kParts = kDim == 128 ? 2 : 1;
+  static constexpr int kSlots = kEarly ? 2 : 1;  // see exchange
 };
 
 // Cluster launch control: asks for a block of this grid that has not started yet, which then will not start; the answer
@@ -137,7 +138,8 @@ struct Work {
   int n;                            // key tiles of the longer one; 0: there is no more work
 };
 
-// What follows the tiles in shared memory.
+// What follows the tiles in shared memory. kSlots: places for what the two threads of a row tell each other, used in turn.
+template <int kSlots>
 struct Rest {
   uint64_t qfull, qfree, full[8], freed[16], sfull[2], sread[2], pfull[2][2], ofull[2], drain;
   uint64_t wfull[2], wempty[2], cfull;
@@ -146,7 +148,7 @@ struct Rest {
   int used[8];    // the event that frees each place of the ring
   uint32_t tmem;
   volatile int abort, special;
-  float half[2][2][kRows];  // [sub-tile][half]: what the two threads of a row tell each other
+  float half[kSlots][2][2][kRows];  // [.][sub-tile][half]
 };
 
 // A block for each item, longest first; but a CTA that has an item's copies under way takes over the next block that has
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // All of the shared memory is this array, which starts on a multiple of 1024 bytes then: there is no room to round up
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + Ly::kKV;
-  Rest& sh = *reinterpret_cast<Rest*>(smem + Ly::kRest);
+  auto& sh = *reinterpret_cast<Rest<Ly::kSlots>*>(smem + Ly::kRest);
   volatile int &s_abort = sh.abort, &s_special = sh.special;
   if (smem_u32(smem) & 1023) {
     if (threadIdx.x == 0) mv_set_error(a.err, kSite, MV_DEVERR_INDEX);
@@ -438,14 +440,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t at_s = lane_base + Ly::kColS + 128 * s + 64 * half;
     const uint32_t at_p = lane_base + Ly::kColP + Ly::kPStep * s + 32 * half;
     const uint32_t at_o = lane_base + Ly::kColO + kDim * s + kDim / 2 * half;  // this thread's half of the row's output
-    // what both threads of a row put in, in either's hand
-    // (the place is free again for the next tile: S of that comes after every warp's P of this)
-    auto exchange = [&](float mine) {
-      sh.half[s][half][r] = mine;
-      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-      return sh.half[s][half ^ 1][r];
-    };
     int c = 0, o_phase = 0;  // tiles and items of this sub-tile so far
+    // What the other thread of the row puts in. With one place for it, it is free again for the next tile because S of
+    // that comes after every warp's P of this. Where S comes as soon as this one has been read (kEarly), the partner may
+    // still be on its way from the barrier to its load when this thread writes for the next tile: the places take turns, and
+    // the barrier of the tile in between keeps a load and the next write of the same place apart. The sum at an item's
+    // end goes in turn like a tile's maximum, with a barrier of its own behind it.
+    auto exchange = [&](float mine) {
+      float(&place)[2][kRows] = sh.half[Ly::kSlots == 2 ? c & 1 : 0][s];
+      place[half][r] = mine;
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+      return place[half ^ 1][r];
+    };
     for (int round = 0;; ++round) {
       const Work* w = work_in(round);
       if (!__any_sync(0xffffffffu, w != nullptr)) break;
@@ -571,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int kDim>
 mv_status launch(const CUtensorMap (&maps)[3], const PromptArgs& a, int64_t grid, cudaStream_t stream) {
-  constexpr int kBytes = Layout<kDim>::kRest + (int)sizeof(Rest);
+  constexpr int kBytes = Layout<kDim>::kRest + (int)sizeof(Rest<Layout<kDim>::kSlots>);
   static_assert(kBytes <= 227 * 1024 && Layout<kDim>::kRing <= 8, "shared memory of one CTA");
   static int flags[64] = {};
   if (!mv_set_smem_once((const void*)prompt_attn_kernel<kDim>, kBytes, flags)) return MV_ERR_CUDA;

@@ -160,6 +160,30 @@ def test_prompts_of_many_items_at_once(d):
     assert torch.equal(graphed, cases[0][5])
 
 
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_prompt_rows_repeat_while_their_maximum_moves(d):
+    """Both threads of a row use the maximum of the same tile: scores that rise by more than any threshold from tile to
+    tile, in more items than SMs, give the same bits on every call, beside another call that disturbs the timing too."""
+    lens, hq, hk = [1500, 1, 900, 1100, 640], 8, 4
+    t = sum(lens)
+    q = (normal(1, t, hq, d).abs() + 0.5).to(torch.bfloat16)
+    at = torch.cat([torch.arange(n) for n in lens]).cuda()[:, None, None]
+    k = ((at * (0.12 / d) + 0.05 * normal(2, t, hk, d).float()) * d ** 0.5).to(torch.bfloat16)
+    v, plan, scale = normal(3, t, hk, d), mv.PromptPlan(lens, hq // hk), 1.0
+    first = torch.empty_like(q)
+    mv.prompt_attention(q, k, v, plan, scale, first)
+    check_prompt(q, k, v, first, lens, scale)
+    side, outs, other = torch.cuda.Stream(), [torch.full_like(q, 7.0) for _ in range(24)], torch.empty_like(q)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        mv.prompt_attention(q, k, v, plan, scale, out)
+        if i % 2:
+            mv.prompt_attention(q, k, v, plan, 0.1, other, stream=side)
+    torch.cuda.synchronize()
+    for out in outs:
+        assert torch.equal(out, first)
+
+
 def test_prompt_leaves_rows_behind_the_plan():
     lens = [130, 20]
     q, k, v, out, scale = run_prompt(lens, 2, 2, 64, extra=45)
