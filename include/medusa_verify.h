@@ -448,8 +448,9 @@ mv_status mv_session_profile_read(mv_session* session, float* ms_by_kind, int32_
  * A plan holds what depends on the lengths alone: the prompts' places and the work items, longest first. It is
  * made once for a batch of prompts and serves every layer. lens: host [n_seq], each >= 0; group = n_heads /
  * n_kv_heads of the calls it will serve. The work items are copied to the current device (without a CUDA device
- * the handle keeps the host copy only). Creating and destroying a plan may synchronise the device: not during
- * stream capture, and destroy it only when no captured graph will be replayed that uses it.
+ * the handle keeps the host copy only), and are there when the call returns: the plan serves calls on any stream. Creating
+ * a plan waits for the legacy default stream, creating and destroying one may synchronise the device: not during stream
+ * capture, and destroy it only when no captured graph will be replayed that uses it.
  * Errors: MV_ERR_INVALID_ARG (null, n_seq < 0, a negative length, group < 1), MV_ERR_SHAPE (group > 256, more than
  * 2^31 - 1 tokens or 2^22 work items), MV_ERR_CAPACITY (out of device memory), MV_ERR_CUDA.
  */

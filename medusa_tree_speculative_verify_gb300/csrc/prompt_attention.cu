@@ -661,7 +661,9 @@ extern "C" mv_status mv_prompt_plan_create(const int32_t* lens, int32_t n_seq, i
     if (e != cudaSuccess) {
       cudaGetLastError();
       s = e == cudaErrorMemoryAllocation ? MV_ERR_CAPACITY : MV_ERR_CUDA;
-    } else if (cudaMemcpy(p->d_items, p->items.data(), bytes, cudaMemcpyHostToDevice) != cudaSuccess) {
+    } else if (cudaMemcpy(p->d_items, p->items.data(), bytes, cudaMemcpyHostToDevice) != cudaSuccess ||
+               // a copy from pageable memory may still be under way, on a stream that the plan's first call does not wait for
+               cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
       cudaGetLastError();
       s = MV_ERR_CUDA;
     }

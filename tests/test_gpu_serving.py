@@ -270,6 +270,26 @@ def test_prompt_captured_and_on_another_stream():
     check_prompt(q, k, v, got, lens, scale)
 
 
+def test_prompt_on_another_stream_right_after_its_plan():
+    """A plan's first call may be on any stream: nothing waits between the two here, for plans of ever other lengths."""
+    hq, hk, d, cases, side = 4, 2, 64, [], torch.cuda.Stream()
+    for i in range(40):
+        lens = [int(x) for x in np.random.default_rng(i).integers(0, 500, 1 + 4 * (i % 20))]
+        q, k, v = normal(i, sum(lens), hq, d), normal(i + 1, sum(lens), hk, d), normal(i + 2, sum(lens), hk, d)
+        cases.append((lens, q, k, v, torch.full_like(q, 7.0)))
+    torch.cuda.synchronize()
+    plans = []
+    for lens, q, k, v, out in cases:
+        plans.append(mv.PromptPlan(lens, hq // hk))
+        mv.prompt_attention(q, k, v, plans[-1], 0.125, out, stream=side)
+    torch.cuda.synchronize()
+    for plan, (lens, q, k, v, out) in zip(plans, cases):
+        again = torch.full_like(out, 7.0)
+        mv.prompt_attention(q, k, v, plan, 0.125, again)
+        assert torch.equal(out, again)
+    check_prompt(q, k, v, out, lens, 0.125)
+
+
 def test_prompt_of_no_tokens():
     e = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
     mv.prompt_attention(e, e, e, mv.PromptPlan([0, 0]), 1.0, torch.empty_like(e))

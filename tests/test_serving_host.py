@@ -1,6 +1,10 @@
 """The serving operators on the host (no GPU needed): the prompt plan's work items, the refusals of every entry point
 before anything is launched, and the oracle's e4m3 against torch's type."""
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -42,6 +46,57 @@ def test_plan_refusals(lens, group, status):
     assert mv.lib().mv_prompt_plan_create(arr, 1, 1, None) == INVALID
     with pytest.raises(ValueError):
         mv.PromptPlan([-1])
+
+
+# A CUDA runtime of one device whose copies from pageable memory are under way when cudaMemcpy returns, as the real one's
+# may be, and come only with a synchronisation of the stream they are on.
+FAKE_RUNTIME = r"""
+#include <stdlib.h>
+#include <string.h>
+static struct { void *dst, *staged; size_t n; } late[64];
+static int n_late;
+int fake_late(void) { return n_late; }
+static int land(void) {
+  while (n_late) { --n_late; memcpy(late[n_late].dst, late[n_late].staged, late[n_late].n); free(late[n_late].staged); }
+  return 0;
+}
+int cudaGetDeviceCount(int* n) { *n = 1; return 0; }
+int cudaGetDevice(int* d) { *d = 0; return 0; }
+int cudaSetDevice(int d) { return d != 0; }
+int cudaGetLastError(void) { return 0; }
+int cudaMalloc(void** p, size_t n) { *p = calloc(n ? n : 1, 1); return 0; }
+int cudaFree(void* p) { land(); free(p); return 0; }
+int cudaMemcpy(void* dst, const void* src, size_t n, int kind) {
+  (void)kind;
+  late[n_late].staged = memcpy(malloc(n), src, n);
+  late[n_late].dst = dst;
+  late[n_late++].n = n;
+  return 0;
+}
+int cudaStreamSynchronize(void* s) { return s == (void*)0 || s == (void*)1 ? land() : 0; }
+int cudaDeviceSynchronize(void) { return land(); }
+"""
+
+
+def in_fake_runtime(tmp_path, code):
+    """Runs ``code`` in a process whose library calls the runtime above; ``late()`` counts the copies not there yet."""
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("needs a C compiler")
+    mv.lib()                                                  # built before the process starts
+    src, so = tmp_path / "fake.c", tmp_path / "fake.so"
+    src.write_text(FAKE_RUNTIME)
+    subprocess.run([cc, "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+    head = "import ctypes, medusa_tree_speculative_verify_gb300 as mv\nlate = ctypes.CDLL(None).fake_late\n"
+    env = dict(os.environ, LD_PRELOAD=str(so), PYTHONPATH=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    return subprocess.run([sys.executable, "-c", head + code], env=env, capture_output=True, text=True, timeout=120)
+
+
+def test_plan_is_on_the_device_when_it_is_handed_out(tmp_path):
+    """A first call may come on any stream, so nothing of a new plan may still be on its way."""
+    r = in_fake_runtime(tmp_path, "p = mv.PromptPlan([300, 5, 900], 2)\nassert p.n_items > 0\nprint(late())")
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == ["0"]
 
 
 def rows(ptr=FAKE, ts=1024, hs=128):
