@@ -124,6 +124,8 @@ extern "C" mv_status mv_tree_create(const int32_t* ranks, const int32_t* lens, i
   if (s == MV_OK) s = upload(&t->d_retrieve, retrieve);
   if (s == MV_OK) s = upload(&t->d_parent, parent);
   if (s == MV_OK) s = upload(&t->d_ancestors, anc);
+  // copies from pageable memory may still be under way, on a stream that the tree's first use does not wait for
+  if (s == MV_OK && cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) s = MV_ERR_CUDA;
   if (s != MV_OK) {
     mv_tree_destroy(t);
     return s;

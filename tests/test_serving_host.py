@@ -99,6 +99,12 @@ def test_plan_is_on_the_device_when_it_is_handed_out(tmp_path):
     assert r.stdout.split() == ["0"]
 
 
+def test_tree_is_on_the_device_when_it_is_handed_out(tmp_path):
+    r = in_fake_runtime(tmp_path, "t = mv.Tree([(0,), (1,), (0, 0)], 2)\nassert t.n_nodes == 4\nprint(late())")
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == ["0"]
+
+
 def rows(ptr=FAKE, ts=1024, hs=128):
     return mv._Rows(ptr, ts, hs)
 
