@@ -496,7 +496,9 @@ mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int
  * sequence's length, the rows of this call included. Entries past a sequence's last page are not read.
  * Every call reads the table and the lengths on the device, so it can be captured and replayed as they change. Found
  * there out of range (a page outside the pool, a length that is negative or over max_pages * page_size), they set the
- * device error word, and what belongs to them is neither read nor written.
+ * device error word, and what belongs to them is neither read nor written: paged_kv_append and paged_kv_read leave out
+ * the rows of such a page or sequence, paged_attention all of out's rows of a sequence with such a length, or with such a
+ * page before its end. The other sequences get what they get without it.
  * Limits: page_size % 16 == 0, 16 <= page_size <= 1024; head_dim % 16 == 0, 16 <= head_dim <= 128; 1 <= n_kv_heads <=
  * 256; 0 <= n_seq <= 4096; pools 16-byte aligned.
  */

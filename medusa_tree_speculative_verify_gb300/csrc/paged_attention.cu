@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
   __shared__ float s_ml[kWarps][3][8];  // references of x and y, sum
-  __shared__ float s_fin[4][8];         // all warps': factor of the output, the two references, sum
+  __shared__ float s_fin[5][8];         // all warps': factor of the output, the two references, sum, bad
+  __shared__ bool s_bad[kWarps];
   __shared__ int s_scan[kWarps];
   struct Split {
     int b, head0, n_heads, u0, n;  // u0, n: first place and steps of the unit; n = 0: none
@@ -343,6 +344,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     return x;
   };
   Next next = look_up(), then = look_up();
+  // A page outside the pool is not copied. What the step's place holds then is of no sequence, so a unit with such a step, in
+  // whichever warp or CTA, is bad: its rows of out stay as they were.
+  constexpr uint32_t kBad = 1u << 16;  // a lane's bad page in the sum of a step's bytes, which are fewer
+  static_assert(Ly::kStage < (int)kBad, "");
+  uint32_t bad_slots = 0;
   int copied = 0, used = 0;  // steps
   auto copy_step = [&](int slot) {
     if (next.valid) {
@@ -350,9 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bad) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)next.entry);
       const bool go = next.has && !bad;
       const uint32_t bytes = go && !my_exp ? (uint32_t)(a.box_tiles * Ly::kRegion) : 0u;
-      const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);  // also: every lane is done with the slot
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes + (bad ? kBad : 0u));  // also: every lane is done with the slot
+      bad_slots = (bad_slots & ~(1u << slot)) | (sum >= kBad ? 1u << slot : 0u);
       uint64_t* bar = &s_full[warp][slot];
-      if (lane == 0) mbar_arrive_expect_tx(bar, sum);
+      if (lane == 0) mbar_arrive_expect_tx(bar, sum & (kBad - 1));
       if (bytes) {
         const int box = my_v ? my_op - Ly::kBoxes : my_op;
         uint8_t* dst = smem + (warp * kStages + slot) * Ly::kStage + (my_op * Ly::kSub + my_u) * Ly::kRegion;
@@ -464,12 +471,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
+    bool bad = false;
     for (int i = 0; i < steps; ++i, key0 += key_add) {
       copy_step(slot == 0 ? kStages - 1 : slot - 1);
-      if (used++ < copied && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase))) {
-        more = next.valid = then.valid = false;  // nothing more is copied; what is on its way is still waited for
+      bool there = used++ < copied;  // not after a wait that gave up
+      if (there && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase))) {
+        more = next.valid = then.valid = there = false;  // nothing more is copied; what is on its way is still waited for
         mv_set_error(a.err, kPagedAttnSite, MV_DEVERR_TIMEOUT);
       }
+      bad |= !there || (bad_slots >> slot & 1u);
       const uint32_t at = queue + slot * Ly::kStage, ex_at = exps + slot * Ly::kExps;
       if (++slot == kStages) {
         slot = 0;
@@ -477,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (key0 >= key_end) continue;
 
-      // S^T: rows keys g, g + 8 of each tile, columns heads 2 t, 2 t + 1. Tiles that nothing was copied to hold what an
+      // S^T: rows keys g, g + 8 of each tile, columns heads 2 t, 2 t + 1. Tiles behind the sequence's last hold what an
       // earlier step left: their scores are masked below, their products with V are left out. Two sums for one chain of
       // products where there is only one.
       constexpr int kSums = Ly::kSub * kNT == 1 ? 2 : 1;
@@ -699,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(o[n][4 * i2 + k][e] * f, o[n][4 * i2 + k][2 + e] * f);
-            if (h < n_heads && d < a.c.dim)
+            if (h < n_heads && d < a.c.dim && !bad)
               *reinterpret_cast<uint4*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)(head0 + h) * a.out.hs + d) =
                   make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -718,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s_ml[warp][2][2 * t + e] = l[n][e];
         }
       }
+      if (lane == 0) s_bad[warp] = bad;
       // warps 4-7 leave their output, 0-3 add it to theirs, then the four sums; warp 4 meanwhile what all have in common
       float* mine = s_merge + (warp & 3) * Ly::kSlot + lane;
       if (warp >= 4) {
@@ -754,6 +765,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_fin[1][lane] = tx;
         s_fin[2][lane] = ty;
         s_fin[3][lane] = sum;
+        bool any_bad = false;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) any_bad |= s_bad[w];
+        s_fin[4][lane] = any_bad ? 1.0f : 0.0f;
       }
       __syncthreads();
       // thread: one head of the tile, 8 consecutive dims
@@ -769,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (h >= n_heads) continue;
         if (whole) {
           const float f = s_fin[0][hh];
-          if (d < a.c.dim)
+          if (d < a.c.dim && s_fin[4][hh] == 0.0f)
             *reinterpret_cast<uint4*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)(head0 + h) * a.out.hs + d) =
                 make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
                            pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
@@ -778,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float4*>(dst + h * kDim + d) = make_float4(v[0], v[1], v[2], v[3]);
           *reinterpret_cast<float4*>(dst + h * kDim + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
           if (d == 0) *reinterpret_cast<float4*>(dst + Ly::kHeads * kDim + 4 * h) =
-                make_float4(s_fin[1][hh], s_fin[2][hh], s_fin[3][hh], 0.0f);
+                make_float4(s_fin[1][hh], s_fin[2][hh], s_fin[3][hh], s_fin[4][hh]);
         }
       }
       __syncthreads();
@@ -795,14 +810,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = e / (kDim / 8), d = e % (kDim / 8) * 8;
       if (h >= n_heads || d >= a.c.dim) continue;
       float4 ml[kClusterMost];
-      float tx = -INFINITY, ty = -INFINITY, sum = 0.0f, v[8] = {};
+      float tx = -INFINITY, ty = -INFINITY, sum = 0.0f, bad = 0.0f, v[8] = {};
 #pragma unroll
       for (int c = 0; c < kClusterMost; ++c) {
         if (c >= c_size) break;
         ml[c] = ld_cluster_f4(map_rank(base + (Ly::kHeads * kDim + 4 * h) * 4, c));
         tx = fmaxf(tx, ml[c].x);
         ty = fmaxf(ty, ml[c].y);
+        bad += ml[c].w;
       }
+      if (bad != 0.0f) continue;
 #pragma unroll
       for (int c = 0; c < kClusterMost; ++c) {
         if (c >= c_size) break;
@@ -869,6 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4 none = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
       float4 ml[kMaxCtas / 32];
       float tx = -INFINITY, ty = -INFINITY, sum = 0.0f;
+      bool bad = false;
 #pragma unroll
       for (int i = 0; i < kMaxCtas / 32; ++i) {
         const int c = c0 + 32 * i + lane;
@@ -878,7 +896,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kMaxCtas / 32; ++i) {
         tx = fmaxf(tx, ml[i].x);
         ty = fmaxf(ty, ml[i].y);
+        bad |= ml[i].w != 0.0f;
       }
+      bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
       for (int w = 16; w >= 1; w >>= 1) {
         tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, w));
@@ -891,7 +911,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-      if (lane == 0) s_ml[0][0][warp] = (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum;
+      if (lane == 0) {
+        s_ml[0][0][warp] = (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum;
+        s_bad[warp] = bad;
+      }
       __syncthreads();
       float v[8] = {};
       auto add = [&](const float4& lo, const float4& hi, float f) {
@@ -918,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 8; ++k) s_sum[k * kThreads + tid] = v[k];
       __syncthreads();
-      if (tid < kDim && 8 * n + hh < n_heads && d < a.c.dim) {
+      if (tid < kDim && 8 * n + hh < n_heads && d < a.c.dim && !s_bad[hh]) {
         const float f = s_ml[0][0][hh];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {

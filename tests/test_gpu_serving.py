@@ -708,6 +708,33 @@ def test_paged_attention_out_of_range_is_reported(what):
     assert torch.equal(run_paged(pool, q, 0.1, ws=ws), good)  # the workspace serves later calls
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("lens,hq,hk,d", [
+    ([40, 17, 300, 0, 90], 4, 2, 64),                         # pieces of the line, units cut across CTAs
+    ([100] * 200 + [33], 32, 4, 128),                         # a unit to each warp
+    ([700, 64, 900, 128], 48, 4, 128),                        # two tiles of heads a unit
+    ([1000], 32, 32, 128), ([1300], 8, 1, 64), ([2300], 96, 8, 64)])   # one sequence: clusters, and pieces
+@pytest.mark.parametrize("nth", [0, 1, -1])
+@pytest.mark.parametrize("entry", [-1, 1 << 30])
+def test_paged_attention_leaves_the_row_of_a_bad_page_alone(dtype, lens, hq, hk, d, nth, entry):
+    """A page outside the pool: the rows of its sequence are not written, all others are what they are without it."""
+    pool = Pool(lens, hk, d, 16, dtype, spare=0).fill(len(lens))
+    q = normal(3, len(lens), hq, d)
+    ws = torch.zeros(mv.paged_attention_workspace(len(lens), hq, hk, d), dtype=torch.uint8, device="cuda")
+    good = run_paged(pool, q, 0.1, ws=ws)
+    b = int(np.argmax(lens)) if nth else 0
+    table = pool.table.copy()
+    table[b, nth % -(-lens[b] // 16)] = entry
+    out = run_paged(pool, q, 0.1, i32(table), ws=ws)
+    take_error(41)
+    rest = [i for i in range(len(lens)) if i != b]
+    assert (out[b] == 7.0).all() and torch.equal(out[rest], good[rest])
+    lens2 = list(lens)
+    lens2[b] = 16 * (nth % -(-lens[b] // 16))                 # the same table, a length that ends before it
+    out = run_paged(pool, q, 0.1, i32(table), i32(lens2), ws)
+    check_paged(pool, q, out, 0.1, lens2)
+
+
 def test_paged_attention_of_no_sequences():
     c = mv.PagedKV.zeros(1, 16, 2, 64)
     q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
