@@ -487,7 +487,7 @@ mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int
  * ============================================================================================
  * The pool: k, v device [n_pages][n_kv_heads][page_size][head_dim], bf16 or e4m3 (MV_DTYPE_E4M3: one sign, four
  * exponent, three fraction bits, no infinities). An e4m3 pool has an exponent byte for every row, k_exp, v_exp device
- * [n_pages][n_kv_heads][page_size]: the row stands for x8 * 2^(byte - 127). Writing a row x takes the smallest e in
+ * [n_pages][n_kv_heads][page_size]: the row stands for x8 * 2^(byte - 127), byte 0 .. 254. Writing a row x takes the smallest e in
  * [-100, 120] with max|x| <= 448 * 2^e (NaNs apart; a row of zeros: -100) and rounds x * 2^-e to the nearest e4m3, ties
  * to even. The scale is a power of two, so what a row stands for is exact in bf16 (where its exponent reaches). A NaN
  * stays a NaN, an infinity becomes 448 * 2^120, which reads back as an infinity.
@@ -526,9 +526,10 @@ mv_status paged_kv_read(const mv_paged_kv* cache, const int32_t* block_table, in
 /* One new token per sequence: for sequence b, query head h and kv head c = h / (n_heads / n_kv_heads),
  *   out[b][h] = sum_{j < seq_lens[b]} softmax_j(scale * q[b][h] . k_j[c]) v_j[c],   zeros when seq_lens[b] = 0.
  * The token's own row is in the cache already (paged_kv_append first). What pages hold behind a sequence's length does
- * not matter, NaN included; an infinity or a NaN in a row that is attended to makes that element of out one of the two.
+ * not matter, NaN included; an infinity or a NaN in a value row that is attended to makes that element of out one of the two.
  * q, out device bf16 rows, token b = sequence b; out must not overlap q or the cache. Scores, softmax statistics and
- * output sums in fp32. The result does not depend on the order in which the parts of a split sequence finish. scale
+ * output sums in fp32. The weights have 16 bits for the product with v, over e4m3 pools 11 where fp16's normal range holds
+ * all of a step's (16 to 64 keys) times their rows' scales. The result does not depend on the order in which the parts of a split sequence finish. scale
  * finite and >= 0, here and in prompt_attention.
  * Limits: n_heads % n_kv_heads == 0, n_heads <= 256. workspace: device memory of paged_attention_workspace() bytes,
  * 16-byte aligned, zero-filled before its first use (see the conventions above). Errors as above; MV_ERR_CAPACITY: the

@@ -14,11 +14,17 @@
 //   V: rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9, piece g: pairs of rows are interleaved byte-wise (prmt) to operands.
 // P goes from the layout of S^T to that of P^T by a transposing movmatrix.
 //
+// A column may have nothing in the rows of the largest weights, so small weights need their bits as much as large ones. In
+// bf16 they are split in two (16 bits), one more product each.
+//
 // e4m3: K and V convert exactly to fp16. Q is brought to fp16 with a power of two for each head (largest element in
-// [2^14, 2^15), so what fp16 loses lies 2^-38 below it). A key row's scale multiplies its score; a value row's scale
-// 2^e goes into the weight's exponent: 2^(x + e - ref) with a reference of its own, so weights of the largest values are
-// in fp16's range and what underflows lies 2^-24 below them; the sum of the softmax keeps the reference of x. Weights in
-// fp16 have 11 bits. bf16: the weights are split in two bf16 (16 bits), one more product each.
+// [2^14, 2^15), so what fp16 loses lies 2^-38 below it). A key row's scale multiplies its score; a value row's scale 2^e
+// goes into the weight's exponent, and the weight in fp16 (11 bits) into one product. Where one of a step's weights is below
+// fp16's normal range, the step is done as for bf16, with rows of V that are multiplied by their scale in bf16. The sums are
+// in units of 2^unit, -24 <= unit <= 0, which only follows the largest e (unit >= e - 7, so weights of up to 2^8 stay within
+// fp16's 2^15): however far rows' scales and weights lie apart, the sums have fp32's range. (Every step in bf16: 16 x
+// 24576 keys of 32/8 heads 151 us, 133 so; 64 ragged sequences 46, 39.5. With a unit that follows the largest scaled weight,
+// and nothing else, a row 2^25 below it was lost. Scores so far apart that all steps are done in bf16: 175 and 53.)
 //
 // Split. The work is a line of steps, kWarps tiles of keys each, over all units (sequence, kv head, 8 or 16 of its
 // heads); every CTA takes an equal piece of the line, whatever the lengths are. A unit's start and end (its Q, putting the
@@ -28,6 +34,7 @@
 // them in the order of the line, so the result does not depend on who comes last.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kernels.cuh"
 #include "paged.cuh"
@@ -42,6 +49,7 @@ constexpr unsigned int kEvenMost = 20;  // places of a piece up to which all hav
 constexpr int kMaxCtas = 160;    // counters at the start of the workspace; CTAs of a launch
 constexpr int kChunkSeq = 1024;  // sequences of one launch
 constexpr int kClusterMost = 16;
+constexpr int kUnitLeast = -24;  // log2 of the sums' unit: from here to 0
 
 struct AttnArgs {
   PagedArgs c;
@@ -136,6 +144,19 @@ MV_DEV float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two e4m3 values of two rows as bf16, times the rows' scales (bf16, powers of two): rounded only below the normal range.
+MV_DEV uint32_t scaled_bf16x2(uint16_t x, uint32_t scales) {
+  const float2 f = half2_to_float2(e4m3x2_to_half2(x));
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(__byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632)), "r"(scales));
+  return r;
+}
+// Two weights each split in two bf16, transposed
+MV_DEV void split_weights(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  const uint32_t h = pack_bf16x2(p0, p1);
+  hi = transpose8x8(h);
+  lo = transpose8x8(pack_bf16x2(p0 - bf16lo(h), p1 - bf16hi(h)));
+}
 // 2^(a - b) where both may be -inf (then the weight of nothing: 0)
 MV_DEV float weight(float a, float b) { return a == -INFINITY ? 0.0f : exp2f(a - b); }
 
@@ -147,8 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
-  __shared__ float s_ml[kWarps][3][8];  // references of x and y, sum
-  __shared__ float s_fin[5][8];         // all warps': factor of the output, the two references, sum, bad
+  __shared__ float s_ml[kWarps][2][8];  // reference, sum
+  __shared__ float s_fin[4][8];         // all warps': factor of the output, reference, sum, bad
+  __shared__ float s_unit[kWarps];      // unit of the sums
   __shared__ bool s_bad[kWarps];
   __shared__ int s_scan[kWarps];
   struct Split {
@@ -457,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mult[n][0] = mult[n][1] = a.scale_log2;
       }
     }
-    float o[kNT][Ly::kMT][4], mx[kNT][2], my[kNT][2], l[kNT][2];
+    int sum_unit = kE4M3 ? kUnitLeast : 0;
+    float o[kNT][Ly::kMT][4], mx[kNT][2], l[kNT][2];
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
 #pragma unroll
@@ -466,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) o[n][m][e] = 0.0f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[n][e] = my[n][e] = -INFINITY;
+        mx[n][e] = -INFINITY;
         l[n][e] = 0.0f;
       }
     }
@@ -534,18 +557,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[0][0][e] += x2[e];
       // scores into the exponent's base; the value rows' exponents
-      float ev[Ly::kSub][2];
+      int ev[Ly::kSub][2], top_ev = kUnitLeast;
 #pragma unroll
       for (int u = 0; u < Ly::kSub; ++u)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int key = key0 + 16 * u + g + 8 * r;
           float ks = 1.0f;
-          ev[u][r] = 0.0f;
           if (kE4M3) {
             const uint32_t ex = ex_at + 32 * u + g + 8 * r;
             ks = exp_byte_scale(lds_byte(ex));
-            ev[u][r] = (float)((int)lds_byte(ex + 16) - 127);
+            ev[u][r] = (int)lds_byte(ex + 16) - 127;
+            top_ev = max(top_ev, key < len ? ev[u][r] : kUnitLeast);
           }
 #pragma unroll
           for (int n = 0; n < kNT; ++n)
@@ -555,48 +578,46 @@ __global__ void __launch_bounds__(kThreads, 1)
               v = key < len ? v * (kE4M3 ? ks * mult[n][e] : mult[n][e]) : -INFINITY;
             }
         }
-      // the references: moved when a score outgrows them by 2^8 (as far as fp16 weights reach)
-      bool grow = false;
-      float tx[kNT][2], ty[kNT][2];
+      // the references: moved when a score outgrows them by 2^8, from nothing at the first key that is seen; the unit too
+      bool grow = kE4M3 && top_ev > sum_unit + 7 && sum_unit < 0;
+      float tx[kNT][2];
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          tx[n][e] = ty[n][e] = -INFINITY;
+          tx[n][e] = -INFINITY;
 #pragma unroll
           for (int u = 0; u < Ly::kSub; ++u)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              tx[n][e] = fmaxf(tx[n][e], x[n][u][2 * r + e]);
-              ty[n][e] = fmaxf(ty[n][e], x[n][u][2 * r + e] + ev[u][r]);
-            }
-          // from nothing: at the first key that is seen
-          grow |= tx[n][e] > mx[n][e] + 8.0f || (kE4M3 && ty[n][e] > my[n][e] + 8.0f);
+            for (int r = 0; r < 2; ++r) tx[n][e] = fmaxf(tx[n][e], x[n][u][2 * r + e]);
+          grow |= tx[n][e] > mx[n][e] + 8.0f;
         }
       if (__any_sync(0xffffffffu, grow)) {
+        float shift = 1.0f;
+        if (kE4M3) {
+          const int next = min(0, max(sum_unit, __reduce_max_sync(0xffffffffu, top_ev) - 7));
+          shift = __uint_as_float((uint32_t)(127 + sum_unit - next) << 23);
+          sum_unit = next;
+        }
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int w = 4; w <= 16; w <<= 1) {
-              tx[n][e] = fmaxf(tx[n][e], __shfl_xor_sync(0xffffffffu, tx[n][e], w));
-              if (kE4M3) ty[n][e] = fmaxf(ty[n][e], __shfl_xor_sync(0xffffffffu, ty[n][e], w));
-            }
-            const float nx = fmaxf(mx[n][e], tx[n][e]), ny = kE4M3 ? fmaxf(my[n][e], ty[n][e]) : nx;
-            l[n][e] *= weight(mx[n][e], nx);
-            const float f = weight(my[n][e], ny);
+            for (int w = 4; w <= 16; w <<= 1) tx[n][e] = fmaxf(tx[n][e], __shfl_xor_sync(0xffffffffu, tx[n][e], w));
+            const float nx = fmaxf(mx[n][e], tx[n][e]), f = weight(mx[n][e], nx), fo = f * shift;
+            l[n][e] *= f;
 #pragma unroll
             for (int m = 0; m < Ly::kMT; ++m) {
-              o[n][m][e] *= f;
-              o[n][m][2 + e] *= f;
+              o[n][m][e] *= fo;
+              o[n][m][2 + e] *= fo;
             }
             mx[n][e] = nx;
-            my[n][e] = ny;
           }
       }
       // weights, their sum, and P^T as the second operand
       uint32_t ph[kNT][Ly::kSub][2], pl[kNT][Ly::kSub][2];
+      float least = 0.0f;
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -606,81 +627,121 @@ __global__ void __launch_bounds__(kThreads, 1)
             float p[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float v = x[n][u][2 * r + e], bx = mx[n][e] == -INFINITY ? 0.0f : mx[n][e];
-              p[e] = ex2(v - bx);
+              float& y = x[n][u][2 * r + e];
+              y -= mx[n][e] == -INFINITY ? 0.0f : mx[n][e];
+              p[e] = ex2(y);
               l[n][e] += p[e];
-              if (kE4M3) p[e] = ex2(v + ev[u][r] - (my[n][e] == -INFINITY ? 0.0f : my[n][e]));
+              if (kE4M3) {
+                const float z = y + (float)(ev[u][r] - sum_unit);
+                least = fminf(least, key0 + 16 * u + g + 8 * r < len ? z : 0.0f);
+                p[e] = ex2(z);
+              }
             }
             if (kE4M3) {
               ph[n][u][r] = transpose8x8(pack_f16x2(p[0], p[1]));
             } else {
-              const uint32_t hi = pack_bf16x2(p[0], p[1]);
-              ph[n][u][r] = transpose8x8(hi);
-              pl[n][u][r] = transpose8x8(pack_bf16x2(p[0] - bf16lo(hi), p[1] - bf16hi(hi)));
+              split_weights(p[0], p[1], ph[n][u][r], pl[n][u][r]);
             }
           }
-      // O^T += V^T P^T
+      const bool low = kE4M3 && __any_sync(0xffffffffu, least < -14.0f || top_ev > 7);
+      // O^T += V^T P^T; kWide: e4m3 rows times their scales in bf16, with ph and pl
+      auto add_values = [&](auto wide) {
+        constexpr bool kWide = decltype(wide)::value;
 #pragma unroll
-      for (int u = 0; u < Ly::kSub; ++u) {
-        if (u > 0 && key0 + 16 * u >= len) break;
-        const uint32_t vt = at + Ly::kV + u * Ly::kRegion;
-        const int left = len - key0 - 16 * u;
-        constexpr int kPieces = Ly::kBoxes, kWords = Ly::kVPiece / 4;
+        for (int u = 0; u < Ly::kSub; ++u) {
+          if (u > 0 && key0 + 16 * u >= len) break;
+          const uint32_t vt = at + Ly::kV + u * Ly::kRegion;
+          const int left = len - key0 - 16 * u;
+          constexpr int kPieces = Ly::kBoxes, kWords = Ly::kVPiece / 4;
+          uint32_t scales[2];  // of rows 2 t and 2 t + 1, 2 t + 8 and 2 t + 9
+          if (kWide) {
 #pragma unroll
-        for (int i2 = 0; i2 < kPieces; ++i2) {
-          uint32_t w[4][4];  // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+            for (int r = 0; r < 2; ++r) {
+              uint32_t s[2];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const uint32_t src = vt + i2 * Ly::kSub * Ly::kRegion + v_off[r & 1] + (r >> 1) * 8 * Ly::kBox;
-            if (kWords == 4) {
-              const uint4 v = lds16(src);
-              w[r][0] = v.x;
-              w[r][1] = v.y;
-              w[r][2] = v.z;
-              w[r][3] = v.w;
+              for (int i = 0; i < 2; ++i) {
+                const int row = 2 * t + i + 8 * r, byte = (int)lds_byte(ex_at + 32 * u + 16 + row) - sum_unit;
+                s[i] = row >= left ? 0u : byte > 0 ? (uint32_t)min(byte, 255) << 7 : 0x40u;
+              }
+              scales[r] = s[0] | s[1] << 16;
+            }
+          }
+#pragma unroll
+          for (int i2 = 0; i2 < kPieces; ++i2) {
+            uint32_t w[4][4];  // rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t src = vt + i2 * Ly::kSub * Ly::kRegion + v_off[r & 1] + (r >> 1) * 8 * Ly::kBox;
+              if (kWords == 4) {
+                const uint4 v = lds16(src);
+                w[r][0] = v.x;
+                w[r][1] = v.y;
+                w[r][2] = v.z;
+                w[r][3] = v.w;
+              } else {
+                const uint2 v = lds8(src);
+                w[r][0] = v.x;
+                w[r][1] = v.y;
+              }
+            }
+            if (left < 16) {  // rows behind the sequence hold anything: weight zero times a NaN would be one
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                if (2 * t + (r & 1) + 4 * (r & 2) >= left)
+#pragma unroll
+                  for (int j = 0; j < kWords; ++j) w[r][j] = 0u;
+            }
+            if (kE4M3) {
+#pragma unroll
+              for (int m = 0; m < 2 * kWords; ++m) {  // two of a word's four dims
+                const uint32_t sel = m & 1 ? 0x7362u : 0x5140u;
+                const uint32_t lo = __byte_perm(w[0][m >> 1], w[1][m >> 1], sel), hi = __byte_perm(w[2][m >> 1], w[3][m >> 1], sel);
+                if (kWide) {
+                  const uint32_t a0 = scaled_bf16x2((uint16_t)lo, scales[0]), a1 = scaled_bf16x2((uint16_t)(lo >> 16), scales[0]);
+                  const uint32_t a2 = scaled_bf16x2((uint16_t)hi, scales[1]), a3 = scaled_bf16x2((uint16_t)(hi >> 16), scales[1]);
+#pragma unroll
+                  for (int n = 0; n < kNT; ++n) mma<false>(o[n][m], a0, a1, a2, a3, ph[n][u][0], ph[n][u][1]);
+#pragma unroll
+                  for (int n = 0; n < kNT; ++n) mma<false>(o[n][m], a0, a1, a2, a3, pl[n][u][0], pl[n][u][1]);
+                } else {
+                  const uint32_t a0 = e4m3x2_to_half2((uint16_t)lo), a1 = e4m3x2_to_half2((uint16_t)(lo >> 16));
+                  const uint32_t a2 = e4m3x2_to_half2((uint16_t)hi), a3 = e4m3x2_to_half2((uint16_t)(hi >> 16));
+#pragma unroll
+                  for (int n = 0; n < kNT; ++n) mma<true>(o[n][m], a0, a1, a2, a3, ph[n][u][0], ph[n][u][1]);
+                }
+              }
             } else {
-              const uint2 v = lds8(src);
-              w[r][0] = v.x;
-              w[r][1] = v.y;
-            }
-          }
-          if (left < 16) {  // rows behind the sequence hold anything: weight zero times a NaN would be one
+              uint32_t f[4][4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (2 * t + (r & 1) + 4 * (r & 2) >= left)
+              for (int j = 0; j < 4; ++j) {
+                f[j][0] = __byte_perm(w[0][j], w[1][j], 0x5410);
+                f[j][1] = __byte_perm(w[0][j], w[1][j], 0x7632);
+                f[j][2] = __byte_perm(w[2][j], w[3][j], 0x5410);
+                f[j][3] = __byte_perm(w[2][j], w[3][j], 0x7632);
+              }
 #pragma unroll
-                for (int j = 0; j < kWords; ++j) w[r][j] = 0u;
-          }
-          if (kE4M3) {
+              for (int n = 0; n < kNT; ++n) {
 #pragma unroll
-            for (int m = 0; m < 2 * kWords; ++m) {  // two of a word's four dims
-              const uint32_t sel = m & 1 ? 0x7362u : 0x5140u;
-              const uint32_t lo = __byte_perm(w[0][m >> 1], w[1][m >> 1], sel), hi = __byte_perm(w[2][m >> 1], w[3][m >> 1], sel);
-              const uint32_t a0 = e4m3x2_to_half2((uint16_t)lo), a1 = e4m3x2_to_half2((uint16_t)(lo >> 16));
-              const uint32_t a2 = e4m3x2_to_half2((uint16_t)hi), a3 = e4m3x2_to_half2((uint16_t)(hi >> 16));
+                for (int j = 0; j < 4; ++j)
+                  mma<false>(o[n][4 * i2 + j], f[j][0], f[j][1], f[j][2], f[j][3], ph[n][u][0], ph[n][u][1]);
 #pragma unroll
-              for (int n = 0; n < kNT; ++n) mma<true>(o[n][m], a0, a1, a2, a3, ph[n][u][0], ph[n][u][1]);
-            }
-          } else {
-            uint32_t f[4][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              f[j][0] = __byte_perm(w[0][j], w[1][j], 0x5410);
-              f[j][1] = __byte_perm(w[0][j], w[1][j], 0x7632);
-              f[j][2] = __byte_perm(w[2][j], w[3][j], 0x5410);
-              f[j][3] = __byte_perm(w[2][j], w[3][j], 0x7632);
-            }
-#pragma unroll
-            for (int n = 0; n < kNT; ++n) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma<false>(o[n][4 * i2 + j], f[j][0], f[j][1], f[j][2], f[j][3], ph[n][u][0], ph[n][u][1]);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                mma<false>(o[n][4 * i2 + j], f[j][0], f[j][1], f[j][2], f[j][3], pl[n][u][0], pl[n][u][1]);
+                for (int j = 0; j < 4; ++j)
+                  mma<false>(o[n][4 * i2 + j], f[j][0], f[j][1], f[j][2], f[j][3], pl[n][u][0], pl[n][u][1]);
+              }
             }
           }
         }
+      };
+      if (low) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int u = 0; u < Ly::kSub; ++u)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) split_weights(ex2(x[n][u][2 * r]), ex2(x[n][u][2 * r + 1]), ph[n][u][r], pl[n][u][r]);
+        add_values(std::integral_constant<bool, kE4M3>());
+      } else {
+        add_values(std::false_type());
       }
     }
 
@@ -694,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       next_entry(here, s - kUnitCost);
       load_q(here);
     }
+    const float unit_scale = __uint_as_float((uint32_t)(127 + sum_unit) << 23);
     if (one) {  // a unit of one warp: done here
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
@@ -702,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int w = 4; w <= 16; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
           const int h = 8 * n + 2 * t + e;
-          const float f = len > 0 ? (kE4M3 ? exp2f(my[n][e] - mx[n][e]) : 1.0f) / l[n][e] : 0.0f;
+          const float f = len > 0 ? unit_scale / l[n][e] : 0.0f;
 #pragma unroll
           for (int i2 = 0; i2 < kDim / 64; ++i2) {
             const int d = kE4M3 ? kDim / 8 * g + 8 * i2 : 8 * (g + 8 * i2);
@@ -724,11 +786,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = 4; w <= 16; w <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], w);
         if (g == 0) {
           s_ml[warp][0][2 * t + e] = mx[n][e];
-          s_ml[warp][1][2 * t + e] = my[n][e];
-          s_ml[warp][2][2 * t + e] = l[n][e];
+          s_ml[warp][1][2 * t + e] = l[n][e];
         }
       }
-      if (lane == 0) s_bad[warp] = bad;
+      if (lane == 0) {
+        s_bad[warp] = bad;
+        s_unit[warp] = unit_scale;
+      }
       // warps 4-7 leave their output, 0-3 add it to theirs, then the four sums; warp 4 meanwhile what all have in common
       float* mine = s_merge + (warp & 3) * Ly::kSlot + lane;
       if (warp >= 4) {
@@ -744,31 +808,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 2; ++e) {
           float top = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][1][2 * t + e]);
-          f[e] = weight(my[n][e], top);
-          f4[e] = weight(s_ml[warp + 4][1][2 * t + e], top);
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][0][2 * t + e]);
+          f[e] = weight(mx[n][e], top) * unit_scale;
+          f4[e] = weight(s_ml[warp + 4][0][2 * t + e], top) * s_unit[warp + 4];
         }
 #pragma unroll
         for (int m = 0; m < Ly::kMT; ++m)
 #pragma unroll
           for (int e = 0; e < 4; ++e) mine[(4 * m + e) * 32] = o[n][m][e] * f[e & 1] + mine[(4 * m + e) * 32] * f4[e & 1];
       } else if (warp == 4 && lane < 8) {
-        float tx = -INFINITY, ty = -INFINITY, sum = 0.0f;
+        float tx = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          tx = fmaxf(tx, s_ml[w][0][lane]);
-          ty = fmaxf(ty, s_ml[w][1][lane]);
-        }
+        for (int w = 0; w < kWarps; ++w) tx = fmaxf(tx, s_ml[w][0][lane]);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += s_ml[w][2][lane] * weight(s_ml[w][0][lane], tx);
-        s_fin[0][lane] = len > 0 ? (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum : 0.0f;
+        for (int w = 0; w < kWarps; ++w) sum += s_ml[w][1][lane] * weight(s_ml[w][0][lane], tx);
+        s_fin[0][lane] = len > 0 ? 1.0f / sum : 0.0f;
         s_fin[1][lane] = tx;
-        s_fin[2][lane] = ty;
-        s_fin[3][lane] = sum;
+        s_fin[2][lane] = sum;
         bool any_bad = false;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) any_bad |= s_bad[w];
-        s_fin[4][lane] = any_bad ? 1.0f : 0.0f;
+        s_fin[3][lane] = any_bad ? 1.0f : 0.0f;
       }
       __syncthreads();
       // thread: one head of the tile, 8 consecutive dims
@@ -784,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (h >= n_heads) continue;
         if (whole) {
           const float f = s_fin[0][hh];
-          if (d < a.c.dim && s_fin[4][hh] == 0.0f)
+          if (d < a.c.dim && s_fin[3][hh] == 0.0f)
             *reinterpret_cast<uint4*>(a.out.p + (int64_t)b * a.out.ts + (int64_t)(head0 + h) * a.out.hs + d) =
                 make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
                            pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
@@ -793,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float4*>(dst + h * kDim + d) = make_float4(v[0], v[1], v[2], v[3]);
           *reinterpret_cast<float4*>(dst + h * kDim + d + 4) = make_float4(v[4], v[5], v[6], v[7]);
           if (d == 0) *reinterpret_cast<float4*>(dst + Ly::kHeads * kDim + 4 * h) =
-                make_float4(s_fin[1][hh], s_fin[2][hh], s_fin[3][hh], s_fin[4][hh]);
+                make_float4(s_fin[1][hh], s_fin[2][hh], s_fin[3][hh], 0.0f);
         }
       }
       __syncthreads();
@@ -810,14 +870,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = e / (kDim / 8), d = e % (kDim / 8) * 8;
       if (h >= n_heads || d >= a.c.dim) continue;
       float4 ml[kClusterMost];
-      float tx = -INFINITY, ty = -INFINITY, sum = 0.0f, bad = 0.0f, v[8] = {};
+      float tx = -INFINITY, sum = 0.0f, bad = 0.0f, v[8] = {};
 #pragma unroll
       for (int c = 0; c < kClusterMost; ++c) {
         if (c >= c_size) break;
         ml[c] = ld_cluster_f4(map_rank(base + (Ly::kHeads * kDim + 4 * h) * 4, c));
         tx = fmaxf(tx, ml[c].x);
-        ty = fmaxf(ty, ml[c].y);
-        bad += ml[c].w;
+        bad += ml[c].z;
       }
       if (bad != 0.0f) continue;
 #pragma unroll
@@ -825,12 +884,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c >= c_size) break;
         const uint32_t src = map_rank(base + (h * kDim + d) * 4, c);
         const float4 lo = ld_cluster_f4(src), hi = ld_cluster_f4(src + 16);
-        const float f = weight(ml[c].y, ty), x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        sum += ml[c].z * weight(ml[c].x, tx);
+        const float f = weight(ml[c].x, tx), x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        sum += ml[c].y * f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += x[k] * f;
       }
-      const float f = here.len > 0 ? (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum : 0.0f;
+      const float f = here.len > 0 ? 1.0f / sum : 0.0f;
       *reinterpret_cast<uint4*>(a.out.p + (int64_t)(head0 + h) * a.out.hs + d) =
           make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f), pack_bf16x2(v[4] * f, v[5] * f),
                      pack_bf16x2(v[6] * f, v[7] * f));
@@ -881,11 +940,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           hi[i] = __ldcg(reinterpret_cast<const float4*>(src + 4));
         }
       }
-      // a warp for each head: the references' maxima, the parts' weights, the sum
+      // a warp for each head: the references' maximum, the parts' weights, the sum
       const int h = 8 * n + warp;
-      const float4 none = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+      const float4 none = make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
       float4 ml[kMaxCtas / 32];
-      float tx = -INFINITY, ty = -INFINITY, sum = 0.0f;
+      float tx = -INFINITY, sum = 0.0f;
       bool bad = false;
 #pragma unroll
       for (int i = 0; i < kMaxCtas / 32; ++i) {
@@ -895,24 +954,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kMaxCtas / 32; ++i) {
         tx = fmaxf(tx, ml[i].x);
-        ty = fmaxf(ty, ml[i].y);
-        bad |= ml[i].w != 0.0f;
+        bad |= ml[i].z != 0.0f;
       }
       bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
-      for (int w = 16; w >= 1; w >>= 1) {
-        tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, w));
-        ty = fmaxf(ty, __shfl_xor_sync(0xffffffffu, ty, w));
-      }
+      for (int w = 16; w >= 1; w >>= 1) tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, w));
 #pragma unroll
       for (int i = 0; i < kMaxCtas / 32; ++i) {
-        s_w[warp * kMaxCtas + 32 * i + lane] = weight(ml[i].y, ty);
-        sum += ml[i].z * weight(ml[i].x, tx);
+        const float f = weight(ml[i].x, tx);
+        s_w[warp * kMaxCtas + 32 * i + lane] = f;
+        sum += ml[i].y * f;
       }
 #pragma unroll
       for (int w = 16; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
       if (lane == 0) {
-        s_ml[0][0][warp] = (kE4M3 ? exp2f(ty - tx) : 1.0f) / sum;
+        s_ml[0][0][warp] = 1.0f / sum;
         s_bad[warp] = bad;
       }
       __syncthreads();

@@ -641,6 +641,54 @@ def test_paged_attention_value_rows_of_any_size():
 
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n,hq,d,n_seq", [(64, 2, 64, 1), (900, 8, 128, 2), (40, 12, 128, 300), (2500, 3, 64, 3)])
+def test_paged_attention_of_columns_that_few_rows_fill(dtype, n, hq, d, n_seq):
+    """Every column's value comes from its own rows, however far their sizes and weights lie below those of rows that have
+    nothing there: each value row fills one column in 16, its size and its key's score follow the column."""
+    rows = np.arange(n_seq * n)
+    col = rows % 16
+    size = 2.0 ** (12.0 * (col - 8))                          # 2^-96 .. 2^84
+    v = np.zeros((len(rows), 1, d))
+    fill = np.abs(f64(normal(1, len(rows), 1, d))) + 0.25
+    v[:, 0, :] = np.where(np.arange(d)[None] % 16 == col[:, None], fill[:, 0] * size[:, None], 0.0)
+    k = np.zeros_like(v)
+    k[:, 0, 0] = -2.5 * (col * 7 % 16)                        # weights down to e^-37.5 of the largest
+    q = np.zeros((n_seq, hq, d))
+    q[:, :, 0] = 1.0 + 0.0625 * (np.arange(hq) % 4)
+    k, v, q = (torch.as_tensor(x, device="cuda").to(torch.bfloat16) for x in (k, v, q))
+    pool = Pool([n] * n_seq, 1, d, 16, dtype)
+    mv.paged_kv_append(k, v, i32(np.arange(n_seq + 1) * n), pool.cache, pool.d_table, pool.d_lens)
+    out = run_paged(pool, q, 1.0)
+    check_paged(pool, q, out, 1.0)
+    # nothing is lost above bf16's normal range (below it, a value may round to zero: column 2 with q = 1.1875 has
+    # 2^-72 e^(-2.5 * 14 * 1.1875) 0.25 = 2^-133.96, under half of the smallest bf16)
+    ref, _ = serving.paged_attention(f64(q), *pool.values(), pool.table, pool.lens, 1.0)
+    assert (f64(out)[ref > 2.0 ** -126] != 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("n", [5, 700])
+def test_paged_attention_of_nan_and_infinity(dtype, bad, n):
+    """In a value row that is attended to: out of its kv head's query heads is not finite there, and the others' as it was."""
+    hq, hk, d, at = 6, 2, 64, n // 2
+    pool = Pool([n], hk, d, 16, dtype)
+    k, v, q = normal(1, n, hk, d), normal(2, n, hk, d), normal(3, 1, hq, d)
+    args = i32([0, n]), pool.cache, pool.d_table, pool.d_lens
+    mv.paged_kv_append(k, v, *args)
+    clean = run_paged(pool, q, 0.125)
+    v[at, 1, 7] = bad
+    mv.paged_kv_append(k, v, *args)
+    out = run_paged(pool, q, 0.125)
+    assert torch.equal(out[:, :3], clean[:, :3])
+    assert not torch.isfinite(out[:, 3:, 7]).any()
+    assert torch.isfinite(out[:, 3:, :7]).all() and torch.isfinite(out[:, 3:, 8:]).all()
+    if dtype == BF16 or bad != bad:                           # a NaN does not count for its row's scale
+        rest = [e for e in range(d) if e != 7]
+        assert torch.equal(out[:, 3:, rest], clean[:, 3:, rest])
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
 @pytest.mark.parametrize("n", [1, 13, 16, 100])
 def test_paged_attention_ignores_what_lies_behind(dtype, n):
     pool = Pool([n], 2, 128, 64, dtype).fill(1)
