@@ -71,7 +71,8 @@ MV_DEV int2 place_of(const MoveArgs& a, int t, int n) {
   if (t >= end) return make_int2(-1, 0);
   if (c0 < 0 || t < c0 || t >= c1) return make_int2(-2, 0);
   const int64_t pos = (int64_t)len - c1 + t;
-  if (len < c1 - c0 || pos < 0 || pos >= (int64_t)a.c.max_pages * a.c.page_size) return make_int2(-2, 0);
+  // a length over the table's is refused with all its rows, those too that would have a place
+  if (len < c1 - c0 || pos < 0 || len > a.c.max_pages * a.c.page_size) return make_int2(-2, 0);
   const int nth = (int)pos / a.c.page_size;
   const int page = __ldcg(a.c.table + (int64_t)lo * a.c.ld_table + nth);
   if (page < 0 || page >= a.c.n_pages) return make_int2(-2, 0);

@@ -513,6 +513,46 @@ def test_rows_out_of_range_are_reported_and_left_alone(what):
     take_error(40)
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("what", ["len_high", "len_negative", "too_many_rows", "page_high", "page_low"])
+def test_rows_of_a_bad_sequence_or_page_stay_where_they_are(dtype, what):
+    """Neither written nor read back: all rows of a sequence with a bad length, the rows of a bad page; the others move."""
+    hk, d, page, rows = 2, 64, 16, [20, 30, 25]
+    lens = [20, 48, 25]                                       # three pages of 16 in the table's rows
+    pool = Pool(lens, hk, d, page, dtype, spare=0)
+    cu, table, cur = i32(np.cumsum([0] + rows)), pool.table.copy(), list(lens)
+    left_out = list(range(20, 50))
+    if what == "len_high":
+        cur[1] = 60                                           # the first 18 of its rows would have places below 48
+    elif what == "len_negative":
+        cur[1] = -1
+    elif what == "too_many_rows":
+        cur[1] = 29
+    else:
+        table[1, 1] = pool.cache.n_pages if what == "page_high" else -1   # positions 16 .. 31: rows 20 .. 33
+        left_out = list(range(20, 34))
+    x, y = normal(1, sum(rows), hk, d), normal(2, sum(rows), hk, d)
+    keep = [i for i in range(sum(rows)) if i not in left_out]
+    before = pool.bits()
+    mv.paged_kv_append(x, y, cu, pool.cache, i32(table), i32(cur))
+    take_error(40)
+    after = pool.bits()
+    mv.paged_kv_append(x, y, cu, pool.cache, pool.d_table, i32(lens))     # what the pool holds with all rows
+    full = pool.bits()
+    at = [(int(pool.table[b, p // page]), p % page) for b in range(3) for p in range(lens[b] - rows[b], lens[b])]
+    for was, now, whole in zip(before, after, full):
+        want = was.clone()
+        for i in keep:
+            want[at[i][0], :, at[i][1]] = whole[at[i][0], :, at[i][1]]
+        assert torch.equal(now, want)
+    want, got = ([torch.full_like(x, 7.0) for _ in range(2)] for _ in range(2))
+    mv.paged_kv_read(pool.cache, pool.d_table, i32(lens), cu, *want)
+    mv.paged_kv_read(pool.cache, i32(table), i32(cur), cu, *got)
+    take_error(40)
+    for w, g in zip(want, got):
+        assert torch.equal(g[keep], w[keep]) and (g[left_out] == 7.0).all()
+
+
 # ------------------------------------------------------------------------------------------------ paged attention
 
 def run_paged(pool, q, scale, table=None, lens=None, ws=None):
