@@ -476,7 +476,7 @@ typedef struct mv_rows {
 /* q, out: n_heads heads, k, v: n_kv_heads, all plan->n_tokens tokens. Rows of out outside the plan are not touched.
  * out must not overlap q, k or v. Limits: head_dim % 8 == 0, 8 <= head_dim <= 128; n_heads = group * n_kv_heads <=
  * 256; token_stride >= head_dim or one token, head_stride >= head_dim or one head (each below 2^30 and 2^39); rows of out that
- * do not overlap one another; scale finite and >= 0.
+ * do not overlap one another; scale >= 0, log2(e) * scale finite.
  * Errors: MV_ERR_INVALID_ARG (null, unaligned, a plan of another device), MV_ERR_SHAPE, MV_ERR_CUDA (also a plan
  * made without a device). */
 mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
@@ -530,7 +530,7 @@ mv_status paged_kv_read(const mv_paged_kv* cache, const int32_t* block_table, in
  * q, out device bf16 rows, token b = sequence b; out must not overlap q or the cache. Scores, softmax statistics and
  * output sums in fp32. The weights have 16 bits for the product with v, over e4m3 pools 11 where fp16's normal range holds
  * all of a step's (16 to 64 keys) times their rows' scales. The result does not depend on the order in which the parts of a split sequence finish. scale
- * finite and >= 0, here and in prompt_attention.
+ * >= 0 and log2(e) * scale finite, here and in prompt_attention.
  * Limits: n_heads % n_kv_heads == 0, n_heads <= 256. workspace: device memory of paged_attention_workspace() bytes,
  * 16-byte aligned, zero-filled before its first use (see the conventions above). Errors as above; MV_ERR_CAPACITY: the
  * workspace is too small. */

@@ -7,6 +7,8 @@
 
 constexpr int kPagedMaxSeq = 4096, kPagedMaxHeads = 256, kPagedMaxDim = 128, kPagedMaxPage = 1024;
 
+constexpr float kLog2E = 1.4426950408889634f;
+
 // Sites of the device error word.
 constexpr uint32_t kPagedRowsSite = 40, kPagedAttnSite = 41;
 

@@ -1138,13 +1138,13 @@ extern "C" mv_status paged_attention(mv_rows q, int32_t n_heads, const mv_paged_
   s = paged_attention_workspace(n_seq, n_heads, a.c.heads, a.c.dim, &need);
   if (s != MV_OK) return s;
   if (!mv_rows_ok(q, n_seq, n_heads, a.c.dim) || !mv_out_rows_ok(out, n_seq, n_heads, a.c.dim)) return MV_ERR_INVALID_ARG;
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) || !(scale >= 0.0f && scale < INFINITY))
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) || !(scale >= 0.0f && scale * kLog2E < INFINITY))
     return MV_ERR_INVALID_ARG;
   if (ws_bytes < need) return MV_ERR_CAPACITY;
   a.group = n_heads / a.c.heads;
   const bool wide = a.group > 8;  // 16 heads a unit: their second tile of 8 shares the copies
   a.parts = wide ? (a.group + 15) / 16 : 1;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale * kLog2E;
   a.count = static_cast<unsigned int*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kMaxCtas * sizeof(uint32_t));
   a.err = mv_error_word();

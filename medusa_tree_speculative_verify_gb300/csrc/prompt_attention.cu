@@ -85,6 +85,9 @@ constexpr uint32_t kTmemCols = 512;
 MV_DEV uint64_t desc_plus(uint64_t d, uint32_t by) { return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + by); }
 
 constexpr float kRescaleLog2 = 8.0f;  // move the exponent reference when the row maximum grows by more than this
+// From here on the reference's rounding is half an exponent and more: a row's scores are rounded like it before it is taken
+// off, and brought back to what the multiplication below makes the difference of.
+constexpr float kLargeLog2 = 0x1p22f;
 
 // kDim: head_dim rounded up to 64 or 128 (the copies fill the rest with zeros). Shared memory from a 1024-byte aligned
 // base: Q of both sub-tiles, then a ring of kRing tiles of 128 keys, K and V of a tile in turn; each as kDim / 64
@@ -488,20 +491,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           tc_after();
         }
-        if (__any_sync(0xffffffffu, move && m_ref > -INFINITY)) {
-          const float f = move ? fast_exp2(m_ref - m_new) : 1.0f;
-          l *= f;
+        float base = move ? m_new : m_ref;
+        if (__any_sync(0xffffffffu, (move && m_ref > -INFINITY) || fabsf(m_new) >= kLargeLog2)) {
+          if (__any_sync(0xffffffffu, move && m_ref > -INFINITY)) {
+            const float f = move ? fast_exp2(m_ref - m_new) : 1.0f;
+            l *= f;
 #pragma unroll 1
-          for (int e0 = 0; e0 < kDim / 2; e0 += 16) {  // seldom: a few registers at a time, the row of S stays in its own
-            uint32_t o[16];
-            tc_ld16u(at_o + e0, o);
+            for (int e0 = 0; e0 < kDim / 2; e0 += 16) {  // seldom: a few registers at a time, the row of S stays in its own
+              uint32_t o[16];
+              tc_ld16u(at_o + e0, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tc_st16u(at_o + e0, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc_st16u(at_o + e0, o);
+            }
           }
+          m_ref = base;
+          if (fabsf(m_new) >= kLargeLog2 && fabsf(m_new) < INFINITY) {  // the score is finite: scale is 2^-106 at least
+            const float back = 1.0f / a.scale_log2;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x[e] = __fsub_rn(__fmul_rn(x[e], a.scale_log2), base) * back;
+            base = 0.0f;
+          }
+        } else {
+          m_ref = base;
         }
-        if (move) m_ref = m_new;
-        const float base = m_ref == -INFINITY ? 0.0f : m_ref;
+        if (base == -INFINITY) base = 0.0f;
         const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), base2 = pack2(-base, -base);
         uint64_t sums[4] = {};
 #pragma unroll
@@ -695,7 +709,7 @@ extern "C" void mv_prompt_plan_destroy(mv_prompt_plan* p) {
 extern "C" mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int32_t n_kv_heads,
                                       int32_t head_dim, const mv_prompt_plan* plan, float scale, mv_rows out,
                                       mv_stream stream) {
-  if (!plan || !(scale >= 0.0f && scale < INFINITY)) return MV_ERR_INVALID_ARG;
+  if (!plan || !(scale >= 0.0f && scale * kLog2E < INFINITY)) return MV_ERR_INVALID_ARG;
   if (n_kv_heads < 1 || n_heads < 1 || n_heads > kPagedMaxHeads || (int64_t)n_kv_heads * plan->group != n_heads)
     return MV_ERR_SHAPE;
   if (head_dim < 8 || head_dim > kPagedMaxDim || head_dim % 8) return MV_ERR_SHAPE;
@@ -715,8 +729,8 @@ extern "C" mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n
   a.group = plan->group;
   a.kv_heads = n_kv_heads;
   a.dim = head_dim;
-  // a masked score is -inf: with a scale of zero the smallest weight in the exponent keeps -inf * scale what it is
-  a.scale_log2 = fmaxf(scale * 1.4426950408889634f, 1e-30f);
+  // a masked score is -inf, and 0 * -inf would be a NaN: the smallest scale in place of zero, with which no score is anything
+  a.scale_log2 = fmaxf(scale * kLog2E, 1.4e-45f);
   a.err = mv_error_word();
   const int64_t grid = (int64_t)(plan->items.size() / 4) * n_kv_heads;  // at most 2^22 * 2^8
   CUtensorMap maps[3];

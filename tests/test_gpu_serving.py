@@ -102,6 +102,32 @@ def test_prompt_scales(scale, std):
     check_prompt(q, k, v, out, lens, scale)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale,k0", [(1.0, 2.0 ** 20), (0.125, 2.0 ** 9), (1.0, 2.0 ** 40), (0.125, -2.0 ** 20), (2e38, 2.0 ** -110),
+                                      (0.0, 2.0 ** 100), (1e-37, 2.0 ** 90)])
+def test_scores_of_any_size(d, scale, k0):
+    """Scores that fp32 holds exactly, from tiny to larger than 2^24: each is one product, and two keys' differ by nothing
+    or by k0 / 8 times 2^20 scale. So a softmax's weights are known to the rounding of an exponent of at most 2^-23 |score|,
+    and where the scores differ by more than 2^10 they are 0 and 1; below that here no score is over 2^7."""
+    n, hq, hk = 400, 2, 1
+    q, k = torch.zeros(n, hq, d, device="cuda"), torch.zeros(n, hk, d, device="cuda")
+    q[:, :, 0] = 2.0 ** 20
+    k[:, :, 0] = k0 * (1 + (torch.arange(n, device="cuda") * 5 % 7)[:, None] / 8)
+    q, k, v = q.to(torch.bfloat16), k.to(torch.bfloat16), normal(3, n, hk, d)
+    got = torch.empty_like(q)
+    mv.prompt_attention(q, k, v, mv.PromptPlan([n], hq), scale, got)
+    pool = Pool([n], hk, d, 16, BF16)
+    mv.paged_kv_append(k, v, i32([0, n]), pool.cache, pool.d_table, pool.d_lens)
+    one = run_paged(pool, q[-1:].contiguous(), scale)
+    scale = float(np.float32(scale))
+    top = abs(k0) * 2.0 ** 21 * scale                         # more than any score
+    assert top < 2.0 ** 7 or top / 16 > 2.0 ** 10
+    ref, mag = serving.prompt_attention(f64(q), f64(k), f64(v), [n], scale)
+    tol = U * np.abs(ref) + (U + (top * 2.0 ** -21 if top < 2.0 ** 7 else 0.0) + (n + 8) * 2.0 ** -23) * mag
+    assert (np.abs(f64(got) - ref) <= tol).all()
+    assert (np.abs(f64(one)[0] - ref[-1]) <= tol[-1]).all()
+
+
 def test_prompt_rising_scores():
     """Each later key scores higher, so every tile moves the running maximum."""
     n, d = 900, 64

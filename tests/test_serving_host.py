@@ -197,6 +197,13 @@ def test_prompt_attention_refusals():
     assert call(p=empty.handle) == 0
 
 
+def test_scale_over_what_fp32_holds_as_a_power_of_two():
+    """Scores are exponents of two in fp32: log2(e) times a scale of 3e38 is none any more."""
+    plan = mv.PromptPlan([3, 200], 2)
+    assert attention(scale=3e38) == INVALID
+    assert mv.lib().prompt_attention(rows(), rows(), rows(), 4, 2, 128, plan.handle, 3e38, rows(), None) == INVALID
+
+
 def test_binding_refuses_what_the_library_cannot_see():
     t = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
