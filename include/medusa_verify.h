@@ -499,7 +499,7 @@ mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int
  * device error word, and what belongs to them is neither read nor written: paged_kv_append and paged_kv_read leave out
  * the rows of such a page or sequence, paged_attention all of out's rows of a sequence with such a length, or with such a
  * page before its end. The other sequences get what they get without it.
- * Limits: page_size % 16 == 0, 16 <= page_size <= 1024; head_dim % 16 == 0, 16 <= head_dim <= 128; 1 <= n_kv_heads <=
+ * Limits: page_size % 16 == 0, 16 <= page_size <= 1024; max_pages * page_size < 2^31 - 1024; head_dim % 16 == 0, 16 <= head_dim <= 128; 1 <= n_kv_heads <=
  * 256; 0 <= n_seq <= 4096; pools 16-byte aligned.
  */
 typedef struct mv_paged_kv {
@@ -531,7 +531,8 @@ mv_status paged_kv_read(const mv_paged_kv* cache, const int32_t* block_table, in
  * output sums in fp32. The weights have 16 bits for the product with v, over e4m3 pools 11 where fp16's normal range holds
  * all of a step's (16 to 64 keys) times their rows' scales. The result does not depend on the order in which the parts of a split sequence finish. scale
  * >= 0 and log2(e) * scale finite, here and in prompt_attention.
- * Limits: n_heads % n_kv_heads == 0, n_heads <= 256. workspace: device memory of paged_attention_workspace() bytes,
+ * Limits: n_heads % n_kv_heads == 0, n_heads <= 256; units * (max_pages * page_size / 128 + 19) < 2^31 with units =
+ * n_kv_heads * ceil(n_heads / n_kv_heads / 16). workspace: device memory of paged_attention_workspace() bytes,
  * 16-byte aligned, zero-filled before its first use (see the conventions above). Errors as above; MV_ERR_CAPACITY: the
  * workspace is too small. */
 mv_status paged_attention_workspace(int32_t n_seq, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,

@@ -47,7 +47,7 @@ constexpr int kUnitCost = 2;     // what a unit costs beside its steps, in steps
 constexpr int kShortSteps = 16;  // steps of one warp up to which a sequence may go a unit to each warp
 constexpr unsigned int kEvenMost = 20;  // places of a piece up to which all have one length
 constexpr int kMaxCtas = 160;    // counters at the start of the workspace; CTAs of a launch
-constexpr int kChunkSeq = 1024;  // sequences of one launch
+constexpr int kChunkSeq = 1024;  // sequences of one launch, at most
 constexpr int kClusterMost = 16;
 constexpr int kUnitLeast = -24;  // log2 of the sums' unit: from here to 0
 
@@ -89,6 +89,7 @@ struct Layout {
   static constexpr int kJoin = (8 * kMaxCtas + 8 * kThreads) * 4;
   static constexpr int kMerge = 4 * kSlot * 4 > kJoin ? 4 * kSlot * 4 : kJoin;
   static constexpr int kExpsAt = kQueue, kMergeAt = kExpsAt + kWarps * kStages * kExps, kPreAt = kMergeAt + kMerge;
+  static_assert(kWarps * kKeys == (kE4M3 ? (kDim > 64 ? 256 : 512) : (kDim > 64 ? 128 : 256)), "paged_attention's chunks");
   static_assert(kStage == 8192 && kSub * 2 * kBoxes <= 16 && 2 * kSub <= 16 && kMergeAt % 16 == 0, "");
   static int bytes(int n_seq) { return 1024 + kPreAt + (2 * n_seq + 1) * 4; }
 };
@@ -1015,6 +1016,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Places on the line that a sequence of all that the table holds would take, steps of `keys` keys.
+int64_t most_places(const AttnArgs& a, int keys) {
+  return (int64_t)a.c.heads * a.parts *
+         (((int64_t)a.c.max_pages * a.c.page_size + keys - 1) / keys + kUnitCost + kShortSteps);
+}
+
 // Clusters of `size` CTAs of the kernel that the device holds at once (found once for each device and size).
 template <int kDim, bool kE4M3, int kNT>
 int most_clusters(int size, int bytes) {
@@ -1048,11 +1055,8 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   const int bytes = Ly::bytes(args.c.n_seq);
   if (!mv_set_smem_once((const void*)paged_attn_kernel<kDim, kE4M3, kNT, false>, Ly::bytes(kChunkSeq), flags))
     return MV_ERR_CUDA;
-  const int units = args.c.heads * args.parts, sms = std::min(mv_sm_count(), kMaxCtas), step = kWarps * Ly::kKeys;
-  const int64_t most = (int64_t)args.c.n_seq * units *
-                       (((int64_t)args.c.max_pages * args.c.page_size + step - 1) / step + kUnitCost + kShortSteps);
-  if (most > 0x7fffffff) return MV_ERR_SHAPE;
-  const int grid = (int)std::min<int64_t>(most, sms);
+  const int units = args.c.heads * args.parts, sms = std::min(mv_sm_count(), kMaxCtas);
+  const int grid = (int)std::min<int64_t>(args.c.n_seq * most_places(args, kWarps * Ly::kKeys), sms);
   AttnArgs a = args;
   // Sequences short enough for one warp to a unit: while there are units for every warp, up to kShortSteps of its steps (128
   // sequences of 160 keys, 8 kv heads: 15 us, cut across warps 28; of half as many steps at most, 128 of up to 300 keys take
@@ -1150,8 +1154,11 @@ extern "C" mv_status paged_attention(mv_rows q, int32_t n_heads, const mv_paged_
   a.err = mv_error_word();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool e4m3 = cache->dtype == MV_DTYPE_E4M3, big = a.c.dim > 64;
-  for (int first = 0; first < n_seq; first += kChunkSeq) {
-    a.c.n_seq = std::min(kChunkSeq, n_seq - first);
+  // sequences of a launch: no more than have places in 31 bits, whatever their lengths
+  const int chunk = (int)std::min<int64_t>(kChunkSeq, 0x7fffffff / most_places(a, e4m3 ? (big ? 256 : 512) : (big ? 128 : 256)));
+  if (chunk < 1) return MV_ERR_SHAPE;
+  for (int first = 0; first < n_seq; first += chunk) {
+    a.c.n_seq = std::min(chunk, n_seq - first);
     a.c.table = block_table + (int64_t)first * ld_table;
     a.c.seq_lens = seq_lens + first;
     a.q = {static_cast<uint16_t*>(q.ptr) + first * q.token_stride, q.token_stride, q.head_stride};

@@ -660,6 +660,34 @@ def test_paged_attention_of_more_sequences_than_a_launch_takes(dtype, n_seq):
     check_paged(pool, q, out, 0.2)
 
 
+@pytest.mark.parametrize("dtype,cols", [(BF16, 1027), (E4M3, 2060)])
+def test_paged_attention_of_wide_tables(dtype, cols):
+    """1024 sequences of 256 kv heads under a table for a million positions each: more places on the line than 31 bits count
+    if all were in use, so it takes several launches. The sequences share their pages and are short."""
+    n_seq, hk, d, page = 1024, 256, 128, 1024
+    lens = [int(x) for x in np.random.default_rng(0).integers(0, 40, n_seq)]
+    lens[3], lens[1021] = 900, 700
+    cache = mv.PagedKV.zeros(2, page, hk, d, dtype)
+    k, v = normal(1, page, hk, d), normal(2, page, hk, d)
+    mv.paged_kv_append(k, v, i32([0, page]), cache, i32([[1]]), i32([page]))
+    held = [torch.empty_like(k) for _ in range(2)]
+    mv.paged_kv_read(cache, i32([[1]]), i32([page]), i32([0, page]), *held)
+    table = torch.full((n_seq, cols), -5, dtype=torch.int32, device="cuda")
+    table[:, 0] = 1
+    q = normal(3, n_seq, hk, d)
+    ws = torch.zeros(mv.paged_attention_workspace(n_seq, hk, hk, d), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 7.0)
+    mv.paged_attention(q, cache, table, i32(lens), 0.1, out, ws)
+    torch.cuda.synchronize()
+    for b in (0, 3, 500, 1010, 1018, 1019, 1020, 1021, 1023):
+        for h in (0, 101, 255):
+            n = lens[b]
+            one = f64(q[b:b + 1, h:h + 1])
+            ks, vs = (f64(x[:n, h]) for x in held)
+            ref, mag = serving.attend(one[:, 0], ks, vs, 0.1, np.ones((1, n), dtype=bool))
+            check(f64(out[b:b + 1, h]), ref, mag, one[0], ks[:, None], 0.1, n)
+
+
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
 @pytest.mark.parametrize("n", [0, 1, 15, 130, 1000, 2300])
 @pytest.mark.parametrize("hq,hk,d", [(32, 32, 128), (64, 8, 64), (16, 8, 128), (128, 128, 64), (64, 64, 32), (144, 9, 128)])

@@ -197,6 +197,12 @@ def test_prompt_attention_refusals():
     assert call(p=empty.handle) == 0
 
 
+def test_paged_attention_of_more_positions_than_places():
+    """256 units of 2^30 positions and more in one sequence: no launch could count them."""
+    c = cache(n_kv_heads=256, page_size=1024, dtype=mv.DTYPE_BF16)
+    assert attention(c, heads=256, q=rows(ts=1 << 20), out=rows(ts=1 << 20), ld=1 << 21, pages=(1 << 21) - 2, n_seq=1) == SHAPE
+
+
 def test_scale_over_what_fp32_holds_as_a_power_of_two():
     """Scores are exponents of two in fp32: log2(e) times a scale of 3e38 is none any more."""
     plan = mv.PromptPlan([3, 200], 2)
