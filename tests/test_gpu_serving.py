@@ -210,6 +210,47 @@ def test_prompt_rows_repeat_while_their_maximum_moves(d):
         assert torch.equal(out, first)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_every_call_of_many_at_once_is_done_in_full(d):
+    """Prompt and paged attention on four streams and from a graph with two calls, each call into rows of its own that held a
+    NaN before: what a call leaves out stays to be seen."""
+    nan, jobs = float("nan"), []
+    for seed, (n, most, hq, hk) in enumerate([(60, 400, 8, 8), (9, 2000, 8, 2), (150, 130, 12, 4)]):
+        lens = [int(x) for x in np.random.default_rng(seed).integers(1, most, n)]
+        q, k, v, want, scale = run_prompt(lens, hq, hk, d, seed=seed)
+        plan, outs = mv.PromptPlan(lens, hq // hk), [torch.full_like(want, nan) for _ in range(6)]
+        jobs.append((want, outs, torch.cuda.Stream(priority=-(seed % 2)),
+                     lambda out, stream=None, a=(q, k, v, plan, scale): mv.prompt_attention(*a, out, stream=stream)))
+    for lens, hq, hk, dtype in (([3000, 5], 8, 2, E4M3), ([2000], 32, 32, BF16), ([900] * 7 + [0], 6, 2, BF16)):
+        pool = Pool(lens, hk, d, 16, dtype).fill(len(lens))
+        q = normal(3, len(lens), hq, d)
+        ws = torch.zeros(mv.paged_attention_workspace(len(lens), hq, hk, d), dtype=torch.uint8, device="cuda")
+        want = run_paged(pool, q, 0.1, ws=ws)
+        jobs.append((want, [torch.full_like(want, nan) for _ in range(6)], torch.cuda.Stream(),
+                     lambda out, stream=None, a=(q, pool.cache, pool.d_table, pool.d_lens, 0.1), ws=ws:
+                     mv.paged_attention(*a, out, ws, stream=stream)))
+    g, graphed = torch.cuda.CUDAGraph(), [torch.full_like(jobs[0][0], nan) for _ in range(2)]
+    with torch.cuda.graph(g):
+        for out in graphed:
+            jobs[0][3](out)
+    seen = []
+    torch.cuda.synchronize()
+    for i in range(6):
+        for _, outs, stream, call in jobs:
+            call(outs[i], stream)
+        g.replay()
+        seen.append([out.clone() for out in graphed])
+        for out in graphed:
+            out.fill_(nan)
+    torch.cuda.synchronize()
+    for want, outs, _, _ in jobs:
+        for out in outs:
+            assert torch.equal(out, want)
+    for outs in seen:
+        for out in outs:
+            assert torch.equal(out, jobs[0][0])
+
+
 def test_prompt_leaves_rows_behind_the_plan():
     lens = [130, 20]
     q, k, v, out, scale = run_prompt(lens, 2, 2, 64, extra=45)
@@ -658,6 +699,43 @@ def test_paged_attention_of_more_sequences_than_a_launch_takes(dtype, n_seq):
     q = normal(3, n_seq, 2, 32)
     out = run_paged(pool, q, 0.2)
     check_paged(pool, q, out, 0.2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("hq,hk,d,page,lens", [
+    (16, 8, 128, 64, [9001, 7310, 0, 8800, 5, 9999, 6007, 8191]),      # 8 kv heads, units of some 70 steps (bf16)
+    (8, 8, 64, 16, [30011, 31, 28000, 160, 30500, 25001]),             # steps of 256 (512) keys
+    (20, 2, 128, 32, [33000, 700, 31017, 1, 29999, 20011, 26000, 30])])  # two tiles of heads a unit
+def test_paged_attention_of_long_pieces(dtype, hq, hk, d, page, lens):
+    """Pieces of more than 20 places, spread over all CTAs with some one longer, units cut into parts at any step and also
+    between their start and first step: a CTA's piece is total / 152 = 21 to 35 places, a unit's width n / step + 2."""
+    steps = {(BF16, 128): 128, (BF16, 64): 256, (E4M3, 128): 256, (E4M3, 64): 512}[dtype, d]
+    total = sum(hk * (2 + max(1, -(-n // steps))) for n in lens)
+    while total <= 21 * 152:                                  # 8-bit caches: as many sequences as that takes
+        total += sum(hk * (2 + max(1, -(-n // steps))) for n in lens)
+        lens = lens + lens
+    pool = Pool(lens, hk, d, page, dtype)
+    k, v = (normal(i, sum(lens), hk, d) * torch.exp2(normal(i + 9, sum(lens), hk, 1)) for i in (1, 2))
+    mv.paged_kv_append(k, v, i32(np.cumsum([0] + lens)), pool.cache, pool.d_table, pool.d_lens)
+    q = normal(3, len(lens), hq, d)
+    ws = torch.zeros(mv.paged_attention_workspace(len(lens), hq, hk, d), dtype=torch.uint8, device="cuda")
+    out = run_paged(pool, q, d ** -0.5, ws=ws)
+    assert torch.equal(run_paged(pool, q, d ** -0.5, ws=ws), out)
+    for b, n in enumerate(lens[:8]):                          # every sequence's first, some of its further kv heads
+        if n == 0:
+            assert (out[b] == 0).all()
+            continue
+        ids = torch.as_tensor(pool.table[b, : -(-n // page)], device="cuda").long()
+        for c in sorted({0, b % hk, hk - 1}):
+            rows, heads = [], slice(c * (hq // hk), (c + 1) * (hq // hk))
+            for x, e in ((pool.cache.k, pool.cache.k_exp), (pool.cache.v, pool.cache.v_exp)):
+                r = (x.view(torch.uint8)[ids, c].view(x.dtype) if dtype == E4M3 else x[ids, c]).float().double()
+                if dtype == E4M3:
+                    r = r * torch.exp2(e[ids, c].double() - 127)[..., None]
+                rows.append(r.reshape(-1, d)[:n].cpu().numpy())
+            one = f64(q[b, heads])
+            ref, mag = serving.attend(one, *rows, d ** -0.5, np.ones((len(one), n), dtype=bool))
+            check(f64(out[b, heads]), ref, mag, one, rows[0][:, None], d ** -0.5, n)
 
 
 @pytest.mark.parametrize("dtype,cols", [(BF16, 1027), (E4M3, 2060)])
