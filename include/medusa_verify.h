@@ -487,9 +487,9 @@ mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int
  * ============================================================================================
  * The pool: k, v device [n_pages][n_kv_heads][page_size][head_dim], bf16 or e4m3 (MV_DTYPE_E4M3: one sign, four
  * exponent, three fraction bits, no infinities). An e4m3 pool has an exponent byte for every row, k_exp, v_exp device
- * [n_pages][n_kv_heads][page_size]: the row stands for x8 * 2^(byte - 127), byte 0 .. 254. Writing a row x takes the smallest e in
- * [-100, 120] with max|x| <= 448 * 2^e (NaNs apart; a row of zeros: -100) and rounds x * 2^-e to the nearest e4m3, ties
- * to even. The scale is a power of two, so what a row stands for is exact in bf16 (where its exponent reaches). A NaN
+ * [n_pages][n_kv_heads][page_size]: the row stands for x8 * 2^(byte - 127), byte 0 .. 254. Writing a row x takes the
+ * smallest e in [-100, 120] with max|x| <= 448 * 2^e (NaNs apart; a row of zeros: -100) and rounds x * 2^-e to the
+ * nearest e4m3, ties to even. The scale is a power of two, so what a row stands for is exact in bf16 (where its exponent reaches). A NaN
  * stays a NaN, an infinity becomes 448 * 2^120, which reads back as an infinity.
  * The sequences: block_table device int32 [n_seq][ld_table], the first max_pages entries of a row used: position p
  * of sequence b lies in page block_table[b][p / page_size] at slot p % page_size; seq_lens device int32 [n_seq]: each
@@ -498,9 +498,9 @@ mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int
  * there out of range (a page outside the pool, a length that is negative or over max_pages * page_size), they set the
  * device error word, and what belongs to them is neither read nor written: paged_kv_append and paged_kv_read leave out
  * the rows of such a page or sequence, paged_attention all of out's rows of a sequence with such a length, or with such a
- * page before its end. The other sequences get what they get without it.
- * Limits: page_size % 16 == 0, 16 <= page_size <= 1024; max_pages * page_size < 2^31 - 1024; head_dim % 16 == 0, 16 <= head_dim <= 128; 1 <= n_kv_heads <=
- * 256; 0 <= n_seq <= 4096; pools 16-byte aligned.
+ * page before its end. The other sequences are done as ever.
+ * Limits: page_size % 16 == 0, 16 <= page_size <= 1024; max_pages * page_size < 2^31 - 1024; head_dim % 16 == 0,
+ * 16 <= head_dim <= 128; 1 <= n_kv_heads <= 256; 0 <= n_seq <= 4096; pools 16-byte aligned.
  */
 typedef struct mv_paged_kv {
   void *k, *v;
@@ -515,6 +515,7 @@ typedef struct mv_paged_kv {
  * a page that two sequences share must not be written by both in one call (either row may stay, or a mix).
  * paged_kv_read turns rows back into bf16: a parked sequence into packed rows, or into a session's [H][S][D] planes.
  * cu_rows out of order or past n_rows, or a sequence with more rows than seq_lens[b], set the device error word.
+ * A call of no rows or no sequences does nothing, whatever its other arguments.
  * Errors: MV_ERR_INVALID_ARG (null, unaligned, bad strides or dtype), MV_ERR_SHAPE (see the limits), MV_ERR_CUDA. */
 mv_status paged_kv_append(mv_rows k, mv_rows v, int32_t n_rows, const int32_t* cu_rows, const mv_paged_kv* cache,
                           const int32_t* block_table, int32_t ld_table, int32_t max_pages, const int32_t* seq_lens,
@@ -529,8 +530,8 @@ mv_status paged_kv_read(const mv_paged_kv* cache, const int32_t* block_table, in
  * not matter, NaN included; an infinity or a NaN in a value row that is attended to makes that element of out one of the two.
  * q, out device bf16 rows, token b = sequence b; out must not overlap q or the cache. Scores, softmax statistics and
  * output sums in fp32. The weights have 16 bits for the product with v, over e4m3 pools 11 where fp16's normal range holds
- * all of a step's (16 to 64 keys) times their rows' scales. The result does not depend on the order in which the parts of a split sequence finish. scale
- * >= 0 and log2(e) * scale finite, here and in prompt_attention.
+ * all of a step's (16 to 64 keys) times their rows' scales. The result does not depend on the order in which the parts of
+ * a split sequence finish. scale >= 0 and log2(e) * scale finite, here and in prompt_attention.
  * Limits: n_heads % n_kv_heads == 0, n_heads <= 256; units * (max_pages * page_size / 128 + 19) < 2^31 with units =
  * n_kv_heads * ceil(n_heads / n_kv_heads / 16). workspace: device memory of paged_attention_workspace() bytes,
  * 16-byte aligned, zero-filled before its first use (see the conventions above). Errors as above; MV_ERR_CAPACITY: the

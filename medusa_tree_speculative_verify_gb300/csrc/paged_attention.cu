@@ -1,7 +1,7 @@
 // Attention of one new token for each sequence over a paged cache (bf16, or e4m3 with an exponent for each row).
 //
-// Bound by the cache's bytes: every row is read once. What a kv head's query heads share is read for all of them
-// together, 8 (or 16) heads a work unit, on the tensor cores with the keys as the rows of the products (mma.sync
+// Bound by the cache's bytes: every row is read once for up to 16 query heads of a kv head (once for each 16 of more). What
+// they share is read for all of them together, 8 (or 16) heads a work unit, on the tensor cores with the keys as the rows of the products (mma.sync
 // m16n8k16): S^T = K Q^T and O^T += V^T P^T. At 8 heads a unit the products cost 16 to 24 instructions for each 16 keys'
 // 4 to 8 KB, far below what the copies take, and keys as rows waste nothing on padding the heads.
 //

@@ -8,10 +8,11 @@
 // only when the row maximum has grown by more than 2^8; then they rescale their row of O in place. Weights are rounded to
 // bf16 since both operands of a product have one type; the sums stay in fp32.
 //
-// 8192 tokens of 32 heads of 128 over 8: 308 us, 1.78 PFLOP/s; of 64: 238 us, 1.16 PFLOP/s. With 128-wide heads the products,
-// their issue and the softmax's chain (read S, maximum, exponentials, write P) bound it alike; with 64-wide ones the softmax,
-// which has as many exponentials for half the products. Short prompts (24 of up to 300 tokens, 32 heads: 19 us) are bound by
-// that chain's latency, of which an item has two or three tiles in a row.
+// 8192 tokens of 32 heads of 128 over 8: 312 us, 1.76 PFLOP/s, in a burst (344 us once the power cap acts); of 64: 245 us, 1.12
+// PFLOP/s. With 128-wide heads the products, their issue and the softmax's chain (read S, maximum, exponentials, write P) bound
+// it alike. With 64-wide ones nothing is near full (tensor cores 41 % of the cycles, exponentials' pipe 42 %, issue 61 %): it is
+// that chain's latency, with a barrier between the two threads of a row, and its six instructions a score, for half the
+// products. Short prompts (24 of up to 300 tokens, 32 heads: 19 us) are bound by the chain too, two or three tiles in a row an item.
 #include <math.h>
 
 #include <algorithm>
@@ -81,7 +82,7 @@ constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;  // 4 * 104 + 64 <= 5 * 96, w
 constexpr uint32_t kTmemCols = 512;
 
 // The descriptor d with its address moved on, in units of 16 bytes, within the field: one 32-bit addition (8192 tokens of
-// 64-wide heads 250 -> 238 us; what the issuing warp computes between products is lost)
+// 64-wide heads 250 -> 238 us when it came; what the issuing warp computes between products is lost)
 MV_DEV uint64_t desc_plus(uint64_t d, uint32_t by) { return (d & 0xffffffff00000000ull) | (uint32_t)((uint32_t)d + by); }
 
 constexpr float kRescaleLog2 = 8.0f;  // move the exponent reference when the row maximum grows by more than this
