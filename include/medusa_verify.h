@@ -293,7 +293,12 @@ typedef struct mv_model mv_model;
 typedef struct mv_session mv_session;
 
 /* Storage and arithmetic type of a model: its weights, activations and KV cache. */
-typedef enum { MV_DTYPE_BF16 = 0, MV_DTYPE_F32 = 1, MV_DTYPE_E4M3 = 2 /* paged caches only */ } mv_dtype;
+typedef enum {
+  MV_DTYPE_BF16 = 0,
+  MV_DTYPE_F32 = 1,
+  MV_DTYPE_E4M3 = 2, /* paged caches only, like the next */
+  MV_DTYPE_E2M1 = 3
+} mv_dtype;
 
 /* Limits: d % 8 == 0, d <= 8192, head_dim in {16, 32, 64, 128}, ffn % 8 == 0, 1 <= n_medusa <= 8; every
  * pointer 16-byte aligned. MV_ERR_SHAPE otherwise. Builds the weights' TMA descriptors (host only). */
@@ -491,6 +496,13 @@ mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int
  * smallest e in [-100, 120] with max|x| <= 448 * 2^e (NaNs apart; a row of zeros: -100) and rounds x * 2^-e to the
  * nearest e4m3, ties to even. The scale is a power of two, so what a row stands for is exact in bf16 (where its exponent reaches). A NaN
  * stays a NaN, an infinity becomes 448 * 2^120, which reads back as an infinity.
+ * An e2m1 pool (MV_DTYPE_E2M1: one sign, two exponent, one fraction bit; 0, 0.5, 1, 1.5, 2, 3, 4, 6) holds two elements a
+ * byte, the first in the low half: k, v [n_pages][n_kv_heads][page_size][head_dim / 2], and a scale byte for each group of 16
+ * elements of a row, k_exp, v_exp [n_pages][n_kv_heads][page_size][head_dim / 16]. A scale byte is the 5 exponent and the
+ * first 3 fraction bits of an fp16 value (byte << 7 is that value). Writing takes the scale nearest to max|x| / 6, at most
+ * 10240, ties to even, and rounds x / scale to the nearest e2m1, ties to even (6 for what is larger). What a row stands for
+ * is exact in bf16 and in fp16. A group with a NaN or an infinity gets the scale byte 255 and reads back as NaNs. The bytes
+ * are 0 .. 0xE2, or 255: attention over others gives infinities or NaNs.
  * The sequences: block_table device int32 [n_seq][ld_table], the first max_pages entries of a row used: position p
  * of sequence b lies in page block_table[b][p / page_size] at slot p % page_size; seq_lens device int32 [n_seq]: each
  * sequence's length, the rows of this call included. Entries past a sequence's last page are not read.
@@ -500,12 +512,12 @@ mv_status prompt_attention(mv_rows q, mv_rows k, mv_rows v, int32_t n_heads, int
  * the rows of such a page or sequence, paged_attention all of out's rows of a sequence with such a length, or with such a
  * page before its end. The other sequences are done as ever.
  * Limits: page_size % 16 == 0, 16 <= page_size <= 1024; max_pages * page_size < 2^31 - 1024; head_dim % 16 == 0,
- * 16 <= head_dim <= 128; 1 <= n_kv_heads <= 256; 0 <= n_seq <= 4096; pools 16-byte aligned.
+ * 16 <= head_dim <= 128 (e2m1: head_dim % 32 == 0); 1 <= n_kv_heads <= 256; 0 <= n_seq <= 4096; pools 16-byte aligned.
  */
 typedef struct mv_paged_kv {
   void *k, *v;
-  uint8_t *k_exp, *v_exp; /* e4m3 pools; NULL for bf16 */
-  int32_t dtype;          /* MV_DTYPE_BF16 or MV_DTYPE_E4M3 */
+  uint8_t *k_exp, *v_exp; /* e4m3 pools: exponents; e2m1 pools: scales; NULL for bf16 */
+  int32_t dtype;          /* MV_DTYPE_BF16, MV_DTYPE_E4M3 or MV_DTYPE_E2M1 */
   int32_t n_pages, page_size, n_kv_heads, head_dim;
 } mv_paged_kv;
 
@@ -541,6 +553,52 @@ mv_status paged_attention_workspace(int32_t n_seq, int32_t n_heads, int32_t n_kv
 mv_status paged_attention(mv_rows q, int32_t n_heads, const mv_paged_kv* cache, const int32_t* block_table,
                           int32_t ld_table, int32_t max_pages, const int32_t* seq_lens, int32_t n_seq, float scale,
                           mv_rows out, void* workspace, size_t ws_bytes, mv_stream stream);
+
+/* ============================================================================================
+ * Lengths, block table and free pages of sequences that grow and shrink
+ * ============================================================================================
+ * Before a step: each sequence b takes by[b] more tokens (a tree's, a prompt's), or gives -by[b] up (what a verify step did
+ * not accept; all of it when the request is done). The pages are those of the section before; one table serves the caches
+ * of all layers. free_pages device int32 [1 + n_pages]: how many pages are free, then that stack of them, the next one to be
+ * taken last. A sequence of n tokens holds ceil(n / page_size) pages, each page belongs to one sequence or to the stack.
+ * The call, in this order:
+ *   1. pages behind a shorter length are pushed on the stack, the last sequence's first and a sequence's last page first;
+ *   2. pages for a greater length are popped, the first sequence's first, into its row of block_table;
+ *   3. seq_lens[b] += by[b]; cu_rows device int32 [n_seq + 1] or NULL: sums of max(by, 0) before each sequence, and all;
+ *   4. for row i of sequence b that comes, row r = cu_rows[b] + i of a step's packed rows: positions[r] = its position, and
+ *      slots[r] = page * page_size + slot in it; -1 in rows cu_rows[n_seq] .. n_rows - 1. Device int32 and int64 [n_rows],
+ *      each may be NULL; with either, cu_rows is wanted.
+ * So growing and then shrinking by the same numbers leaves the stack as it was, and rows, lengths and table are what
+ * paged_kv_append and qk_norm_rope take. Table entries and stack places that are given up keep their last value.
+ * Everything is read on the device, so the call can be captured and replayed. Where a length would leave 0 .. max_pages *
+ * page_size, the pages do not suffice (or are more than n_pages), or there are more than n_rows rows, nothing of this is
+ * done: the device error word is set, cu_rows is all zeros, positions and slots are all -1, the rest is as it was. A page
+ * number outside the pool is moved like another, and sets the error word.
+ * Limits: page_size as above, 0 <= n_seq <= 4096, n_pages >= 1. The arrays do not overlap.
+ * Errors: MV_ERR_INVALID_ARG (null, unaligned, negative), MV_ERR_SHAPE, MV_ERR_CUDA. */
+mv_status paged_kv_resize(const int32_t* by, int32_t n_seq, int32_t page_size, int32_t n_pages, int32_t* block_table,
+                          int32_t ld_table, int32_t max_pages, int32_t* seq_lens, int32_t* free_pages, int32_t* cu_rows,
+                          int32_t* positions, int64_t* slots, int32_t n_rows, mv_stream stream);
+
+/* ============================================================================================
+ * Norms of the heads of Q and K, and their rotation by position
+ * ============================================================================================
+ * For each token's head x of head_dim elements, q's with q_gain and k's with k_gain (device bf16 [head_dim]; NULL: ones):
+ *   y = x / sqrt(mean(x^2) + eps) * gain, then of the first rot_dim elements each pair (a, b) = (y[i], y[i + rot_dim / 2]),
+ *   or (y[2 i], y[2 i + 1]) with neighbours = 1, becomes (a cos w - b sin w, a sin w + b cos w), w = positions[t] * f_i.
+ * In fp32, rounded to bf16 once (|x| below 2^60, so that fp32 holds the sum of squares). turns device [rot_dim / 2]: f_i / (2
+ * pi) in units of 2^-64, the angle of one position as a part of a turn; the product with a position is taken modulo whole
+ * turns, so it is exact for every position. rot_dim = 0: the norm alone, turns may be NULL. positions device int32
+ * [n_tokens]; the rows of a token with a negative one (padding, see paged_kv_resize) are left as they were. With rot_dim = 0
+ * positions may be NULL.
+ * q_out and k_out may be q and k themselves (the same address and strides), and must not overlap them otherwise.
+ * Limits: head_dim % 16 == 0, 16 <= head_dim <= 256; rot_dim % 16 == 0, rot_dim <= head_dim; 0 <= n_heads, n_kv_heads <= 256
+ * (rows of no heads are not looked at); eps >= 0; rows as in prompt_attention, gains 16-byte aligned.
+ * Errors: MV_ERR_INVALID_ARG (null, unaligned, bad strides), MV_ERR_SHAPE, MV_ERR_CUDA. */
+mv_status qk_norm_rope(mv_rows q, mv_rows k, int32_t n_tokens, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                       const mv_bf16* q_gain, const mv_bf16* k_gain, float eps, const int32_t* positions,
+                       const uint64_t* turns, int32_t rot_dim, int32_t neighbours, mv_rows q_out, mv_rows k_out,
+                       mv_stream stream);
 
 /* ============================================================================================
  * Errors

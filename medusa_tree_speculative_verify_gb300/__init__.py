@@ -8,6 +8,7 @@ or fails to load, :func:`lib` raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -21,7 +22,7 @@ __all__ = ["lib", "MVError", "Tree", "AcceptParams", "PosteriorResult", "GREEDY"
            "tree_attention_workspace", "evaluate_posterior", "evaluate_posterior_workspace", "kv_compact",
            "get_error", "fill_normal", "selftest_wait_timeout", "DTYPE_BF16", "DTYPE_F32", "DTYPE_E4M3", "MAX_NODES",
            "PromptPlan", "prompt_attention", "PagedKV", "paged_kv_append", "paged_kv_read", "paged_attention",
-           "paged_attention_workspace",
+           "paged_attention_workspace", "paged_kv_resize", "Rope", "qk_norm_rope", "DTYPE_E2M1",
            "MAX_DEPTH", "EXPORTED_SYMBOLS"]
 
 MAX_NODES = 256
@@ -29,7 +30,7 @@ NOALLOC_MAX_NODES = 64
 MAX_DEPTH = 8
 MASK_WORDS = 4
 GREEDY, TYPICAL = 0, 1
-DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
+DTYPE_BF16, DTYPE_F32, DTYPE_E4M3, DTYPE_E2M1 = 0, 1, 2, 3
 ROOT_ARGMAX, ROOT_TYPICAL, ROOT_NUCLEUS = 0, 1, 2
 
 _lib = None
@@ -140,6 +141,8 @@ _SIGS = {
     "paged_kv_read": ([ctypes.POINTER(_PagedKVDesc), _P, _I, _I, _P, _I, _P, _I, _Rows, _Rows, _P], _I),
     "paged_attention_workspace": ([_I, _I, _I, _I, ctypes.POINTER(_S)], _I),
     "paged_attention": ([_Rows, _I, ctypes.POINTER(_PagedKVDesc), _P, _I, _I, _P, _I, _F, _Rows, _P, _S, _P], _I),
+    "paged_kv_resize": ([_P, _I, _I, _I, _P, _I, _I, _P, _P, _P, _P, _P, _I, _P], _I),
+    "qk_norm_rope": ([_Rows, _Rows, _I, _I, _I, _I, _P, _P, _F, _P, _P, _I, _I, _Rows, _Rows, _P], _I),
     "mv_get_error": ([ctypes.POINTER(_U)], _I),
     "mv_get_error_detail": ([ctypes.POINTER(_U)], _I),
     "mv_selftest_wait_timeout": ([_U, _P, _P], _I),
@@ -499,21 +502,23 @@ def prompt_attention(q, k, v, plan: PromptPlan, scale, out, stream=None):
 
 class PagedKV:
     """One layer's paged cache over the caller's tensors: k, v [n_pages, kv heads, page_size, D], bf16 or
-    torch.float8_e4m3fn; for the latter k_exp, v_exp uint8 [n_pages, kv heads, page_size] (see mv_paged_kv)."""
+    torch.float8_e4m3fn; for the latter k_exp, v_exp uint8 [n_pages, kv heads, page_size]. Or 4 bits: k, v uint8 [n_pages,
+    kv heads, page_size, D / 2], k_exp, v_exp uint8 [n_pages, kv heads, page_size, D / 16] (see mv_paged_kv)."""
 
     def __init__(self, k, v, k_exp=None, v_exp=None):
         torch = _load_torch()
-        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v.dtype != k.dtype:
-            raise ValueError(f"PagedKV: k and v are both bf16 or both float8_e4m3fn, got {k.dtype} and {v.dtype}")
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8) or v.dtype != k.dtype:
+            raise ValueError(f"PagedKV: k and v are both bf16, both float8_e4m3fn or both uint8, got {k.dtype} and {v.dtype}")
         if k.dim() != 4 or v.shape != k.shape or not k.is_cuda:
             raise ValueError(f"PagedKV: k and v are CUDA tensors [n_pages, kv heads, page_size, head_dim], got "
                              f"{tuple(k.shape)} and {tuple(v.shape)} on {k.device}")
-        e4m3 = k.dtype == torch.float8_e4m3fn
+        dtype = {torch.bfloat16: DTYPE_BF16, torch.float8_e4m3fn: DTYPE_E4M3, torch.uint8: DTYPE_E2M1}[k.dtype]
+        want = None if dtype == DTYPE_BF16 else k.shape[:3] if dtype == DTYPE_E4M3 else (*k.shape[:3], k.shape[3] // 8)
         for name, e in (("k_exp", k_exp), ("v_exp", v_exp)):
-            if (e is not None) != e4m3:
-                raise ValueError(f"PagedKV: {name} belongs to e4m3 pages and to no others")
-            if e is not None and (e.dtype != torch.uint8 or e.shape != k.shape[:3]):
-                raise ValueError(f"PagedKV: {name} is uint8 {tuple(k.shape[:3])}, got {e.dtype} {tuple(e.shape)}")
+            if (e is not None) != (want is not None):
+                raise ValueError(f"PagedKV: {name} belongs to e4m3 and 4-bit pages and to no others")
+            if e is not None and (e.dtype != torch.uint8 or e.shape != want):
+                raise ValueError(f"PagedKV: {name} is uint8 {tuple(want)}, got {e.dtype} {tuple(e.shape)}")
         tensors = [t for t in (k, v, k_exp, v_exp) if t is not None]
         if any(t.device != k.device for t in tensors):
             raise ValueError(f"PagedKV: tensors on different devices: {[str(t.device) for t in tensors]}")
@@ -521,21 +526,27 @@ class PagedKV:
             raise ValueError("PagedKV: the pages must be contiguous")
         self.k, self.v, self.k_exp, self.v_exp, self.device = k, v, k_exp, v_exp, k.get_device()
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
-        self._desc = _PagedKVDesc(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if e4m3 else None,
-                                  v_exp.data_ptr() if e4m3 else None, DTYPE_E4M3 if e4m3 else DTYPE_BF16,
-                                  self.n_pages, self.page_size, self.n_kv_heads, self.head_dim)
+        if dtype == DTYPE_E2M1:
+            self.head_dim *= 2
+        self._desc = _PagedKVDesc(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if want is not None else None,
+                                  v_exp.data_ptr() if want is not None else None, dtype, self.n_pages, self.page_size,
+                                  self.n_kv_heads, self.head_dim)
         self._ref = ctypes.byref(self._desc)
 
     @classmethod
     def zeros(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=DTYPE_BF16, device="cuda"):
-        """A pool of zero pages, DTYPE_BF16 or DTYPE_E4M3."""
+        """A pool of zero pages, DTYPE_BF16, DTYPE_E4M3 or DTYPE_E2M1."""
         import torch
-        if dtype not in (DTYPE_BF16, DTYPE_E4M3):
-            raise ValueError(f"PagedKV.zeros: DTYPE_BF16 or DTYPE_E4M3, got {dtype}")
+        if dtype not in (DTYPE_BF16, DTYPE_E4M3, DTYPE_E2M1):
+            raise ValueError(f"PagedKV.zeros: DTYPE_BF16, DTYPE_E4M3 or DTYPE_E2M1, got {dtype}")
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         if dtype == DTYPE_BF16:
             return cls(torch.zeros(shape, dtype=torch.bfloat16, device=device),
                        torch.zeros(shape, dtype=torch.bfloat16, device=device))
+        if dtype == DTYPE_E2M1:
+            if head_dim % 32:
+                raise ValueError(f"PagedKV.zeros: 4-bit rows have a multiple of 32 elements, got {head_dim}")
+            return cls(*(torch.zeros(*shape[:3], head_dim // w, dtype=torch.uint8, device=device) for w in (2, 2, 16, 16)))
         k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
         ke, ve = (torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in range(2))
         return cls(k, v, ke, ve)
@@ -579,6 +590,92 @@ def paged_attention(q, cache: PagedKV, block_table, seq_lens, scale, out, worksp
         raise ValueError(f"paged_attention: a contiguous workspace on CUDA device {dev} is wanted")
     _call_on(dev, stream, lib().paged_attention, _rows(q, "q", dev, heads, d, n), heads, cache._ref, *seqs, scale,
              _rows(out, "out", dev, heads, d, n), workspace.data_ptr(), workspace.nbytes)
+
+
+def paged_kv_resize(by, cache: PagedKV, block_table, seq_lens, free_pages, cu_rows=None, positions=None, slots=None,
+                    stream=None):
+    """Each sequence grows or shrinks by ``by`` int32 [n_seq] tokens: seq_lens, block_table and free_pages int32 [1 +
+    n_pages] (how many are free, then the stack of them) follow; cu_rows int32 [n_seq + 1], positions int32 [rows] and slots
+    int64 [rows] are written for the rows that come, -1 behind the last one. ``cache``: any of the layers' caches."""
+    dev, seqs = cache.device, cache._seqs(block_table, seq_lens)
+    n, rows, at = seqs[4], 0, [None, None, None]
+    if cu_rows is not None:
+        at[0] = _ints(cu_rows, "cu_rows", dev, (n + 1,))
+    elif positions is not None or slots is not None:
+        raise ValueError("paged_kv_resize: positions and slots are of the rows that cu_rows counts")
+    if positions is not None:
+        rows = positions.numel()
+        at[1] = _ints(positions, "positions", dev, (rows,))
+    if slots is not None:
+        if slots.dtype is not _torch.int64 or slots.get_device() != dev or not slots.is_contiguous() or slots.dim() != 1 or \
+                (positions is not None and slots.numel() != rows):
+            raise ValueError(f"slots: a contiguous int64 tensor on CUDA device {dev} of as many rows as positions is wanted, "
+                             f"got {slots.dtype} {tuple(slots.shape)} on {slots.device}")
+        rows = slots.numel()
+        at[2] = slots.data_ptr()
+    _call_on(dev, stream, lib().paged_kv_resize, _ints(by, "by", dev, (n,)), n, cache.page_size, cache.n_pages, *seqs[:4],
+             _ints(free_pages, "free_pages", dev, (1 + cache.n_pages,)), *at, rows)
+
+
+class Rope:
+    """How far a position turns each pair of the first ``rot_dim`` elements of a head: by theta^(-2 i / rot_dim), or by
+    ``freqs`` (radians for one position, rot_dim / 2 of them). Pairs are (i, i + rot_dim / 2), or with ``neighbours``
+    (2 i, 2 i + 1). Held on the current device, or on ``device``, as parts of a turn in 64 bits (see qk_norm_rope)."""
+
+    def __init__(self, rot_dim, theta=10000.0, neighbours=False, freqs=None, device=None):
+        torch = _load_torch()
+        if rot_dim < 16 or rot_dim % 16:
+            raise ValueError(f"Rope: rot_dim is a multiple of 16, got {rot_dim}")
+        if freqs is None:
+            if not (theta > 0 and math.isfinite(theta)):
+                raise ValueError(f"Rope: theta is positive and finite, got {theta}")
+            freqs = [theta ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != rot_dim // 2 or not all(math.isfinite(f) for f in freqs):
+            raise ValueError(f"Rope: {rot_dim // 2} finite frequencies are wanted, got {freqs}")
+        turns = [round(f / (2 * math.pi) % 1.0 * 2 ** 64) % 2 ** 64 for f in freqs]
+        self.rot_dim, self.neighbours = rot_dim, bool(neighbours)
+        self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns], dtype=torch.int64,
+                                  device="cuda" if device is None else device)
+        self._at = self.turns.data_ptr(), rot_dim, int(self.neighbours)
+
+
+_NO_ROWS = _Rows(None, 0, 0)
+
+
+def qk_norm_rope(q, k, q_gain, k_gain, eps, positions, rope: Rope, q_out=None, k_out=None, stream=None):
+    """Heads of q bf16 [tokens, heads, D] and k bf16 [tokens, kv heads, D] divided by their root mean square, times q_gain
+    and k_gain (bf16 [D] or None), turned by positions int32 [tokens] as ``rope`` says (None: not turned), into q_out and
+    k_out or in place. Rows of a negative position are left as they were. q or k may be None."""
+    if _torch is None:
+        _load_torch()
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("qk_norm_rope: q and k are both None")
+    (t, _), d, dev = _heads(x, "q" if q is not None else "k"), x.shape[2], x.get_device()
+
+    def rows(x, to, gain, what):
+        if x is None:
+            if to is not None or gain is not None:
+                raise ValueError(f"qk_norm_rope: {what} is None, its gain or output is not")
+            return _NO_ROWS, 0, None, _NO_ROWS
+        h = _heads(x, what)[1]
+        src = _rows(x, what, dev, h, d, t)
+        if gain is not None and (gain.dtype is not _torch.bfloat16 or gain.shape != (d,) or gain.get_device() != dev or
+                                 not gain.is_contiguous()):
+            raise ValueError(f"{what}_gain: a contiguous bf16 tensor [{d}] on CUDA device {dev} is wanted, got {gain.dtype} "
+                             f"{tuple(gain.shape)} on {gain.device}")
+        return src, h, None if gain is None else gain.data_ptr(), src if to is None else _rows(to, what + "_out", dev, h, d, t)
+
+    q_in, hq, qg, q_to = rows(q, q_out, q_gain, "q")
+    k_in, hk, kg, k_to = rows(k, k_out, k_gain, "k")
+    if rope is not None and rope.turns.get_device() != dev:
+        raise ValueError(f"qk_norm_rope: the rope is on {rope.turns.device}, the tensors are on CUDA device {dev}")
+    if positions is None and rope is not None:
+        raise ValueError("qk_norm_rope: a rotation wants positions")
+    _call_on(dev, stream, lib().qk_norm_rope, q_in, k_in, t, hq, hk, d, qg, kg, eps,
+             None if positions is None else _ints(positions, "positions", dev, (t,)),
+             *(rope._at if rope is not None else (None, 0, 0)), q_to, k_to)
 
 
 # --------------------------------------------------------------------------------------------- model / session

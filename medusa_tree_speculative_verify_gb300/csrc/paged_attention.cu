@@ -1138,6 +1138,7 @@ extern "C" mv_status paged_attention(mv_rows q, int32_t n_heads, const mv_paged_
   AttnArgs a;
   mv_status s = mv_paged_check(cache, block_table, ld_table, max_pages, seq_lens, n_seq, &a.c);
   if (s != MV_OK) return s;
+  if (cache->dtype == MV_DTYPE_E2M1) return MV_ERR_UNSUPPORTED;
   size_t need = 0;
   s = paged_attention_workspace(n_seq, n_heads, a.c.heads, a.c.dim, &need);
   if (s != MV_OK) return s;

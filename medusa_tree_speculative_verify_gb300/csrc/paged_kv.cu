@@ -5,6 +5,11 @@
 // product with 2^-e is exact (short of underflow), so the row is rounded once, by the conversion, and what it stands
 // for is exact in bf16 again.
 //
+// Writing e2m1: a thread's 16 elements are a group. Its scale s is the one nearest to max|x| / 6 and each element goes to the
+// value nearest to x / s. A border between two values (0.25, 0.75, 1.25 .. 5) times s has at most 7 significant bits and x has
+// 8, so x / s is a border or at least 2^-8 of itself from one. x times the rounded 1 / s, rounded to a multiple of 2^-11 by
+// adding 6144 and taking it off again, is a border just where x / s is one, and on the same side of it elsewhere.
+//
 // Bound by memory: 2 * dim bytes read (written) and dim + 1 or 2 * dim written (read) for each row, K and V. A CTA takes up
 // to 64 consecutive tokens, all heads, K and V: their places are looked up once, by 16 to 4 lanes a token; what a
 // thread computes of an address serves a row of K and one of V.
@@ -80,13 +85,13 @@ MV_DEV int2 place_of(const MoveArgs& a, int t, int n) {
 }
 
 // kLanes threads a row, the power of two from dim / kEl up
-template <bool kE4M3, bool kWrite, int kLanes>
+template <PagedFormat kFormat, bool kWrite, int kLanes>
 __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const MoveArgs a) {
   constexpr int kEl = 16;  // elements of a thread
   // Rows on their way, K and V in turn: as many as a thread's registers hold (8294 tokens x 8 heads written and read back:
   // bf16 with two 35 us, with four 26; e4m3 written with four 26.8, with two 24.9; 38 k e4m3 tokens read with two 43, with four 41)
-  constexpr int kAhead = kE4M3 && kWrite ? 2 : 4;
-  constexpr int kWords = kE4M3 && !kWrite ? 4 : 8;
+  constexpr int kAhead = kFormat != kBf16 && kWrite ? 2 : 4;
+  constexpr int kWords = kWrite || kFormat == kBf16 ? 8 : kFormat == kE4M3 ? 4 : 2;
   __shared__ int2 s_place[kTokens];
   pdl_trigger();
   pdl_wait();
@@ -126,17 +131,23 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
       const int tok = kWrite ? slow : fast, h = kWrite ? fast : slow;
       const int2 at = r0 + i / 2 * kGroups < pairs ? s_place[tok] : make_int2(-1, 0);
       if (at.x >= 0 && d0 < D) {
-        const int64_t prow = ((int64_t)at.x * H + h) * P + at.y, held_at = (prow * D + d0) * (kE4M3 ? 1 : 2);
+        const int64_t prow = ((int64_t)at.x * H + h) * P + at.y;
+        const int64_t held_at = kFormat == kE2M1 ? (prow * D + d0) / 2 : (prow * D + d0) * (kFormat == kE4M3 ? 1 : 2);
 #pragma unroll
         for (int is_v = 0; is_v < 2; ++is_v) {
           const RowsArgs& p = is_v ? a.v : a.k;
           uint8_t* row = reinterpret_cast<uint8_t*>(p.p + (int64_t)(t0 + tok) * p.ts + (int64_t)h * p.hs + d0);
           uint8_t* held = (is_v ? a.c.v : a.c.k) + held_at;
           to[i + is_v] = kWrite ? held : row;
-          if (kE4M3) exp[i + is_v] = (is_v ? a.c.v_exp : a.c.k_exp) + prow;
+          if (kFormat != kBf16)
+            exp[i + is_v] = (is_v ? a.c.v_exp : a.c.k_exp) + (kFormat == kE2M1 ? prow * (D / kGroup) + ln : prow);
           const uint8_t* from = kWrite ? row : held;
           if constexpr (kWords == 8) {
             load32(from, x[i + is_v], a.wide);
+          } else if constexpr (kWords == 2) {
+            const uint2 w = *reinterpret_cast<const uint2*>(from);
+            x[i + is_v][0] = w.x;
+            x[i + is_v][1] = w.y;
           } else {
             const uint4 w = *reinterpret_cast<const uint4*>(from);
             x[i + is_v][0] = w.x;
@@ -144,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
             x[i + is_v][2] = w.z;
             x[i + is_v][3] = w.w;
           }
-          if (kE4M3 && !kWrite) byte[i + is_v] = *exp[i + is_v];
+          if (kFormat != kBf16 && !kWrite) byte[i + is_v] = *exp[i + is_v];
         }
       }
       slow += add_slow;
@@ -156,11 +167,42 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (!kE4M3) {
-        if constexpr (kWords == 8) {
-          if (to[i]) store32(to[i], x[i], a.wide);
+      if constexpr (kFormat == kBf16) {
+        if (to[i]) store32(to[i], x[i], a.wide);
+      } else if constexpr (kFormat == kE2M1 && kWrite) {
+        if (!to[i]) continue;
+        uint32_t top = 0u;  // of the 16, without the sign: bf16 bits are ordered as their values are, NaN above infinity
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = __vmaxu2(top, x[i][j] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
+        const bool finite = top < 0x7f80u;
+        const uint32_t b = finite ? scale_byte(__fdiv_rn(bf16lo(top), 6.0f)) : kNanScale;
+        const float inv = b && finite ? __fdiv_rn(1.0f, scale_value(b)) : 0.0f;
+        auto quotient = [&](float f) { return __fsub_rn(__fmaf_rn(f, inv, 6144.0f), 6144.0f); };
+        uint32_t q[2] = {0u, 0u};
+        if (finite)  // what an infinity or a NaN times zero becomes does not matter under a scale that is none
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            q[j >> 1] |= float4_to_e2m1x4(quotient(bf16lo(x[i][2 * j])), quotient(bf16hi(x[i][2 * j])),
+                                          quotient(bf16lo(x[i][2 * j + 1])), quotient(bf16hi(x[i][2 * j + 1]))) << (16 * (j & 1));
+        *reinterpret_cast<uint2*>(to[i]) = make_uint2(q[0], q[1]);
+        *exp[i] = (uint8_t)b;
+      } else if constexpr (kFormat == kE2M1) {
+        if (!to[i]) continue;
+        const float s = scale_value(byte[i]);
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t h[4];
+          e2m1x8_to_half2(x[i][j], h);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = half2_to_float2(h[k]);
+            o[4 * j + k] = pack_bf16x2(f.x * s, f.y * s);
+          }
         }
-      } else if (kWrite) {
+        store32(to[i], o, a.wide);
+      } else if constexpr (kWrite) {
         float f[16], top = 0.0f;
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
@@ -198,12 +240,12 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
   }
 }
 
-template <bool kE4M3, bool kWrite>
+template <PagedFormat kFormat, bool kWrite>
 cudaError_t launch_rows(const MoveArgs& a, dim3 grid, cudaStream_t st) {
   constexpr int kMost = 8;
-  if (a.c.dim > 64) return mv_launch(paged_rows_kernel<kE4M3, kWrite, kMost>, grid, dim3(kThreads), 0, st, a);
-  if (a.c.dim > 32) return mv_launch(paged_rows_kernel<kE4M3, kWrite, kMost / 2>, grid, dim3(kThreads), 0, st, a);
-  return mv_launch(paged_rows_kernel<kE4M3, kWrite, kMost / 4>, grid, dim3(kThreads), 0, st, a);
+  if (a.c.dim > 64) return mv_launch(paged_rows_kernel<kFormat, kWrite, kMost>, grid, dim3(kThreads), 0, st, a);
+  if (a.c.dim > 32) return mv_launch(paged_rows_kernel<kFormat, kWrite, kMost / 2>, grid, dim3(kThreads), 0, st, a);
+  return mv_launch(paged_rows_kernel<kFormat, kWrite, kMost / 4>, grid, dim3(kThreads), 0, st, a);
 }
 
 template <bool kWrite>
@@ -225,7 +267,7 @@ mv_status move_rows(const mv_rows& k, const mv_rows& v, int32_t n_rows, const in
     return !((reinterpret_cast<uintptr_t>(r.ptr) | (uint64_t)r.token_stride * 2 | (uint64_t)r.head_stride * 2) & 31);
   };
   a.wide = whole(k) && whole(v) &&
-           (cache->dtype == MV_DTYPE_E4M3 ||
+           (cache->dtype != MV_DTYPE_BF16 ||
             !((reinterpret_cast<uintptr_t>(cache->k) | reinterpret_cast<uintptr_t>(cache->v)) & 31));
   a.n_rows = n_rows;
   // Whole waves of CTAs with as many tokens each as share one round of lookups, which nothing hides. Reads do better with
@@ -242,8 +284,9 @@ mv_status move_rows(const mv_rows& k, const mv_rows& v, int32_t n_rows, const in
   a.err = mv_error_word();
   const dim3 grid((n_rows + a.tokens - 1) / a.tokens);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->dtype == MV_DTYPE_E4M3 ? launch_rows<true, kWrite>(a, grid, st)
-                                                      : launch_rows<false, kWrite>(a, grid, st);
+  const cudaError_t e = cache->dtype == MV_DTYPE_E4M3   ? launch_rows<kE4M3, kWrite>(a, grid, st)
+                        : cache->dtype == MV_DTYPE_E2M1 ? launch_rows<kE2M1, kWrite>(a, grid, st)
+                                                        : launch_rows<kBf16, kWrite>(a, grid, st);
   return e == cudaSuccess ? mv_last_launch("paged_rows") : MV_ERR_CUDA;
 }
 

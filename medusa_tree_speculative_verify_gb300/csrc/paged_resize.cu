@@ -1,0 +1,246 @@
+// Lengths, block table and free pages of a batch of sequences that grow and shrink; places of the rows that come.
+//
+// With exclusive sums over the sequences of rows that come, pages taken and pages given up, everything has a place of its
+// own: page a of all that are given up (counted in the table's order) is pushed as number R - 1 - a of R, the j-th that is
+// taken comes from the stack's place F + R - 1 - j of F + R, which is page j of those given up while j < R. So no page waits
+// for another, and which page goes where does not depend on the order of threads.
+//
+// Bound by latency: lengths, sums, then one dependent load for each page or row. A cluster of CTAs, each of which does the
+// sums for itself, moves the pages; all have read the lengths before the first of them writes (the cluster's barrier). More
+// than kRowsHere rows go to a second kernel over the whole GPU, which looks them up in what the first one wrote.
+#include <algorithm>
+
+#include "kernels.cuh"
+#include "paged.cuh"
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kRowsHere = 8192;
+
+struct ResizeArgs {
+  const int32_t* by;
+  int32_t *lens, *table, *free;  // free: how many, then the stack
+  int n_seq, ld_table, page_size, n_pages;
+  int64_t most;  // positions of a row of the table
+  int32_t *cu, *positions;
+  int64_t* slots;
+  int n_rows;
+  bool rows_here;
+  unsigned int* err;
+};
+
+// the last b with sums[b] <= i, where sums[0] <= i < sums[n]
+MV_DEV int find(const int* sums, int n, int i) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) paged_resize_kernel(const ResizeArgs a) {
+  extern __shared__ int s_all[];
+  const int n = a.n_seq;
+  int *s_rows = s_all, *s_take = s_rows + n + 1, *s_give = s_take + n + 1, *s_len = s_give + n + 1;
+  __shared__ int64_t s_scan[3][kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = (int)cluster_rank();
+  pdl_trigger();
+  pdl_wait();
+  const int held = __ldcg(a.free);
+  bool bad = held < 0 || held > a.n_pages;
+  int64_t carry[3] = {0, 0, 0};
+  for (int base = 0; base < n; base += kThreads) {
+    const int b = base + tid;
+    int64_t x[3] = {0, 0, 0};  // rows that come, pages taken, pages given up
+    int len = 0;
+    if (b < n) {
+      len = __ldcg(a.lens + b);
+      const int64_t to = (int64_t)len + __ldcg(a.by + b);
+      if (len < 0 || len > a.most || to < 0 || to > a.most) {
+        bad = true;
+        if (rank == 0) mv_set_error_detail(a.err, kPagedResizeSite, MV_DEVERR_INDEX, (uint32_t)b);
+      } else {
+        const int more = (int)((to + a.page_size - 1) / a.page_size) - (len + a.page_size - 1) / a.page_size;
+        x[0] = max((int64_t)0, to - len);
+        x[1] = max(0, more);
+        x[2] = max(0, -more);
+      }
+    }
+    int64_t incl[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      incl[k] = x[k];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl[k], o);
+        if (lane >= o) incl[k] += up;
+      }
+      if (lane == 31) s_scan[k][warp] = incl[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      int64_t before = carry[k], all = carry[k];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_scan[k][w];
+        all += s_scan[k][w];
+      }
+      if (b < n) s_all[k * (n + 1) + b] = (int)(before + incl[k] - x[k]);
+      carry[k] = all;
+    }
+    if (b < n) s_len[b] = len;
+    __syncthreads();
+  }
+  const int64_t rows64 = carry[0], take64 = carry[1], give64 = carry[2];
+  const bool over = rows64 > (a.positions || a.slots ? a.n_rows : 0x7fffffff) || held + give64 > a.n_pages || take64 > held + give64;
+  if (over && rank == 0 && tid == 0) mv_set_error_detail(a.err, kPagedResizeSite, MV_DEVERR_INDEX, (uint32_t)n);
+  bad = __syncthreads_or(bad || over);
+  const int rows = bad ? 0 : (int)rows64, take = bad ? 0 : (int)take64, give = bad ? 0 : (int)give64;
+  if (tid == 0) {
+    s_rows[n] = rows;
+    s_take[n] = take;
+    s_give[n] = give;
+  }
+  __syncthreads();
+
+  auto pages_of = [&](int len) { return (int)((unsigned)(len + a.page_size - 1) / (unsigned)a.page_size); };
+  auto given = [&](int i) {  // page i of those given up
+    const int b = find(s_give, n, i), left = pages_of(s_len[b]) - (s_give[b + 1] - s_give[b]);
+    return __ldcg(a.table + (int64_t)b * a.ld_table + left + i - s_give[b]);
+  };
+  auto taken = [&](int j) { return j < give ? given(j) : __ldcg(a.free + 1 + (held + give - 1 - j)); };
+  const int step = kThreads * (int)gridDim.x, first = rank * kThreads + tid;
+  bool odd = false;  // a page outside the pool
+  for (int i = first; i < give; i += step) {
+    const int page = given(i);
+    odd |= page < 0 || page >= a.n_pages;
+    a.free[1 + (held + give - 1 - i)] = page;  // at or over `held`: nothing here reads that
+  }
+  for (int j = first; j < take; j += step) {
+    const int page = taken(j), b = find(s_take, n, j);
+    odd |= page < 0 || page >= a.n_pages;
+    a.table[(int64_t)b * a.ld_table + pages_of(s_len[b]) + j - s_take[b]] = page;
+  }
+  if (odd) mv_set_error_detail(a.err, kPagedResizeSite, MV_DEVERR_INDEX, (uint32_t)n + 1);
+  if (a.rows_here)
+    for (int64_t i = first; i < a.n_rows; i += step) {
+      int pos = -1;
+      int64_t slot = -1;
+      if (i < rows) {
+        const int b = find(s_rows, n, (int)i);
+        pos = s_len[b] + (int)i - s_rows[b];
+        if (a.slots) {
+          const int nth = pos / a.page_size, had = pages_of(s_len[b]);
+          const int page = nth < had ? __ldcg(a.table + (int64_t)b * a.ld_table + nth) : taken(s_take[b] + nth - had);
+          slot = (int64_t)page * a.page_size + (pos - nth * a.page_size);
+        }
+      }
+      if (a.positions) a.positions[i] = pos;
+      if (a.slots) a.slots[i] = slot;
+    }
+  cluster_sync_all();  // all have read what is overwritten now
+  if (rank != 0) return;
+  if (a.cu)
+    for (int b = tid; b <= n; b += kThreads) a.cu[b] = bad ? 0 : s_rows[b];
+  if (bad) return;
+  for (int b = tid; b < n; b += kThreads) {
+    const int by = __ldcg(a.by + b);
+    if (by) a.lens[b] = s_len[b] + by;
+  }
+  if (tid == 0) a.free[0] = held + give - take;
+}
+
+// positions and slots of all rows, from cu, the new lengths and the new table
+__global__ void __launch_bounds__(kThreads) paged_places_kernel(const ResizeArgs a) {
+  extern __shared__ int s_all[];
+  const int n = a.n_seq;
+  int *s_rows = s_all, *s_end = s_all + n + 1;  // s_end[b] + row = position
+  pdl_trigger();
+  pdl_wait();
+  for (int b = threadIdx.x; b <= n; b += kThreads) {
+    s_rows[b] = __ldcg(a.cu + b);
+    if (b < n) s_end[b] = __ldcg(a.lens + b) - __ldcg(a.cu + b + 1);
+  }
+  __syncthreads();
+  const int rows = s_rows[n];
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < a.n_rows; i += (int64_t)gridDim.x * kThreads) {
+    int pos = -1;
+    int64_t slot = -1;
+    if (i < rows) {
+      const int b = find(s_rows, n, (int)i);
+      pos = s_end[b] + (int)i;
+      if (a.slots) {
+        const int nth = pos / a.page_size;
+        slot = (int64_t)__ldcg(a.table + (int64_t)b * a.ld_table + nth) * a.page_size + (pos - nth * a.page_size);
+      }
+    }
+    if (a.positions) a.positions[i] = pos;
+    if (a.slots) a.slots[i] = slot;
+  }
+}
+
+cudaError_t launch_resize(const ResizeArgs& a, int ctas, int bytes, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim = {(unsigned)ctas, 1, 1};
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = mv_pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, paged_resize_kernel, a);
+}
+
+}  // namespace
+
+extern "C" mv_status paged_kv_resize(const int32_t* by, int32_t n_seq, int32_t page_size, int32_t n_pages,
+                                     int32_t* block_table, int32_t ld_table, int32_t max_pages, int32_t* seq_lens,
+                                     int32_t* free_pages, int32_t* cu_rows, int32_t* positions, int64_t* slots,
+                                     int32_t n_rows, mv_stream stream) {
+  if (n_seq < 0 || n_rows < 0) return MV_ERR_INVALID_ARG;
+  if (n_seq > kPagedMaxSeq || n_pages < 1 || page_size < 16 || page_size > kPagedMaxPage || page_size % 16)
+    return MV_ERR_SHAPE;
+  if (max_pages < 1 || ld_table < max_pages || (int64_t)max_pages * page_size > 0x7fffffff - 1024) return MV_ERR_SHAPE;
+  if (!free_pages || (n_seq && (!by || !block_table || !seq_lens))) return MV_ERR_INVALID_ARG;
+  if (((positions || slots) && !cu_rows) || (reinterpret_cast<uintptr_t>(slots) & 7)) return MV_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(by) | reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens) |
+       reinterpret_cast<uintptr_t>(free_pages) | reinterpret_cast<uintptr_t>(cu_rows) |
+       reinterpret_cast<uintptr_t>(positions)) & 3)
+    return MV_ERR_INVALID_ARG;
+  ResizeArgs a;
+  a.by = by;
+  a.lens = seq_lens;
+  a.table = block_table;
+  a.free = free_pages;
+  a.n_seq = n_seq;
+  a.ld_table = ld_table;
+  a.page_size = page_size;
+  a.n_pages = n_pages;
+  a.most = (int64_t)max_pages * page_size;
+  a.cu = cu_rows;
+  a.positions = positions;
+  a.slots = slots;
+  a.n_rows = positions || slots ? n_rows : 0;
+  a.rows_here = a.n_rows <= kRowsHere;
+  a.err = mv_error_word();
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  static int flags[64] = {};
+  const int bytes = (4 * n_seq + 3) * (int)sizeof(int);
+  if (!mv_set_smem_once((const void*)paged_resize_kernel, (4 * kPagedMaxSeq + 3) * (int)sizeof(int), flags)) return MV_ERR_CUDA;
+  if (launch_resize(a, kCluster, bytes, st) != cudaSuccess) return MV_ERR_CUDA;
+  if (!a.rows_here) {
+    const int ctas = (int)std::min<int64_t>(2 * mv_sm_count(), ((int64_t)a.n_rows + kThreads - 1) / kThreads);
+    if (mv_launch(paged_places_kernel, dim3(ctas), dim3(kThreads), (2 * n_seq + 1) * sizeof(int), st, a) != cudaSuccess)
+      return MV_ERR_CUDA;
+  }
+  return mv_last_launch("paged_resize");
+}
