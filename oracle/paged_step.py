@@ -70,14 +70,14 @@ def _nearest(x, grid):
 
 def quantise(x):
     """(codes of 4 bits, scale bytes) of the rows of x; a group with a NaN or an infinity has byte 0xFF and codes of 0."""
-    x = np.asarray(x, dtype=np.float64).reshape(*np.shape(x)[:-1], -1, GROUP)
+    x = np.asarray(x, dtype=np.float64).reshape(*np.shape(x)[:-1], np.shape(x)[-1] // GROUP, GROUP)
     fin = np.isfinite(x).all(axis=-1)
     x = np.where(fin[..., None], x, 0.0)
     byte = _nearest(np.max(np.abs(x), axis=-1) / 6, scale_value(np.arange(TOP_BYTE + 1)))
     s = scale_value(byte)[..., None]
     code = _nearest(np.abs(x) / np.where(s > 0, s, 1.0), E2M1)
     code = np.where(s > 0, code + 8 * (x < 0), 0)
-    return code.reshape(*x.shape[:-2], -1).astype(np.uint8), np.where(fin, byte, NAN_BYTE).astype(np.uint8)
+    return code.reshape(*x.shape[:-2], GROUP * x.shape[-2]).astype(np.uint8), np.where(fin, byte, NAN_BYTE).astype(np.uint8)
 
 
 def pack(code):
@@ -87,7 +87,7 @@ def pack(code):
 
 def stored_value(packed, byte):
     """float64 values of packed rows."""
-    code = np.stack([packed & 15, packed >> 4], axis=-1).reshape(*packed.shape[:-1], -1)
+    code = np.stack([packed & 15, packed >> 4], axis=-1).reshape(*packed.shape[:-1], 2 * packed.shape[-1])
     v = np.where(code & 8, -1.0, 1.0) * E2M1[code & 7]
     with np.errstate(invalid="ignore"):
         return v * np.repeat(scale_value(byte), GROUP, axis=-1)
