@@ -6,8 +6,8 @@ namespace {
 // Keys of a step of all warps.
 template <PagedFormat kFormat>
 int step_keys(bool big, bool wide) {
-  return kWarps * (big ? (wide ? Layout<128, kFormat, 2>::kKeys : Layout<128, kFormat, 1>::kKeys)
-                       : (wide ? Layout<64, kFormat, 2>::kKeys : Layout<64, kFormat, 1>::kKeys));
+  if (big) return wide ? Layout<128, kFormat, 2>::kStepKeys : Layout<128, kFormat, 1>::kStepKeys;
+  return wide ? Layout<64, kFormat, 2>::kStepKeys : Layout<64, kFormat, 1>::kStepKeys;
 }
 
 }  // namespace
@@ -58,7 +58,7 @@ extern "C" mv_status paged_attention(mv_rows q, int32_t n_heads, const mv_paged_
     a.q = {static_cast<uint16_t*>(q.ptr) + first * q.token_stride, q.token_stride, q.head_stride};
     a.out = {static_cast<uint16_t*>(out.ptr) + first * out.token_stride, out.token_stride, out.head_stride};
     if (e2m1)
-      s = launch_paged_attention_e2m1(a, big, wide, st);
+      s = launch_paged_attention_e2m1(a, wide, st);
     else if (big)
       s = e4m3 ? (wide ? launch<128, kE4M3, 2>(a, st) : launch<128, kE4M3, 1>(a, st))
                : (wide ? launch<128, kBf16, 2>(a, st) : launch<128, kBf16, 1>(a, st));

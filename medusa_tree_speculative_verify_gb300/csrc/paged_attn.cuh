@@ -75,8 +75,8 @@ struct AttnArgs {
   float* part;          // [CTAs][2] partial results
   unsigned int* err;
 };
-// over 4-bit pages (paged_attention_e2m1.cu): heads of over 64 dims, units of over 8 heads
-mv_status launch_paged_attention_e2m1(const AttnArgs& a, bool big, bool wide, cudaStream_t stream);
+// over 4-bit pages (paged_attention_e2m1.cu); wide: units of over 8 heads
+mv_status launch_paged_attention_e2m1(const AttnArgs& a, bool wide, cudaStream_t stream);
 
 namespace {
 
@@ -89,6 +89,7 @@ struct Layout {
   // 16-key tiles of a warp's step: 8 KB, or as many as registers hold the scores of
   static constexpr int kSub = 256 / kRow < 4 ? 256 / kRow : 4;
   static constexpr int kKeys = 16 * kSub;                // keys of a warp's step
+  static constexpr int kStepKeys = kWarps * kKeys;       // of all warps'
   // a step: for each box of the row the regions of its kSub tiles, K, then the same of V
   // steps of a warp's queue: as many as shared memory holds
   static constexpr int kStages = kFormat != kE2M1 ? 3 : kDim > 64 ? 2 : 4;
@@ -125,25 +126,23 @@ MV_DEV uint32_t lds4(uint32_t a) {
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-MV_DEV uint32_t lds_half(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-  return v;
+MV_DEV void sts_half(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)v) : "memory");
 }
 MV_DEV uint32_t lds_byte(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
-// `bytes` (a multiple of 16) of global memory to shared memory, both 16-byte aligned, counted on `bar`
-MV_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 // 16 bytes of global memory to shared memory by this thread
 MV_DEV void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+MV_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until all but the last kPending groups of this thread's cp_async16 have come
+template <int kPending>
+MV_DEV void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 // arrives at `bar` once this thread's cp_async16 so far have come
 MV_DEV void cp_async_arrive(uint64_t* bar) {
@@ -203,8 +202,8 @@ MV_DEV void split_weights(float p0, float p1, uint32_t& hi, uint32_t& lo) {
 // 2^(a - b) where both may be -inf (then the weight of nothing: 0)
 MV_DEV float weight(float a, float b) { return a == -INFINITY ? 0.0f : exp2f(a - b); }
 
-// kCluster: one sequence, a cluster of CTAs for each unit (see launch).
-template <int kDim, PagedFormat kFormat, int kNT, bool kCluster>
+// kCluster: one sequence, a cluster of CTAs for each unit (see launch). kWhole: heads of kDim dims, not fewer (e2m1).
+template <int kDim, PagedFormat kFormat, int kNT, bool kCluster, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
   using Ly = Layout<kDim, kFormat, kNT>;
@@ -228,13 +227,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* s_len = s_pre + a.c.n_seq + 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int n_seq = a.c.n_seq, units = a.c.heads * a.parts, groups = (units + kWarps - 1) / kWarps;  // of a sequence
-  constexpr int kStepKeys = kWarps * Ly::kKeys;
+  constexpr int kStepKeys = Ly::kStepKeys;
   pdl_trigger();
-  if (tid == 0) {
+  if (kFormat != kE2M1 && tid == 0) {
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
   }
-  if (lane == 0) {
+  if (kFormat != kE2M1 && lane == 0) {
 #pragma unroll
     for (int i = 0; i < Ly::kStages; ++i) mbar_init(&s_full[warp][i], kFormat == kE4M3 ? 33 : 1);  // the copies' bytes, and each lane's exponents
     mbar_fence_init();
@@ -362,12 +361,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t queue = smem_u32(smem) + warp * Ly::kStages * Ly::kStage;
   const uint32_t exps = smem_u32(smem) + Ly::kExpsAt + warp * Ly::kStages * Ly::kExps;
   const int page16 = a.c.page_size >> 4, box_groups = 1 << a.groups_log2;
-  const bool my_exp = lane >= 16;
-  const bool one_exp = my_exp && kFormat == kE4M3;  // one tile's; scales go with the tiles of a copy
-  const int my_u = one_exp ? (lane - 16) >> 1 : (lane & (box_groups - 1)) * a.box_tiles;
-  const int my_op = one_exp ? lane & 1 : (lane & 15) >> a.groups_log2;  // K boxes, then V boxes
+  const bool my_exp = kFormat == kE4M3 && lane >= 16;
+  const int my_u = kFormat == kE2M1 ? lane / (32 / Ly::kSub) : my_exp ? (lane - 16) >> 1 : (lane & (box_groups - 1)) * a.box_tiles;
+  const int my_op = my_exp ? lane & 1 : lane >> a.groups_log2;  // K boxes, then V boxes
   const bool my_v = my_exp ? my_op : my_op >= Ly::kBoxes;
-  const bool mine_any = my_exp ? (one_exp ? my_u < Ly::kSub : kFormat == kE2M1 && my_op < 2) : my_op < 2 * Ly::kBoxes;
+  const bool mine_any = kFormat == kE2M1 || (my_exp ? my_u < Ly::kSub : my_op < 2 * Ly::kBoxes);
   int s_ahead = s_begin, page, tile;  // of the step that is looked up next
   int key_ahead, h_ahead;             // its first key here (past the end: nothing to do) and kv head
   bool more = s_begin < s_end;
@@ -415,24 +413,61 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A page outside the pool is not copied. What the step's place holds then is of no sequence, so a unit with such a step, in
   // whichever warp or CTA, is bad: its rows of out stay as they were.
   constexpr uint32_t kBad = 1u << 16;  // a lane's bad page in the sum of a step's bytes, which are fewer
-  static_assert(Ly::kStage + Ly::kExps < (int)kBad, "");
+  static_assert(Ly::kStage < (int)kBad, "");
   uint32_t bad_slots = 0;
   int copied = 0, used = 0;  // steps
+  // e2m1: 16 rows of a head are one piece of memory, and so are their scales: copied by kTileLanes lanes, 16 bytes each, all
+  // tiles of a step side by side whatever pages they lie in. Two rows (128 dims) or four (64) share 128 bytes of shared
+  // memory, their 16-byte pieces turned so that neither reads of K nor of V meet in a bank.
+  const int per_row = kWhole ? kDim / kGroup : a.c.dim / kGroup, pieces = per_row / 2;
+  auto place = [](int row, int piece) {
+    if (kDim > 64) return (row >> 1) * 128 + ((((row & 1) * 4 + piece) ^ (row & 6)) << 4);
+    return (row >> 2) * 128 + ((((row & 3) * 2 + piece) ^ ((row >> 1) & 2)) << 4);
+  };
+  constexpr int kTileLanes = 32 / Ly::kSub, kCopies = kDim / 2 / kTileLanes, kPeriod = kWhole ? (kDim > 64 ? 4 : 2) * 8 / kTileLanes : kCopies;
+  const int my_piece = lane % kTileLanes;
+  uint32_t copy_to[kPeriod];  // this lane's pieces of a tile: the first few, the others as much further
+#pragma unroll
+  for (int i = 0; i < kPeriod; ++i) {
+    const int c = my_piece + kTileLanes * i, row = c / pieces;
+    copy_to[i] = (uint32_t)(my_u * Ly::kRegion + place(row, c - row * pieces));
+  }
+  const int page_rows = a.c.heads * a.c.page_size;
   auto copy_step = [&](int slot) {
-    if (next.valid) {
+    if constexpr (kFormat == kE2M1) {
+      __syncwarp();  // every lane is done with the slot
+      if (next.valid) {
+        const bool bad = next.has && (next.entry < 0 || next.entry >= a.c.n_pages);
+        if (bad) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)next.entry);
+        bad_slots = (bad_slots & ~(1u << slot)) | (__any_sync(0xffffffffu, bad) ? 1u << slot : 0u);
+        if (next.has && !bad) {
+          const int64_t at = ((int64_t)next.entry * page_rows + next.row) * per_row;  // of the scales; elements: 8 times as far
+          const uint8_t *k = a.c.k + (at * 8 + my_piece * 16), *v = a.c.v + (at * 8 + my_piece * 16);
+#pragma unroll
+          for (int i = 0; i < kCopies; ++i)
+            if (kWhole || i * kTileLanes < 16 * pieces) {
+              const uint32_t dst = queue + slot * Ly::kStage + copy_to[i % kPeriod] + i / kPeriod * (kPeriod * kTileLanes * 16);
+              cp_async16(dst, k + i * (kTileLanes * 16));
+              cp_async16(dst + Ly::kV, v + i * (kTileLanes * 16));
+            }
+          if (my_piece < per_row) {
+            const uint32_t dst = exps + slot * Ly::kExps + my_u * 16 * per_row + my_piece * 16;
+            cp_async16(dst, a.c.k_exp + at + my_piece * 16);
+            cp_async16(dst + Ly::kExps / 2, a.c.v_exp + at + my_piece * 16);
+          }
+        }
+      }
+      cp_async_commit();
+    } else if (next.valid) {
       const bool bad = next.has && (next.entry < 0 || next.entry >= a.c.n_pages);
       if (bad) mv_set_error_detail(a.err, kPagedAttnSite, MV_DEVERR_INDEX, (uint32_t)next.entry);
       const bool go = next.has && !bad;
-      const uint32_t bytes = !go ? 0u : !my_exp ? (uint32_t)(a.box_tiles * Ly::kRegion) : kFormat == kE2M1 ? (uint32_t)(a.box_tiles * a.c.dim) : 0u;
+      const uint32_t bytes = go && !my_exp ? (uint32_t)(a.box_tiles * Ly::kRegion) : 0u;
       const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes + (bad ? kBad : 0u));  // also: every lane is done with the slot
       bad_slots = (bad_slots & ~(1u << slot)) | (sum >= kBad ? 1u << slot : 0u);
       uint64_t* bar = &s_full[warp][slot];
       if (lane == 0) mbar_arrive_expect_tx(bar, sum & (kBad - 1));
-      if (kFormat == kE2M1 && bytes && my_exp) {
-        bulk_load(exps + slot * Ly::kExps + my_op * (Ly::kExps / 2) + my_u * a.c.dim,
-                  (my_v ? a.c.v_exp : a.c.k_exp) + ((int64_t)next.entry * a.c.heads * a.c.page_size + next.row) * (a.c.dim / kGroup),
-                  bytes, bar);
-      } else if (bytes) {
+      if (bytes) {
         const int box = my_v ? my_op - Ly::kBoxes : my_op;
         uint8_t* dst = smem + (warp * Ly::kStages + slot) * Ly::kStage + (my_op * Ly::kSub + my_u) * Ly::kRegion;
         tma_load_3d(dst, my_v ? &vmap : &kmap, bar, box * (kFormat == kBf16 ? Ly::kBox / 2 : Ly::kBox), next.row, next.entry);
@@ -456,20 +491,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_off = g * 128 + ((t ^ g) << 4);  // piece t; piece t + 4: ^ 64
     v_off[0] = 2 * t * 128 + ((g ^ (2 * t)) << 4);
     v_off[1] = (2 * t + 1) * 128 + ((g ^ (2 * t + 1)) << 4);
-  } else if (Ly::kBox == 32) {  // not swizzled: pieces of 8 and of 4 bytes
-    k_off = g * 32 + t * 8;
-    v_off[0] = 2 * t * 32 + g * 4;
-    v_off[1] = v_off[0] + 32;
+  } else if (kFormat == kE2M1) {
+    constexpr int kBytes = kDim / 16;  // a lane's of a value row
+    k_off = kDim > 64 ? place(g, t) : place(g, t >> 1) + (t & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v_off[i] = place(2 * t + i, g * kBytes / 16) + g * kBytes % 16;
   } else {
     k_off = g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
     v_off[0] = 2 * t * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
     v_off[1] = v_off[0] + 64;
   }
 
-  // where this lane's scales lie (of K row g, of V row 2 t), from tile to tile and for 8 rows; dims behind the head's have none
-  const int per_row = a.c.dim / kGroup;
+  // where this lane's scales lie (of K row g, of V row 2 t); dims behind the head's have none
   const uint32_t ks_off = g * per_row + (kDim > 64 ? 2 * t : t), vs_off = Ly::kExps / 2 + 2 * t * per_row + (kDim > 64 ? g : g >> 1);
-  const bool ks_any = (kDim > 64 ? 2 * t : t) < per_row, vs_any = (kDim > 64 ? g : g >> 1) < per_row;
+  const bool ks_any = kWhole || (kDim > 64 ? 2 * t : t) < per_row, vs_any = kWhole || (kDim > 64 ? g : g >> 1) < per_row;
 
   // the words of Q of a unit: head g of each tile of 8, the pieces as of K
   uint32_t q_raw[kNT][kDim / 8];
@@ -556,8 +591,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool bad = false;
     for (int i = 0; i < steps; ++i, key0 += key_add) {
       copy_step(slot == 0 ? Ly::kStages - 1 : slot - 1);
-      bool there = used++ < copied;  // not after a wait that gave up
-      if (there && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase))) {
+      bool there = kFormat == kE2M1 || used++ < copied;  // not after a wait that gave up
+      if (kFormat == kE2M1) {
+        cp_async_wait<Ly::kStages - 1>();
+        __syncwarp();
+      } else if (there && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][slot], phase))) {
         more = next.valid = then.valid = there = false;  // nothing more is copied; what is on its way is still waited for
         mv_set_error(a.err, kPagedAttnSite, MV_DEVERR_TIMEOUT);
       }
@@ -580,45 +618,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = 0; u < Ly::kSub; ++u)
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[n][u][e] = 0.0f;
+      const bool tail = key0 + Ly::kKeys > len;
       if constexpr (kFormat == kE2M1) {
-#pragma unroll
-        for (int u = 0; u < Ly::kSub; ++u) {
-          constexpr int kWords = kDim / 32;  // of 8 elements; a scale for each two
-          uint32_t kw[2][kWords], sc[2][kWords / 2];  // keys g, g + 8
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t src = at + u * Ly::kRegion + k_off + r * 8 * Ly::kBox, ex = ex_at + ks_off + (16 * u + 8 * r) * per_row;
-            if constexpr (kWords == 4) {
-              const uint4 v = lds16(src);
-              kw[r][0] = v.x;
-              kw[r][1] = v.y;
-              kw[r][2] = v.z;
-              kw[r][3] = v.w;
-              const uint32_t two = ks_any ? lds_half(ex) : 0u;
-              sc[r][0] = (two & 0xffu) * 0x00800080u;  // both halves
-              sc[r][1] = (two >> 8) * 0x00800080u;
-            } else {
-              const uint2 v = lds8(src);
-              kw[r][0] = v.x;
-              kw[r][1] = v.y;
-              sc[r][0] = (ks_any ? lds_byte(ex) : 0u) * 0x00800080u;
+        if (tail) {  // rows behind the sequence hold anything: with scales of zero it is zero, codes being finite
+          for (int row = len - key0 + lane; row < Ly::kKeys; row += 32)
+            for (int c = 0; c < per_row; c += 2) {
+              sts_half(ex_at + row * per_row + c, 0u);
+              sts_half(ex_at + Ly::kExps / 2 + row * per_row + c, 0u);
             }
-          }
+          __syncwarp();
+        }
+        constexpr int kWords = kDim / 32;  // of 8 elements; a scale for each two
 #pragma unroll
-          for (int j = 0; j < kWords; ++j) {
-            uint32_t f[2][4];
+        for (int u0 = 0; u0 < Ly::kSub; u0 += 2) {  // two tiles' products in turn: one would wait for the one before
+          uint32_t kw[2][2][kWords], sc[2][2][kWords / 2];  // keys g, g + 8
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              e2m1x8_to_half2(kw[r][j], f[r]);
+              const uint32_t src = at + (u0 + u) * Ly::kRegion + k_off + r * 8 * Ly::kBox;
+              const uint32_t ex = ex_at + ks_off + (16 * (u0 + u) + 8 * r) * per_row;
+              if constexpr (kWords == 4) {
+                const uint4 v = lds16(src);
+                kw[u][r][0] = v.x;
+                kw[u][r][1] = v.y;
+                kw[u][r][2] = v.z;
+                kw[u][r][3] = v.w;
+              } else {
+                const uint2 v = lds8(src);
+                kw[u][r][0] = v.x;
+                kw[u][r][1] = v.y;
+              }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) f[r][i] = mul_f16x2(f[r][i], sc[r][j >> 1]);
+              for (int i = 0; i < kWords / 2; ++i) sc[u][r][i] = (ks_any ? lds_byte(ex + i) : 0u) * 0x00800080u;  // both halves
             }
 #pragma unroll
-            for (int i = 0; i < 4; i += 2)
+          for (int j = 0; j < kWords; ++j)
 #pragma unroll
-              for (int n = 0; n < kNT; ++n)
-                mma<true>(x[n][u], f[0][i], f[1][i], f[0][i + 1], f[1][i + 1], qf[n][2 * j + i / 2][0], qf[n][2 * j + i / 2][1]);
-          }
+            for (int u = 0; u < 2; ++u) {
+              uint32_t f[2][4];
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                e2m1x8_to_half2(kw[u][r][j], f[r]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[r][i] = mul_f16x2(f[r][i], sc[u][r][j >> 1]);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; i += 2)
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+                  mma<true>(x[n][u0 + u], f[0][i], f[1][i], f[0][i + 1], f[1][i + 1], qf[n][2 * j + i / 2][0],
+                            qf[n][2 * j + i / 2][1]);
+            }
         }
       }
 #pragma unroll
@@ -675,9 +726,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float& v = x[n][u][2 * r + e];
-              v = key < len ? v * (kFormat == kE4M3 ? ks * mult[n][e] : mult[n][e]) : -INFINITY;
+              if (kFormat == kE2M1) v *= mult[n][e];  // masked below, if need be
+              else v = key < len ? v * (kFormat == kE4M3 ? ks * mult[n][e] : mult[n][e]) : -INFINITY;
             }
         }
+      // e2m1: the least score of the step. (A row behind the sequence has 0, which counts here and does no harm.)
+      float least_score[kNT][2];
+      if (kFormat == kE2M1) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            least_score[n][e] = INFINITY;
+#pragma unroll
+            for (int u = 0; u < Ly::kSub; ++u)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) least_score[n][e] = fminf(least_score[n][e], x[n][u][2 * r + e]);
+          }
+        if (tail)
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int u = 0; u < Ly::kSub; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (key0 + 16 * u + g + 8 * (i >> 1) >= len) x[n][u][i] = -INFINITY;
+      }
       // the references: moved when a score outgrows them by 2^kGrow, from nothing at the first key that is seen; the unit too
       bool grow = kFormat == kE4M3 && top_ev > sum_unit + 7 && sum_unit < 0;
       float tx[kNT][2];
@@ -731,10 +805,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               y -= mx[n][e] == -INFINITY ? 0.0f : mx[n][e] - kLift;
               p[e] = ex2(y);
               l[n][e] += p[e];
-              if (kFp16) {
-                const float z = kFormat == kE4M3 ? y + (float)(ev[u][r] - sum_unit) : y;
+              if (kFormat == kE4M3) {
+                const float z = y + (float)(ev[u][r] - sum_unit);
                 least = fminf(least, key0 + 16 * u + g + 8 * r < len ? z : 0.0f);
-                if (kFormat == kE4M3) p[e] = ex2(z);
+                p[e] = ex2(z);
               }
             }
             if (kFp16) {
@@ -743,13 +817,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               split_weights(p[0], p[1], ph[n][u][r], pl[n][u][r]);
             }
           }
+      if (kFormat == kE2M1)
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) least = fminf(least, least_score[n][e] - (mx[n][e] == -INFINITY ? 0.0f : mx[n][e] - kLift));
       const bool low = kFp16 && __any_sync(0xffffffffu, least < -14.0f || top_ev > 7);
       // O^T += V^T P^T; kWide: 8-bit or 4-bit rows times their scales in bf16, with ph and pl
       auto add_values = [&](auto wide) {
         constexpr bool kWide = decltype(wide)::value;
 #pragma unroll
         for (int u = 0; u < Ly::kSub; ++u) {
-          if (u > 0 && key0 + 16 * u >= len) break;
+          if (kFormat != kE2M1 && u > 0 && key0 + 16 * u >= len) break;  // e2m1: zeros, and no branch between tiles
           const uint32_t vt = at + Ly::kV + u * Ly::kRegion;
           const int left = len - key0 - 16 * u;
           constexpr int kPieces = Ly::kBoxes, kWords = Ly::kVPiece / 4;
@@ -761,8 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t s[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i)
-                s[i] = vs_any && 2 * t + i + 8 * r < left ? lds_byte(ex + (i + 8 * r) * per_row) : 0u;
-              scales[r] = s[0] << 7 | s[1] << 23;
+                s[i] = vs_any ? lds_byte(ex + (i + 8 * r) * per_row) : 0u;
+              scales[r] = s[0] * 0x80u + s[1] * 0x800000u;
             }
           } else if (kWide) {
 #pragma unroll
@@ -796,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[r][1] = v.y;
               }
             }
-            if (left < 16) {  // rows behind the sequence hold anything: weight zero times a NaN would be one
+            if (kFormat != kE2M1 && left < 16) {  // rows behind the sequence hold anything: weight zero times a NaN would be one
 #pragma unroll
               for (int r = 0; r < 4; ++r)
                 if (2 * t + (r & 1) + 4 * (r & 2) >= left)
@@ -1161,7 +1240,7 @@ int64_t most_places(const AttnArgs& a, int keys) {
 }
 
 // Clusters of `size` CTAs of the kernel that the device holds at once (found once for each device and size).
-template <int kDim, PagedFormat kFormat, int kNT>
+template <int kDim, PagedFormat kFormat, int kNT, bool kWhole>
 int most_clusters(int size, int bytes) {
   static std::atomic<int> found[64][5];  // 0: not asked yet, else one more
   const int dev = mv_device(), log2 = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : size == 8 ? 3 : 4;
@@ -1177,7 +1256,7 @@ int most_clusters(int size, int bytes) {
     at[0].val.clusterDim = {(unsigned)size, 1, 1};
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, paged_attn_kernel<kDim, kFormat, kNT, true>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, paged_attn_kernel<kDim, kFormat, kNT, true, kWhole>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -1186,15 +1265,15 @@ int most_clusters(int size, int bytes) {
   return n - 1;
 }
 
-template <int kDim, PagedFormat kFormat, int kNT>
+template <int kDim, PagedFormat kFormat, int kNT, bool kWhole = true>
 mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   using Ly = Layout<kDim, kFormat, kNT>;
   static int flags[64] = {}, c_flags[64] = {}, c_wide[64] = {};
   const int bytes = Ly::bytes(args.c.n_seq);
-  if (!mv_set_smem_once((const void*)paged_attn_kernel<kDim, kFormat, kNT, false>, Ly::bytes(kChunkSeq), flags))
+  if (!mv_set_smem_once((const void*)paged_attn_kernel<kDim, kFormat, kNT, false, kWhole>, Ly::bytes(kChunkSeq), flags))
     return MV_ERR_CUDA;
   const int units = args.c.heads * args.parts, sms = std::min(mv_sm_count(), kMaxCtas);
-  const int grid = (int)std::min<int64_t>(args.c.n_seq * most_places(args, kWarps * Ly::kKeys), sms);
+  const int grid = (int)std::min<int64_t>(args.c.n_seq * most_places(args, Ly::kStepKeys), sms);
   AttnArgs a = args;
   // Sequences short enough for one warp to a unit: while there are units for every warp, up to kShortSteps of its steps (128
   // sequences of 160 keys, 8 kv heads: 15 us, cut across warps 28; of half as many steps at most, 128 of up to 300 keys take
@@ -1208,15 +1287,15 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   a.tile_add = kWarps * Ly::kSub % page16;
   a.page_one = Ly::kSub / page16;
   a.tile_one = Ly::kSub % page16;
+  CUtensorMap maps[2] = {};
   // a pool as (dim, row of the page, page), boxes of box_tiles * 16 rows; dims behind the head's are filled with zeros
-  CUtensorMap maps[2];
-  const uint64_t row = (uint64_t)a.c.dim * (kFormat == kBf16 ? 4 : kFormat == kE4M3 ? 2 : 1) / 2, rows = (uint64_t)a.c.heads * a.c.page_size;
-  const uint64_t dims[3] = {kFormat == kBf16 ? (uint64_t)a.c.dim : row, rows, (uint64_t)a.c.n_pages}, strides[2] = {row, row * rows};
+  const uint64_t row = (uint64_t)a.c.dim * (kFormat == kBf16 ? 2 : 1), rows = (uint64_t)a.c.heads * a.c.page_size;
+  const uint64_t dims[3] = {(uint64_t)a.c.dim, rows, (uint64_t)a.c.n_pages}, strides[2] = {row, row * rows};
   const uint32_t box[3] = {(uint32_t)(kFormat == kBf16 ? Ly::kBox / 2 : Ly::kBox), 16u * a.box_tiles, 1};
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 2 && kFormat != kE2M1; ++i)
     if (!mv_encode_tmap(&maps[i], kFormat == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
                         i ? a.c.v : a.c.k, dims, strides, box,
-                        Ly::kBox == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : Ly::kBox == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE))
+                        Ly::kBox == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
       return MV_ERR_CUDA;
 
   // One sequence: its units are alike, and a cluster for each, joined over distributed shared memory, is sooner done than
@@ -1225,13 +1304,13 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   if (a.c.n_seq == 1) {
     int size = kClusterMost;
     while (size > 1 && units * size > sms) size /= 2;
-    const void* fn = (const void*)paged_attn_kernel<kDim, kFormat, kNT, true>;
+    const void* fn = (const void*)paged_attn_kernel<kDim, kFormat, kNT, true, kWhole>;
     if (units * size <= sms && 4 * units * size >= 3 * sms && mv_set_smem_once(fn, Ly::bytes(1), c_flags)) {
       const int dev = mv_device();
       if (size > 8 && !c_wide[dev])
         c_wide[dev] = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess ? 1 : -1;
       if (size > 8 && c_wide[dev] < 0) cudaGetLastError();
-      if ((size <= 8 || c_wide[dev] > 0) && most_clusters<kDim, kFormat, kNT>(size, Ly::bytes(1)) >= units) {
+      if ((size <= 8 || c_wide[dev] > 0) && most_clusters<kDim, kFormat, kNT, kWhole>(size, Ly::bytes(1)) >= units) {
         a.cluster = size;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(units * size);
@@ -1245,13 +1324,13 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
         at[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = mv_pdl_enabled() ? 2 : 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<kDim, kFormat, kNT, true>, maps[0], maps[1], a);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<kDim, kFormat, kNT, true, kWhole>, maps[0], maps[1], a);
         return e == cudaSuccess ? mv_last_launch("paged_attention") : MV_ERR_CUDA;
       }
     }
   }
   const cudaError_t e =
-      mv_launch(paged_attn_kernel<kDim, kFormat, kNT, false>, dim3(grid), dim3(kThreads), bytes, stream, maps[0], maps[1], a);
+      mv_launch(paged_attn_kernel<kDim, kFormat, kNT, false, kWhole>, dim3(grid), dim3(kThreads), bytes, stream, maps[0], maps[1], a);
   return e == cudaSuccess ? mv_last_launch("paged_attention") : MV_ERR_CUDA;
 }
 
