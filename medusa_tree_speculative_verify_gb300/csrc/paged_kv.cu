@@ -58,6 +58,12 @@ MV_DEV void store32(uint8_t* p, const uint32_t (&x)[8], bool wide) {
   reinterpret_cast<uint4*>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
 }
 
+// The page and slot of position `pos` of sequence b, page -2 for one outside the pool
+MV_DEV int2 slot_of(const MoveArgs& a, int b, int pos) {
+  const int nth = pos / a.c.page_size, page = __ldcg(a.c.table + (int64_t)b * a.c.ld_table + nth);
+  return page < 0 || page >= a.c.n_pages ? make_int2(-2, 0) : make_int2(page, pos - nth * a.c.page_size);
+}
+
 // Where token t of the packed rows lies: page and slot; page -1 for a row behind the last sequence, -2 when the table,
 // the lengths or cu are out of range. By n = 2^k consecutive lanes, which narrow the sequences down to an n-th at a time.
 MV_DEV int2 place_of(const MoveArgs& a, int t, int n) {
@@ -78,10 +84,119 @@ MV_DEV int2 place_of(const MoveArgs& a, int t, int n) {
   const int64_t pos = (int64_t)len - c1 + t;
   // a length over the table's is refused with all its rows, those too that would have a place
   if (len < c1 - c0 || pos < 0 || len > a.c.max_pages * a.c.page_size) return make_int2(-2, 0);
-  const int nth = (int)pos / a.c.page_size;
-  const int page = __ldcg(a.c.table + (int64_t)lo * a.c.ld_table + nth);
-  if (page < 0 || page >= a.c.n_pages) return make_int2(-2, 0);
-  return make_int2(page, (int)pos - nth * a.c.page_size);
+  return slot_of(a, lo, (int)pos);
+}
+
+// The same with cu and the lengths in shared memory
+MV_DEV int2 place_in(const MoveArgs& a, int t, const int* cu, const int* lens) {
+  const int n_seq = a.c.n_seq;
+  int lo = 0, hi = n_seq;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const int c0 = cu[lo], c1 = cu[lo + 1], len = lens[lo];
+  if (t >= cu[n_seq]) return make_int2(-1, 0);
+  const int64_t pos = (int64_t)len - c1 + t;
+  if (c0 < 0 || t < c0 || t >= c1 || len < c1 - c0 || pos < 0 || len > a.c.max_pages * a.c.page_size) return make_int2(-2, 0);
+  return slot_of(a, lo, (int)pos);
+}
+
+// A group's 16 bf16 as 4-bit values and their scale byte
+MV_DEV uint2 quantise(const uint32_t (&x)[8], uint32_t& byte) {
+  uint32_t top = 0u;  // without the sign, bf16 bits are ordered as their values are, NaN above infinity
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = __vmaxu2(top, x[j] & 0x7fff7fffu);
+  top = max(top & 0xffffu, top >> 16);
+  const bool finite = top < 0x7f80u;
+  byte = finite ? scale_byte(__fdiv_rn(bf16lo(top), 6.0f)) : kNanScale;
+  const float inv = byte && finite ? __fdiv_rn(1.0f, scale_value(byte)) : 0.0f;
+  auto quotient = [&](float f) { return __fsub_rn(__fmaf_rn(f, inv, 6144.0f), 6144.0f); };
+  uint32_t q[2] = {0u, 0u};
+  if (finite)  // (an infinity or a NaN times zero would be no number)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      q[j >> 1] |= float4_to_e2m1x4(quotient(bf16lo(x[2 * j])), quotient(bf16hi(x[2 * j])), quotient(bf16lo(x[2 * j + 1])),
+                                    quotient(bf16hi(x[2 * j + 1]))) << (16 * (j & 1));
+  return make_uint2(q[0], q[1]);
+}
+// and back
+MV_DEV void dequantise(uint2 q, uint32_t byte, uint32_t (&x)[8]) {
+  const float s = scale_value(byte);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t h[4];
+    e2m1x8_to_half2(j ? q.y : q.x, h);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = half2_to_float2(h[k]);
+      x[4 * j + k] = pack_bf16x2(f.x * s, f.y * s);
+    }
+  }
+}
+
+// The rows of nt tokens over a 4-bit pool: a thread has a group of 16 elements of a row of K and of V, of several rows at once.
+template <bool kWrite, int kLanes>
+MV_DEV void move_e2m1(const MoveArgs& a, const int2* s_place, int t0, int nt) {
+  constexpr int kAhead = kWrite ? 2 : 4;  // pairs of rows
+  constexpr int kGroups = kThreads / kLanes;
+  const int ln = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int H = a.c.heads, D = a.c.dim, P = a.c.page_size, pairs = nt * H, per_row = D / kGroup;
+  const int n_fast = kWrite ? H : nt, add_slow = kGroups / n_fast, add_fast = kGroups % n_fast;
+  int slow = group / n_fast, fast = group - slow * n_fast;
+  for (int r0 = group; r0 < pairs; r0 += kAhead * kGroups) {
+    int64_t held[kAhead];  // the group's number in the pool, -1: nothing to move
+    int tok[kAhead], head[kAhead];
+    uint32_t x[kAhead][2][kWrite ? 8 : 2], byte[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      tok[i] = kWrite ? slow : fast;
+      head[i] = kWrite ? fast : slow;
+      held[i] = -1;
+      const int2 at = r0 + i * kGroups < pairs ? s_place[tok[i]] : make_int2(-1, 0);
+      if (at.x >= 0 && ln < per_row) {
+        held[i] = (((int64_t)at.x * H + head[i]) * P + at.y) * per_row + ln;
+#pragma unroll
+        for (int is_v = 0; is_v < 2; ++is_v) {
+          if constexpr (kWrite) {
+            const RowsArgs& p = is_v ? a.v : a.k;
+            load32(reinterpret_cast<const uint8_t*>(p.p + (int64_t)(t0 + tok[i]) * p.ts + (int64_t)head[i] * p.hs + ln * kGroup),
+                   x[i][is_v], a.wide);
+          } else {
+            const uint2 w = __ldcg(reinterpret_cast<const uint2*>((is_v ? a.c.v : a.c.k) + held[i] * 8));
+            x[i][is_v][0] = w.x;
+            x[i][is_v][1] = w.y;
+            byte[i][is_v] = (is_v ? a.c.v_exp : a.c.k_exp)[held[i]];
+          }
+        }
+      }
+      slow += add_slow;
+      fast += add_fast;
+      if (fast >= n_fast) {
+        fast -= n_fast;
+        ++slow;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (held[i] < 0) continue;
+#pragma unroll
+      for (int is_v = 0; is_v < 2; ++is_v) {
+        if constexpr (kWrite) {
+          uint32_t b;
+          *reinterpret_cast<uint2*>((is_v ? a.c.v : a.c.k) + held[i] * 8) = quantise(x[i][is_v], b);
+          (is_v ? a.c.v_exp : a.c.k_exp)[held[i]] = (uint8_t)b;
+        } else {
+          const RowsArgs& p = is_v ? a.v : a.k;
+          uint32_t o[8];
+          dequantise(make_uint2(x[i][is_v][0], x[i][is_v][1]), byte[i][is_v], o);
+          store32(reinterpret_cast<uint8_t*>(p.p + (int64_t)(t0 + tok[i]) * p.ts + (int64_t)head[i] * p.hs + ln * kGroup), o,
+                  a.wide);
+        }
+      }
+    }
+  }
 }
 
 // kLanes threads a row, the power of two from dim / kEl up
@@ -91,12 +206,23 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
   // Rows on their way, K and V in turn: as many as a thread's registers hold (8294 tokens x 8 heads written and read back:
   // bf16 with two 35 us, with four 26; e4m3 written with four 26.8, with two 24.9; 38 k e4m3 tokens read with two 43, with four 41)
   constexpr int kAhead = kFormat != kBf16 && kWrite ? 2 : 4;
-  constexpr int kWords = kWrite || kFormat == kBf16 ? 8 : kFormat == kE4M3 ? 4 : 2;
+  constexpr int kWords = kWrite || kFormat == kBf16 ? 8 : 4;
   __shared__ int2 s_place[kTokens];
   pdl_trigger();
   pdl_wait();
   const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n_rows - t0);
-  {
+  const bool few = a.c.n_seq < kThreads;
+  __shared__ int s_cu[kThreads], s_lens[kThreads];
+  if (few) {  // all sequences at once: two loads one after the other, with the table's, in place of four and more
+    if ((int)threadIdx.x <= a.c.n_seq) s_cu[threadIdx.x] = __ldcg(a.cu + threadIdx.x);
+    if ((int)threadIdx.x < a.c.n_seq) s_lens[threadIdx.x] = __ldcg(a.c.seq_lens + threadIdx.x);
+    __syncthreads();
+    if ((int)threadIdx.x < nt) {
+      const int2 at = place_in(a, t0 + threadIdx.x, s_cu, s_lens);
+      if (at.x == -2) mv_set_error_detail(a.err, kPagedRowsSite, MV_DEVERR_INDEX, (uint32_t)(t0 + threadIdx.x));
+      s_place[threadIdx.x] = at;
+    }
+  } else {
     const int i = threadIdx.x / a.look_lanes;
     if (i < nt) {
       const int2 at = place_of(a, t0 + i, a.look_lanes);
@@ -117,6 +243,10 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
   const int ln = threadIdx.x % kLanes, group = threadIdx.x / kLanes, d0 = ln * kEl;  // elements d0 .. of a row
   const int H = a.c.heads, D = a.c.dim, P = a.c.page_size;
   const int pairs = nt * H;  // a row of K and one of V, which lie at the same place of the two pools
+  if constexpr (kFormat == kE2M1) {
+    move_e2m1<kWrite, kLanes>(a, s_place, t0, nt);
+    return;
+  }
   // The order of the rows is the source's: heads, then tokens of the caller's; tokens, then heads of the pool's
   const int n_fast = kWrite ? H : nt, add_slow = kGroups / n_fast, add_fast = kGroups % n_fast;
   int slow = group / n_fast, fast = group - slow * n_fast;
@@ -132,22 +262,17 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
       const int2 at = r0 + i / 2 * kGroups < pairs ? s_place[tok] : make_int2(-1, 0);
       if (at.x >= 0 && d0 < D) {
         const int64_t prow = ((int64_t)at.x * H + h) * P + at.y;
-        const int64_t held_at = kFormat == kE2M1 ? (prow * D + d0) / 2 : (prow * D + d0) * (kFormat == kE4M3 ? 1 : 2);
+        const int64_t held_at = (prow * D + d0) * (kFormat == kE4M3 ? 1 : 2);
 #pragma unroll
         for (int is_v = 0; is_v < 2; ++is_v) {
           const RowsArgs& p = is_v ? a.v : a.k;
           uint8_t* row = reinterpret_cast<uint8_t*>(p.p + (int64_t)(t0 + tok) * p.ts + (int64_t)h * p.hs + d0);
           uint8_t* held = (is_v ? a.c.v : a.c.k) + held_at;
           to[i + is_v] = kWrite ? held : row;
-          if (kFormat != kBf16)
-            exp[i + is_v] = (is_v ? a.c.v_exp : a.c.k_exp) + (kFormat == kE2M1 ? prow * (D / kGroup) + ln : prow);
+          if (kFormat != kBf16) exp[i + is_v] = (is_v ? a.c.v_exp : a.c.k_exp) + prow;
           const uint8_t* from = kWrite ? row : held;
           if constexpr (kWords == 8) {
             load32(from, x[i + is_v], a.wide);
-          } else if constexpr (kWords == 2) {
-            const uint2 w = *reinterpret_cast<const uint2*>(from);
-            x[i + is_v][0] = w.x;
-            x[i + is_v][1] = w.y;
           } else {
             const uint4 w = *reinterpret_cast<const uint4*>(from);
             x[i + is_v][0] = w.x;
@@ -169,39 +294,6 @@ __global__ void __launch_bounds__(kThreads, kResident) paged_rows_kernel(const M
     for (int i = 0; i < kAhead; ++i) {
       if constexpr (kFormat == kBf16) {
         if (to[i]) store32(to[i], x[i], a.wide);
-      } else if constexpr (kFormat == kE2M1 && kWrite) {
-        if (!to[i]) continue;
-        uint32_t top = 0u;  // of the 16, without the sign: bf16 bits are ordered as their values are, NaN above infinity
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = __vmaxu2(top, x[i][j] & 0x7fff7fffu);
-        top = max(top & 0xffffu, top >> 16);
-        const bool finite = top < 0x7f80u;
-        const uint32_t b = finite ? scale_byte(__fdiv_rn(bf16lo(top), 6.0f)) : kNanScale;
-        const float inv = b && finite ? __fdiv_rn(1.0f, scale_value(b)) : 0.0f;
-        auto quotient = [&](float f) { return __fsub_rn(__fmaf_rn(f, inv, 6144.0f), 6144.0f); };
-        uint32_t q[2] = {0u, 0u};
-        if (finite)  // what an infinity or a NaN times zero becomes does not matter under a scale that is none
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            q[j >> 1] |= float4_to_e2m1x4(quotient(bf16lo(x[i][2 * j])), quotient(bf16hi(x[i][2 * j])),
-                                          quotient(bf16lo(x[i][2 * j + 1])), quotient(bf16hi(x[i][2 * j + 1]))) << (16 * (j & 1));
-        *reinterpret_cast<uint2*>(to[i]) = make_uint2(q[0], q[1]);
-        *exp[i] = (uint8_t)b;
-      } else if constexpr (kFormat == kE2M1) {
-        if (!to[i]) continue;
-        const float s = scale_value(byte[i]);
-        uint32_t o[8];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t h[4];
-          e2m1x8_to_half2(x[i][j], h);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = half2_to_float2(h[k]);
-            o[4 * j + k] = pack_bf16x2(f.x * s, f.y * s);
-          }
-        }
-        store32(to[i], o, a.wide);
       } else if constexpr (kWrite) {
         float f[16], top = 0.0f;
 #pragma unroll

@@ -7,23 +7,25 @@
 // angle without its whole turns, exact to position * 2^-64 turns: a position of 2^31 is as good as one of 1. (In fp32 an
 // angle of a million radians is off by up to 0.03.)
 //
-// Bound by memory: 2 bytes read and 2 written for each element; about 110 instructions for 16 elements of a thread. A thread
-// takes 16 elements of a row as two pieces of 16 bytes, chosen so that pairs meet in it; what is left to exchange is the sum
-// of squares. A CTA takes the rows of a few tokens: their sines and cosines are computed once for all heads, while the first
-// rows are on their way.
+// Bound by memory: 2 bytes read and 2 written for each element. A warp takes some heads of one token, a group of lanes to a
+// head: side by side in memory and then the next ones. A lane has 16 elements of a head as two pieces of 16 bytes, chosen
+// so that pairs meet in it; what is left to exchange
+// is the sum of squares. What a lane's elements are multiplied with but for the row's own factor, cosines and sines times
+// gains, it computes once for all its heads. Sine and cosine are the special-function unit's (within 2^-21.4, below the
+// 2^-9 of the result's rounding); the angle is within half a turn of zero there.
 #include <algorithm>
 
 #include "kernels.cuh"
 #include "paged.cuh"
+#include "tc.cuh"
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxRopeDim = 256;
-constexpr int kAhead = 2;        // rows of a thread on their way
-constexpr int kResident = 3;     // CTAs of an SM
-constexpr int kRows = 256;       // of a CTA, about
-constexpr int kTokens = 16;      // of a CTA, at most
+constexpr int kAhead = 4;         // rows of a group on their way
+constexpr int kResident = 5;      // CTAs of an SM
+constexpr int kWarpsWanted = 24;  // of an SM
 
 struct RopeArgs {
   RowsArgs q, k, q_out, k_out;
@@ -32,129 +34,158 @@ struct RopeArgs {
   const uint64_t* turns;            // [rot / 2]
   float eps;
   int n_tokens, heads, kv_heads, dim, rot;
-  int tokens, span;                 // tokens of a CTA, and heads (of Q and K together)
+  int span, q_spans, spans;         // heads of a warp, warps of a token for Q, and in all
 };
 
-MV_DEV void unpack8(const uint4& w, float (&f)[8]) {
+MV_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Eight bf16 as four pairs of fp32, and back
+MV_DEV void unpack8(const uint4& w, uint64_t (&f)[4]) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16lo(x[i]);
-    f[2 * i + 1] = bf16hi(x[i]);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = pack2(bf16lo(x[i]), bf16hi(x[i]));
 }
-MV_DEV uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+MV_DEV uint4 pack8(const uint64_t (&f)[4]) {
+  uint32_t x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2(f[i]);
+    x[i] = pack_bf16x2(v.x, v.y);
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+MV_DEV void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+MV_DEV uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
 }
 
 // kLanes threads a row, the power of two from dim / 16 up. kNeighbours: pairs (2 i, 2 i + 1).
 template <int kLanes, bool kNeighbours>
 __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const RopeArgs a) {
-  __shared__ float s_cos[kTokens * kMaxRopeDim / 2], s_sin[kTokens * kMaxRopeDim / 2];
-  __shared__ bool s_real[kTokens];
-  constexpr int kGroups = kThreads / kLanes;  // rows at a time
-  const int tid = threadIdx.x, j = tid % kLanes, group = tid / kLanes;
-  const int half = a.rot / 2, turned = a.rot / 16;  // lanes whose elements are turned
-  const int t0 = blockIdx.x * a.tokens, nt = min(a.tokens, a.n_tokens - t0);
-  const int h0 = blockIdx.y * a.span, nh = min(a.span, a.heads + a.kv_heads - h0);
+  constexpr int kGroups = 32 / kLanes;
+  __shared__ uint4 s_x[kAhead][2][kThreads];  // each thread's pieces on their way
+  const int j = threadIdx.x % kLanes, group = threadIdx.x % 32 / kLanes;
+  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32;
   const bool mine = j < a.dim / 16;
-  // this thread's pieces of 8 elements: pairs of halves meet across R/2 elements, what is not turned lies side by side
-  const bool rot = mine && j < turned;
-  const int e0 = kNeighbours || !rot ? 16 * j : 8 * j, e1 = kNeighbours || !rot ? 16 * j + 8 : 8 * j + half;
-  uint4 gain[2][2];
+  // this lane's pieces of 8 elements: pairs of halves meet across R/2 elements, what is not turned lies side by side
+  const bool rot = mine && j < a.rot / 16;
+  const int e0 = kNeighbours || !rot ? 16 * j : 8 * j, e1 = kNeighbours || !rot ? 16 * j + 8 : 8 * j + a.rot / 2;
+  const int t = (int)(unit / a.spans), part = (int)(unit - (int64_t)t * a.spans);
+  const bool is_k = part >= a.q_spans;
+  const int h_from = (is_k ? part - a.q_spans : part) * a.span, h_to = min(h_from + a.span, is_k ? a.kv_heads : a.heads);
+  uint4 g0 = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), g1 = g0;
+  const uint16_t* gain = is_k ? a.k_gain : a.q_gain;
+  if (gain && mine) {
+    g0 = *reinterpret_cast<const uint4*>(gain + e0);
+    g1 = *reinterpret_cast<const uint4*>(gain + e1);
+  }
+  uint64_t turns[8];
+  if (rot) {
 #pragma unroll
-  for (int is_k = 0; is_k < 2; ++is_k) {
-    const uint16_t* g = is_k ? a.k_gain : a.q_gain;
-    const uint32_t one = 0x3f803f80u;
-    gain[is_k][0] = gain[is_k][1] = make_uint4(one, one, one, one);
-    if (g && mine) {
-      gain[is_k][0] = *reinterpret_cast<const uint4*>(g + e0);
-      gain[is_k][1] = *reinterpret_cast<const uint4*>(g + e1);
-    }
+    for (int i = 0; i < 8; ++i) turns[i] = __ldg(a.turns + 8 * j + i);
   }
   pdl_trigger();
   pdl_wait();
-  const int rows = nt * nh, add_t = kGroups / nh, add_h = kGroups - add_t * nh;
-  int tok = group / nh, h = group - tok * nh;  // of the next row that is asked for
-  uint4 x[kAhead][2];
-  int at_t[kAhead], at_h[kAhead];
-  auto ask = [&](int r0) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      at_t[i] = tok;
-      at_h[i] = h0 + h;
-      x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (r0 + i * kGroups < rows && mine) {
-        const bool is_k = at_h[i] >= a.heads;
-        const RowsArgs& p = is_k ? a.k : a.q;
-        const uint16_t* row = p.p + (int64_t)(t0 + tok) * p.ts + (int64_t)(is_k ? at_h[i] - a.heads : at_h[i]) * p.hs;
-        x[i][0] = __ldcg(reinterpret_cast<const uint4*>(row + e0));
-        x[i][1] = __ldcg(reinterpret_cast<const uint4*>(row + e1));
-      }
-      tok += add_t;
-      h += add_h;
-      if (h >= nh) {
-        h -= nh;
-        ++tok;
-      }
+  if (t >= a.n_tokens) return;
+  const int pos = a.positions ? __ldcg(a.positions + t) : 0;
+  const RowsArgs& from = is_k ? a.k : a.q;
+  const uint16_t* src = from.p + (int64_t)t * from.ts + (h_from + group) * from.hs;
+  const int64_t src_add = from.hs * kGroups;
+  const uint32_t mem = smem_u32(&s_x[0][0][threadIdx.x]);
+  int asked = h_from + group;
+  auto ask = [&](int slot) {
+    if (asked < h_to && mine) {
+      cp_async16(mem + slot * (2 * kThreads * 16), src + e0);
+      cp_async16(mem + slot * (2 * kThreads * 16) + kThreads * 16, src + e1);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asked += kGroups;
+    src += src_add;
   };
-  ask(group);
-  for (int i = tid; i < nt * half; i += kThreads) {
-    const int t = i / half, f = i - t * half;
-    const uint64_t angle = (uint64_t)(uint32_t)__ldcg(a.positions + t0 + t) * __ldg(a.turns + f);
-    // in half turns, -1 .. 1
-    sincospif((float)(int32_t)(angle >> 32) * 4.656612873077393e-10f, &s_sin[i], &s_cos[i]);
-  }
-  if (tid < nt) s_real[tid] = !a.positions || __ldcg(a.positions + t0 + tid) >= 0;
-  __syncthreads();
-  const float inv = 1.0f / (float)a.dim;
-  for (int r0 = group; r0 < rows; r0 += kAhead * kGroups) {  // the lanes of a group stay together
-    if (r0 != group) ask(r0);
-    const unsigned int mask = kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1u) << (tid & 31 & ~(kLanes - 1));
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const bool real = r0 + i * kGroups < rows && s_real[at_t[i]];
-      float u[8], v[8], sum = 0.0f;
-      unpack8(x[i][0], u);
-      unpack8(x[i][1], v);
+  for (int i = 0; i < kAhead; ++i) ask(i);
+  // The first piece's elements times `a0`, plus the other element of their pairs times `b0`; the second piece's `a1`, `b1`.
+  // Pairs of halves: the other piece's element of the same place. Neighbours: the one beside it.
+  uint64_t a0[4], a1[4], b0[4] = {}, b1[4] = {};
+  unpack8(g0, a0);
+  unpack8(g1, a1);
+  if (rot) {
+    float c[8], s[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += u[e] * u[e] + v[e] * v[e];
-#pragma unroll
-      for (int o = kLanes >> 1; o >= 1; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
-      if (!real || !mine) continue;
-      const bool is_k = at_h[i] >= a.heads;
-      const float f = rsqrtf(sum * inv + a.eps);
-      float g[8];
-      unpack8(is_k ? gain[1][0] : gain[0][0], g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] *= f * g[e];
-      unpack8(is_k ? gain[1][1] : gain[0][1], g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= f * g[e];
-      if (rot) {
-        float c[8], s[8];
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const int at = at_t[i] * half + 8 * j + e;
-          const float4 c4 = *reinterpret_cast<const float4*>(s_cos + at), s4 = *reinterpret_cast<const float4*>(s_sin + at);
-          c[e] = c4.x, c[e + 1] = c4.y, c[e + 2] = c4.z, c[e + 3] = c4.w;
-          s[e] = s4.x, s[e + 1] = s4.y, s[e + 2] = s4.z, s[e + 3] = s4.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float& p = kNeighbours ? (e < 4 ? u[(2 * e) & 7] : v[(2 * e) & 7]) : u[e];
-          float& q = kNeighbours ? (e < 4 ? u[(2 * e + 1) & 7] : v[(2 * e + 1) & 7]) : v[e];
-          const float was = p;
-          p = was * c[e] - q * s[e];
-          q = q * c[e] + was * s[e];
-        }
-      }
-      const RowsArgs& p = is_k ? a.k_out : a.q_out;
-      uint16_t* row = p.p + (int64_t)(t0 + at_t[i]) * p.ts + (int64_t)(is_k ? at_h[i] - a.heads : at_h[i]) * p.hs;
-      *reinterpret_cast<uint4*>(row + e0) = pack8(u);
-      *reinterpret_cast<uint4*>(row + e1) = pack8(v);
+    for (int e = 0; e < 8; ++e) {
+      const int32_t part_of = (int32_t)((uint64_t)(uint32_t)pos * turns[e] >> 32);  // of a turn, -2^31 .. 2^31 - 1
+      const float angle = (float)part_of * 1.4629180792671596e-09f;                 // 2 pi / 2^32
+      c[e] = __cosf(angle);
+      s[e] = __sinf(angle);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 u = unpack2(a0[e]), v = unpack2(a1[e]);
+      if (kNeighbours) {
+        a0[e] = pack2(u.x * c[e], u.y * c[e]);
+        b0[e] = pack2(-u.y * s[e], u.x * s[e]);
+        a1[e] = pack2(v.x * c[4 + e], v.y * c[4 + e]);
+        b1[e] = pack2(-v.y * s[4 + e], v.x * s[4 + e]);
+      } else {
+        a0[e] = pack2(u.x * c[2 * e], u.y * c[2 * e + 1]);
+        b0[e] = pack2(-v.x * s[2 * e], -v.y * s[2 * e + 1]);
+        a1[e] = pack2(v.x * c[2 * e], v.y * c[2 * e + 1]);
+        b1[e] = pack2(u.x * s[2 * e], u.y * s[2 * e + 1]);
+      }
+    }
+  }
+  const float inv = 1.0f / (float)a.dim;
+  const RowsArgs& to = is_k ? a.k_out : a.q_out;
+  uint16_t* dst = to.p + (int64_t)t * to.ts + (h_from + group) * to.hs;
+  const int64_t dst_add = to.hs * kGroups;
+  int slot = 0;
+#pragma unroll 1
+  for (int h0 = h_from; h0 < h_to; h0 += kGroups) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    uint64_t u[4] = {}, v[4] = {}, sums = 0;
+    if (mine) {
+      unpack8(lds16(mem + slot * (2 * kThreads * 16)), u);
+      unpack8(lds16(mem + slot * (2 * kThreads * 16) + kThreads * 16), v);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sums = fma2(u[e], u[e], fma2(v[e], v[e], sums));
+    float sum = unpack2(sums).x + unpack2(sums).y;
+#pragma unroll
+    for (int o = kLanes >> 1; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    ask(slot);
+    slot = slot + 1 == kAhead ? 0 : slot + 1;
+    const float by = rsqrtf(sum * inv + a.eps);
+    uint64_t y0[4], y1[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y0[e] = mul2(u[e], a0[e]);
+      y1[e] = mul2(v[e], a1[e]);
+    }
+    if (rot)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 p = unpack2(u[e]), r = unpack2(v[e]);
+        y0[e] = fma2(kNeighbours ? pack2(p.y, p.x) : v[e], b0[e], y0[e]);
+        y1[e] = fma2(kNeighbours ? pack2(r.y, r.x) : u[e], b1[e], y1[e]);
+      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y0[e] = mul2(y0[e], pack2(by, by));
+      y1[e] = mul2(y1[e], pack2(by, by));
+    }
+    if (mine && h0 + group < h_to && pos >= 0) {
+      *reinterpret_cast<uint4*>(dst + e0) = pack8(y0);
+      *reinterpret_cast<uint4*>(dst + e1) = pack8(y1);
+    }
+    dst += dst_add;
   }
 }
 
@@ -203,13 +234,16 @@ extern "C" mv_status qk_norm_rope(mv_rows q, mv_rows k, int32_t n_tokens, int32_
   a.rot = rot_dim;
   int lanes = 1;
   while (16 * lanes < head_dim) lanes *= 2;
-  // about kRows rows a CTA, of fewer tokens or heads where the GPU would not be full
-  const int all = n_heads + n_kv_heads, groups = kThreads / lanes;
-  const int64_t ctas = (int64_t)kResident * mv_sm_count();
-  a.tokens = std::max(1, std::min(kTokens, kRows / all));
-  a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(a.tokens, n_tokens / ctas));
-  a.span = a.tokens > 1 ? all : std::min(all, n_tokens >= ctas ? kRows : groups);
-  const dim3 grid((n_tokens + a.tokens - 1) / a.tokens, (all + a.span - 1) / a.span);
+  // heads of a warp: few enough for kWarpsWanted warps on every SM, in rounds of all groups
+  const int round = 32 / lanes;
+  const int64_t warps = (int64_t)mv_sm_count() * kWarpsWanted, rounds = (std::max(n_heads, n_kv_heads) + round - 1) / round;
+  const int64_t all = (int64_t)n_tokens * ((n_heads + n_kv_heads + round - 1) / round);
+  a.span = round * (int)std::min<int64_t>(rounds, std::max<int64_t>(1, (all + warps - 1) / warps));
+  a.q_spans = (n_heads + a.span - 1) / a.span;
+  a.spans = a.q_spans + (n_kv_heads + a.span - 1) / a.span;
+  const int64_t ctas = ((int64_t)n_tokens * a.spans * 32 + kThreads - 1) / kThreads;
+  if (ctas > 0x7fffffff) return MV_ERR_SHAPE;
+  const dim3 grid((unsigned)ctas);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = lanes == 16  ? launch_rope<16>(a, grid, neighbours, st)
                         : lanes == 8 ? launch_rope<8>(a, grid, neighbours, st)

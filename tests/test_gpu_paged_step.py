@@ -3,9 +3,9 @@ with their rotation, rows held in 4 bits. (Attention over such rows: test_gpu_pa
 
 Tolerances. Whole numbers and what a cache holds are compared exactly. A rotated element may be off its float64 value by
   2^-8 |ref|     its rounding to bf16 (half a step),
-  40 2^-24 size  with size the length of its pair: fp32 sums of at most 256 squares in 16 + 4 steps, the reciprocal root (2
-                 units), products with it and the gain (2), the angle (a fraction of a turn rounded to 2^-25 of a half turn
-                 is 2^-25 pi radians: 2), its sine and cosine (2 each), two products and a sum (3), rounded up.
+  40 2^-24 size  with size the length of its pair: fp32 sums of at most 256 squares in 16 + 4 steps (under a root: 10 units of
+                 2^-24), the reciprocal root (2), products with it and the gain (3), the angle (rounded to 2^-24 of at most
+                 pi, and its factor: 7), its sine and cosine within 2^-21.4 each (6 each), two products and a sum (3), rounded up.
 """
 import numpy as np
 import pytest
