@@ -393,62 +393,18 @@ def pack_model_weights(w, drop_source=False):
 
 # --------------------------------------------------------------------------------------------- serving operators
 
-_torch = None       # the module, imported by the first call that takes tensors
-_raw_stream = None  # a device's current stream as an integer
+_compiled = None    # the compiled part of the binding: checks of tensors, and the calls (csrc/calls.cpp)
 
 
-def _load_torch():
-    global _torch, _raw_stream
-    import torch
-    _torch = torch
-    # torch.cuda.current_stream costs a microsecond, most of a small call's checks
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-        (lambda device: torch.cuda.current_stream(device).cuda_stream)
-    return torch
-
-
-def _rows(t, what, device, heads, dim, tokens):
-    """A bf16 tensor [tokens, heads, dim] on ``device`` (an index) as mv_rows; its last dimension must be contiguous."""
-    shape, strides = t.shape, t.stride()
-    if t.dtype is not _torch.bfloat16 or shape != (tokens, heads, dim) or t.get_device() != device or \
-            device < 0 or (strides[2] != 1 and dim != 1):
-        raise ValueError(f"{what}: a bf16 tensor [{tokens}, {heads}, {dim}] on CUDA device {device} with a contiguous last "
-                         f"dimension is wanted, got {t.dtype} {tuple(shape)} on {t.device} with strides {strides}")
-    return _Rows(t.data_ptr(), strides[0] if tokens > 1 else 0, strides[1] if heads > 1 else 0)
-
-
-def _heads(t, what):
-    """The tokens and heads of a tensor [tokens, heads, dim]."""
-    shape = t.shape
-    if len(shape) != 3:
-        raise ValueError(f"{what}: [tokens, heads, head_dim] is wanted, got {tuple(shape)}")
-    return shape[0], shape[1]
-
-
-def _ints(t, what, device, shape):
-    """The address of a contiguous int32 tensor of ``shape`` on ``device``; a 2-D one may have longer rows."""
-    if t.dtype is not _torch.int32 or t.shape != shape or t.get_device() != device or \
-            not (t.is_contiguous() or (len(shape) == 2 and t.stride(1) == 1)):
-        raise ValueError(f"{what}: a contiguous int32 tensor {tuple(shape)} on CUDA device {device} is wanted, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device} with strides {t.stride()}")
-    return t.data_ptr()
-
-
-def _call_on(device, stream, fn, *args):
-    """fn(*args, stream) with CUDA device ``device`` current, on ``stream`` or on that device's current stream."""
-    if stream is None:
-        raw = _raw_stream(device)
-    elif stream.device.index == device:
-        raw = stream.cuda_stream
-    else:
-        raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors are on CUDA device {device}")
-    if _torch.cuda.current_device() == device:
-        status = fn(*args, raw)
-    else:
-        with _torch.cuda.device(device):
-            status = fn(*args, raw)
-    if status:
-        raise MVError(status, fn.__name__)
+def _load_calls():
+    """The compiled calls, loaded by the first call that takes tensors."""
+    global _compiled
+    if _compiled is None:
+        import torch  # noqa: F401  (whose libraries the module is linked against)
+        lib()
+        from . import _calls
+        _compiled = _calls
+    return _compiled
 
 
 class PromptPlan:
@@ -491,13 +447,8 @@ class PromptPlan:
 def prompt_attention(q, k, v, plan: PromptPlan, scale, out, stream=None):
     """Causal attention of packed prompts: q, out bf16 [tokens, heads, D]; k, v bf16 [tokens, kv heads, D] (any strides
     that are multiples of 8, last dimension contiguous); tokens = plan.n_tokens at least, later rows are not touched."""
-    if _torch is None:
-        _load_torch()
-    (t, hq), (_, hk), n, d, dev = _heads(q, "q"), _heads(k, "k"), plan.n_tokens, q.shape[2], q.get_device()
-    if t < n:
-        raise ValueError(f"prompt_attention: the plan has {n} tokens, q {t}")
-    _call_on(dev, stream, lib().prompt_attention, _rows(q, "q", dev, hq, d, t), _rows(k, "k", dev, hk, d, t),
-             _rows(v, "v", dev, hk, d, t), hq, hk, d, plan.handle, scale, _rows(out, "out", dev, hq, d, t))
+    _check((_compiled or _load_calls()).prompt_attention(q, k, v, out, plan.handle.value, plan.n_tokens, scale, stream),
+           "prompt_attention")
 
 
 class PagedKV:
@@ -506,7 +457,7 @@ class PagedKV:
     kv heads, page_size, D / 2], k_exp, v_exp uint8 [n_pages, kv heads, page_size, D / 16] (see mv_paged_kv)."""
 
     def __init__(self, k, v, k_exp=None, v_exp=None):
-        torch = _load_torch()
+        import torch
         if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8) or v.dtype != k.dtype:
             raise ValueError(f"PagedKV: k and v are both bf16, both float8_e4m3fn or both uint8, got {k.dtype} and {v.dtype}")
         if k.dim() != 4 or v.shape != k.shape or not k.is_cuda:
@@ -531,7 +482,7 @@ class PagedKV:
         self._desc = _PagedKVDesc(k.data_ptr(), v.data_ptr(), k_exp.data_ptr() if want is not None else None,
                                   v_exp.data_ptr() if want is not None else None, dtype, self.n_pages, self.page_size,
                                   self.n_kv_heads, self.head_dim)
-        self._ref = ctypes.byref(self._desc)
+        self._at = ctypes.addressof(self._desc)
 
     @classmethod
     def zeros(cls, n_pages, page_size, n_kv_heads, head_dim, dtype=DTYPE_BF16, device="cuda"):
@@ -551,31 +502,18 @@ class PagedKV:
         ke, ve = (torch.zeros(shape[:3], dtype=torch.uint8, device=device) for _ in range(2))
         return cls(k, v, ke, ve)
 
-    def _seqs(self, block_table, seq_lens):
-        """block_table int32 [n_seq, pages] and seq_lens int32 [n_seq] as the arguments of the C entry points."""
-        shape, dev = block_table.shape, self.device
-        if len(shape) != 2:
-            raise ValueError(f"block_table: [n_seq, pages] is wanted, got {tuple(shape)}")
-        n, pages = shape
-        return (_ints(block_table, "block_table", dev, shape), block_table.stride(0) if n > 1 else pages, pages,
-                _ints(seq_lens, "seq_lens", dev, (n,)), n)
-
 
 def paged_kv_append(k, v, cu_rows, cache: PagedKV, block_table, seq_lens, stream=None):
     """Writes rows cu_rows[b] .. of k, v bf16 [rows, kv heads, D] as the last ones of sequence b (the last at position
     seq_lens[b] - 1); cu_rows int32 [n_seq + 1], block_table int32 [n_seq, pages], seq_lens int32 [n_seq]."""
-    dev, h, d, seqs = cache.device, cache.n_kv_heads, cache.head_dim, cache._seqs(block_table, seq_lens)
-    rows, _ = _heads(k, "k")
-    _call_on(dev, stream, lib().paged_kv_append, _rows(k, "k", dev, h, d, rows), _rows(v, "v", dev, h, d, rows), rows,
-             _ints(cu_rows, "cu_rows", dev, (seqs[4] + 1,)), cache._ref, *seqs)
+    _check((_compiled or _load_calls()).paged_kv_append(k, v, cu_rows, cache._at, cache.device, block_table, seq_lens, stream),
+           "paged_kv_append")
 
 
 def paged_kv_read(cache: PagedKV, block_table, seq_lens, cu_rows, k_out, v_out, stream=None):
     """The last rows of every sequence as bf16 [rows, kv heads, D]: the mirror of paged_kv_append."""
-    dev, h, d, seqs = cache.device, cache.n_kv_heads, cache.head_dim, cache._seqs(block_table, seq_lens)
-    rows, _ = _heads(k_out, "k_out")
-    _call_on(dev, stream, lib().paged_kv_read, cache._ref, *seqs, _ints(cu_rows, "cu_rows", dev, (seqs[4] + 1,)), rows,
-             _rows(k_out, "k_out", dev, h, d, rows), _rows(v_out, "v_out", dev, h, d, rows))
+    _check((_compiled or _load_calls()).paged_kv_read(k_out, v_out, cu_rows, cache._at, cache.device, block_table, seq_lens, stream),
+           "paged_kv_read")
 
 
 def paged_attention_workspace(n_seq, n_heads, n_kv_heads, head_dim):
@@ -584,12 +522,8 @@ def paged_attention_workspace(n_seq, n_heads, n_kv_heads, head_dim):
 
 def paged_attention(q, cache: PagedKV, block_table, seq_lens, scale, out, workspace, stream=None):
     """One new token per sequence: q, out bf16 [n_seq, heads, D]; attends to the first seq_lens[b] rows of sequence b."""
-    dev, d, seqs = cache.device, cache.head_dim, cache._seqs(block_table, seq_lens)
-    n, (_, heads) = seqs[4], _heads(q, "q")
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"paged_attention: a contiguous workspace on CUDA device {dev} is wanted")
-    _call_on(dev, stream, lib().paged_attention, _rows(q, "q", dev, heads, d, n), heads, cache._ref, *seqs, scale,
-             _rows(out, "out", dev, heads, d, n), workspace.data_ptr(), workspace.nbytes)
+    _check((_compiled or _load_calls()).paged_attention(q, out, workspace, scale, cache._at, cache.device, block_table, seq_lens,
+                                                     stream), "paged_attention")
 
 
 def paged_kv_resize(by, cache: PagedKV, block_table, seq_lens, free_pages, cu_rows=None, positions=None, slots=None,
@@ -597,24 +531,8 @@ def paged_kv_resize(by, cache: PagedKV, block_table, seq_lens, free_pages, cu_ro
     """Each sequence grows or shrinks by ``by`` int32 [n_seq] tokens: seq_lens, block_table and free_pages int32 [1 +
     n_pages] (how many are free, then the stack of them) follow; cu_rows int32 [n_seq + 1], positions int32 [rows] and slots
     int64 [rows] are written for the rows that come, -1 behind the last one. ``cache``: any of the layers' caches."""
-    dev, seqs = cache.device, cache._seqs(block_table, seq_lens)
-    n, rows, at = seqs[4], 0, [None, None, None]
-    if cu_rows is not None:
-        at[0] = _ints(cu_rows, "cu_rows", dev, (n + 1,))
-    elif positions is not None or slots is not None:
-        raise ValueError("paged_kv_resize: positions and slots are of the rows that cu_rows counts")
-    if positions is not None:
-        rows = positions.numel()
-        at[1] = _ints(positions, "positions", dev, (rows,))
-    if slots is not None:
-        if slots.dtype is not _torch.int64 or slots.get_device() != dev or not slots.is_contiguous() or slots.dim() != 1 or \
-                (positions is not None and slots.numel() != rows):
-            raise ValueError(f"slots: a contiguous int64 tensor on CUDA device {dev} of as many rows as positions is wanted, "
-                             f"got {slots.dtype} {tuple(slots.shape)} on {slots.device}")
-        rows = slots.numel()
-        at[2] = slots.data_ptr()
-    _call_on(dev, stream, lib().paged_kv_resize, _ints(by, "by", dev, (n,)), n, cache.page_size, cache.n_pages, *seqs[:4],
-             _ints(free_pages, "free_pages", dev, (1 + cache.n_pages,)), *at, rows)
+    _check((_compiled or _load_calls()).paged_kv_resize(by, free_pages, cu_rows, positions, slots, cache._at, cache.device,
+                                                     block_table, seq_lens, stream), "paged_kv_resize")
 
 
 class Rope:
@@ -623,7 +541,7 @@ class Rope:
     (2 i, 2 i + 1). Held on the current device, or on ``device``, as parts of a turn in 64 bits (see qk_norm_rope)."""
 
     def __init__(self, rot_dim, theta=10000.0, neighbours=False, freqs=None, device=None):
-        torch = _load_torch()
+        import torch
         if rot_dim < 16 or rot_dim % 16:
             raise ValueError(f"Rope: rot_dim is a multiple of 16, got {rot_dim}")
         if freqs is None:
@@ -637,45 +555,15 @@ class Rope:
         self.rot_dim, self.neighbours = rot_dim, bool(neighbours)
         self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns], dtype=torch.int64,
                                   device="cuda" if device is None else device)
-        self._at = self.turns.data_ptr(), rot_dim, int(self.neighbours)
-
-
-_NO_ROWS = _Rows(None, 0, 0)
 
 
 def qk_norm_rope(q, k, q_gain, k_gain, eps, positions, rope: Rope, q_out=None, k_out=None, stream=None):
     """Heads of q bf16 [tokens, heads, D] and k bf16 [tokens, kv heads, D] divided by their root mean square, times q_gain
     and k_gain (bf16 [D] or None), turned by positions int32 [tokens] as ``rope`` says (None: not turned), into q_out and
     k_out or in place. Rows of a negative position are left as they were. q or k may be None."""
-    if _torch is None:
-        _load_torch()
-    x = q if q is not None else k
-    if x is None:
-        raise ValueError("qk_norm_rope: q and k are both None")
-    (t, _), d, dev = _heads(x, "q" if q is not None else "k"), x.shape[2], x.get_device()
-
-    def rows(x, to, gain, what):
-        if x is None:
-            if to is not None or gain is not None:
-                raise ValueError(f"qk_norm_rope: {what} is None, its gain or output is not")
-            return _NO_ROWS, 0, None, _NO_ROWS
-        h = _heads(x, what)[1]
-        src = _rows(x, what, dev, h, d, t)
-        if gain is not None and (gain.dtype is not _torch.bfloat16 or gain.shape != (d,) or gain.get_device() != dev or
-                                 not gain.is_contiguous()):
-            raise ValueError(f"{what}_gain: a contiguous bf16 tensor [{d}] on CUDA device {dev} is wanted, got {gain.dtype} "
-                             f"{tuple(gain.shape)} on {gain.device}")
-        return src, h, None if gain is None else gain.data_ptr(), src if to is None else _rows(to, what + "_out", dev, h, d, t)
-
-    q_in, hq, qg, q_to = rows(q, q_out, q_gain, "q")
-    k_in, hk, kg, k_to = rows(k, k_out, k_gain, "k")
-    if rope is not None and rope.turns.get_device() != dev:
-        raise ValueError(f"qk_norm_rope: the rope is on {rope.turns.device}, the tensors are on CUDA device {dev}")
-    if positions is None and rope is not None:
-        raise ValueError("qk_norm_rope: a rotation wants positions")
-    _call_on(dev, stream, lib().qk_norm_rope, q_in, k_in, t, hq, hk, d, qg, kg, eps,
-             None if positions is None else _ints(positions, "positions", dev, (t,)),
-             *(rope._at if rope is not None else (None, 0, 0)), q_to, k_to)
+    turns, neighbours = (None, 0) if rope is None else (rope.turns, rope.neighbours)
+    _check((_compiled or _load_calls()).qk_norm_rope(q, k, q_gain, k_gain, q_out, k_out, eps, positions, turns, neighbours, stream),
+           "qk_norm_rope")
 
 
 # --------------------------------------------------------------------------------------------- model / session

@@ -55,7 +55,7 @@ def test_rope_refusals():
                dict(hq=-1), dict(hk=257)):
         assert rope(**kw) == SHAPE, kw
     assert rope(n=0) == rope(hq=0, hk=0) == 0                 # nothing to do
-    assert rope(hq=0, q=mv._NO_ROWS, qo=mv._NO_ROWS, k=rows(ptr=None)) == INVALID
+    assert rope(hq=0, q=rows(ptr=None, ts=0, hs=0), qo=rows(ptr=None, ts=0, hs=0), k=rows(ptr=None)) == INVALID
 
 
 def test_binding_refusals():
