@@ -7,8 +7,8 @@
 // angle without its whole turns, exact to position * 2^-64 turns: a position of 2^31 is as good as one of 1. (In fp32 an
 // angle of a million radians is off by up to 0.03.)
 //
-// Bound by memory: 2 bytes read and 2 written for each element. A warp takes some heads of one token, a group of lanes to a
-// head: side by side in memory and then the next ones. A lane has 16 elements of a head as two pieces of 16 bytes, chosen
+// Bound by memory: 2 bytes read and 2 written for each element. A warp takes some heads of one token (few heads: of
+// several), a group of lanes to a head: side by side in memory and then the next ones. A lane has 16 elements of a head as two pieces of 16 bytes, chosen
 // so that pairs meet in it; what is left to exchange
 // is the sum of squares. What a lane's elements are multiplied with but for the row's own factor, cosines and sines times
 // gains, it computes once for all its heads. Sine and cosine are the special-function unit's (within 2^-21.4, below the
@@ -34,7 +34,9 @@ struct RopeArgs {
   const uint64_t* turns;            // [rot / 2]
   float eps;
   int n_tokens, heads, kv_heads, dim, rot;
-  int span, q_spans, spans;         // heads of a warp, warps of a token for Q, and in all
+  // For Q and for K: log2 of the tokens that a warp takes, the most of their heads that it does, and warps for all of these
+  int tokens_log2[2], span[2];
+  unsigned int spans[2], q_warps;   // q_warps: of Q
 };
 
 MV_DEV uint64_t mul2(uint64_t a, uint64_t b) {
@@ -73,14 +75,17 @@ __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const
   constexpr int kGroups = 32 / kLanes;
   __shared__ uint4 s_x[kAhead][2][kThreads];  // each thread's pieces on their way
   const int j = threadIdx.x % kLanes, group = threadIdx.x % 32 / kLanes;
-  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32;
+  const unsigned int unit = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
   const bool mine = j < a.dim / 16;
   // this lane's pieces of 8 elements: pairs of halves meet across R/2 elements, what is not turned lies side by side
   const bool rot = mine && j < a.rot / 16;
   const int e0 = kNeighbours || !rot ? 16 * j : 8 * j, e1 = kNeighbours || !rot ? 16 * j + 8 : 8 * j + a.rot / 2;
-  const int t = (int)(unit / a.spans), part = (int)(unit - (int64_t)t * a.spans);
-  const bool is_k = part >= a.q_spans;
-  const int h_from = (is_k ? part - a.q_spans : part) * a.span, h_to = min(h_from + a.span, is_k ? a.kv_heads : a.heads);
+  const int is_k = unit >= a.q_warps, log2 = a.tokens_log2[is_k], per_token = kGroups >> log2;  // groups of a token
+  const unsigned int mine_of = is_k ? unit - a.q_warps : unit, block = mine_of / a.spans[is_k];
+  const int h_from = (int)(mine_of - block * a.spans[is_k]) * a.span[is_k], heads = is_k ? a.kv_heads : a.heads;
+  const int h_to = min(h_from + a.span[is_k], heads);
+  const int64_t t_first = (int64_t)block << log2, t = t_first + group / per_token;
+  const bool real = t < a.n_tokens;
   uint4 g0 = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), g1 = g0;
   const uint16_t* gain = is_k ? a.k_gain : a.q_gain;
   if (gain && mine) {
@@ -94,20 +99,21 @@ __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const
   }
   pdl_trigger();
   pdl_wait();
-  if (t >= a.n_tokens) return;
-  const int pos = a.positions ? __ldcg(a.positions + t) : 0;
+  if (t_first >= a.n_tokens) return;  // the whole warp
+  const int pos = !real ? -1 : a.positions ? __ldcg(a.positions + t) : 0;
+  const int h_first = h_from + group % per_token;
   const RowsArgs& from = is_k ? a.k : a.q;
-  const uint16_t* src = from.p + (int64_t)t * from.ts + (h_from + group) * from.hs;
-  const int64_t src_add = from.hs * kGroups;
+  const uint16_t* src = from.p + t * from.ts + h_first * from.hs;
+  const int64_t src_add = from.hs * per_token;
   const uint32_t mem = smem_u32(&s_x[0][0][threadIdx.x]);
-  int asked = h_from + group;
+  int asked = real ? h_first : h_to;
   auto ask = [&](int slot) {
     if (asked < h_to && mine) {
       cp_async16(mem + slot * (2 * kThreads * 16), src + e0);
       cp_async16(mem + slot * (2 * kThreads * 16) + kThreads * 16, src + e1);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    asked += kGroups;
+    asked += per_token;
     src += src_add;
   };
 #pragma unroll
@@ -144,11 +150,11 @@ __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const
   }
   const float inv = 1.0f / (float)a.dim;
   const RowsArgs& to = is_k ? a.k_out : a.q_out;
-  uint16_t* dst = to.p + (int64_t)t * to.ts + (h_from + group) * to.hs;
-  const int64_t dst_add = to.hs * kGroups;
+  uint16_t* dst = to.p + t * to.ts + h_first * to.hs;
+  const int64_t dst_add = to.hs * per_token;
   int slot = 0;
 #pragma unroll 1
-  for (int h0 = h_from; h0 < h_to; h0 += kGroups) {
+  for (int h0 = h_from; h0 < h_to; h0 += per_token) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
     uint64_t u[4] = {}, v[4] = {}, sums = 0;
     if (mine) {
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const
       y0[e] = mul2(y0[e], pack2(by, by));
       y1[e] = mul2(y1[e], pack2(by, by));
     }
-    if (mine && h0 + group < h_to && pos >= 0) {
+    if (mine && h0 + group % per_token < h_to && pos >= 0) {
       *reinterpret_cast<uint4*>(dst + e0) = pack8(y0);
       *reinterpret_cast<uint4*>(dst + e1) = pack8(y1);
     }
@@ -234,15 +240,31 @@ extern "C" mv_status qk_norm_rope(mv_rows q, mv_rows k, int32_t n_tokens, int32_
   a.rot = rot_dim;
   int lanes = 1;
   while (16 * lanes < head_dim) lanes *= 2;
-  // heads of a warp: few enough for kWarpsWanted warps on every SM, in rounds of all groups
-  const int round = 32 / lanes;
-  const int64_t warps = (int64_t)mv_sm_count() * kWarpsWanted, rounds = (std::max(n_heads, n_kv_heads) + round - 1) / round;
-  const int64_t all = (int64_t)n_tokens * ((n_heads + n_kv_heads + round - 1) / round);
-  a.span = round * (int)std::min<int64_t>(rounds, std::max<int64_t>(1, (all + warps - 1) / warps));
-  a.q_spans = (n_heads + a.span - 1) / a.span;
-  a.spans = a.q_spans + (n_kv_heads + a.span - 1) / a.span;
-  const int64_t ctas = ((int64_t)n_tokens * a.spans * 32 + kThreads - 1) / kThreads;
-  if (ctas > 0x7fffffff) return MV_ERR_SHAPE;
+  // Fewer heads than a warp has groups: several tokens a warp. More: as many rounds of heads as leave kWarpsWanted warps to
+  // every SM.
+  const int groups = 32 / lanes;
+  const int64_t warps = (int64_t)mv_sm_count() * kWarpsWanted;
+  int64_t rounds = 0, all = 0;  // of a warp that does a token's heads, in all
+  for (int i = 0; i < 2; ++i) {
+    const int heads = i ? n_kv_heads : n_heads;
+    a.tokens_log2[i] = 0;
+    while (heads && groups >> (a.tokens_log2[i] + 1) >= heads) ++a.tokens_log2[i];
+    const int per_token = groups >> a.tokens_log2[i];
+    rounds = (heads + per_token - 1) / per_token;
+    all += rounds * (((int64_t)n_tokens >> a.tokens_log2[i]) + 1);
+  }
+  const int64_t most = std::max<int64_t>(1, (all + warps - 1) / warps);
+  int64_t total = 0;
+  for (int i = 0; i < 2; ++i) {
+    const int heads = i ? n_kv_heads : n_heads, per_token = groups >> a.tokens_log2[i];
+    rounds = (heads + per_token - 1) / per_token;
+    a.span[i] = per_token * (int)std::min(std::max<int64_t>(1, rounds), most);
+    a.spans[i] = std::max(1, (heads + a.span[i] - 1) / a.span[i]);
+    if (i == 1) a.q_warps = (unsigned int)total;
+    if (heads) total += (((int64_t)n_tokens + (1 << a.tokens_log2[i]) - 1) >> a.tokens_log2[i]) * a.spans[i];
+  }
+  // (below 2^32: two warps a token where there are that many)
+  const int64_t ctas = (total * 32 + kThreads - 1) / kThreads;
   const dim3 grid((unsigned)ctas);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = lanes == 16  ? launch_rope<16>(a, grid, neighbours, st)
