@@ -161,6 +161,13 @@ MV_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The first product of a sum, in fp16
+MV_DEV void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%10, %10, %10, %10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 MV_DEV uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -209,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using Ly = Layout<kDim, kFormat, kNT>;
   constexpr bool kFp16 = kFormat != kBf16;  // products in fp16
   constexpr float kGrow = kFormat == kE2M1 ? 2.0f : 8.0f, kLift = kFormat == kE2M1 ? 13.0f : 0.0f;  // see e2m1 above
+  constexpr float kLiftMost = 4194304.0f;  // 2^22: larger references are not lifted, a difference of 13 may round to 16 there
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t s_full[kWarps][Ly::kStages];
@@ -617,7 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < Ly::kSub; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[n][u][e] = 0.0f;
+          for (int e = 0; e < 4; ++e)
+            if (kFormat != kE2M1) x[n][u][e] = 0.0f;
       const bool tail = key0 + Ly::kKeys > len;
       if constexpr (kFormat == kE2M1) {
         if (tail) {  // rows behind the sequence hold anything: with scales of zero it is zero, codes being finite
@@ -666,9 +675,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; i += 2)
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
-                  mma<true>(x[n][u0 + u], f[0][i], f[1][i], f[0][i + 1], f[1][i + 1], qf[n][2 * j + i / 2][0],
-                            qf[n][2 * j + i / 2][1]);
+                for (int n = 0; n < kNT; ++n) {
+                  const uint32_t(&b)[2] = qf[n][2 * j + i / 2];
+                  if (j == 0 && i == 0) mma_first(x[n][u0 + u], f[0][i], f[1][i], f[0][i + 1], f[1][i + 1], b[0], b[1]);
+                  else mma<true>(x[n][u0 + u], f[0][i], f[1][i], f[0][i + 1], f[1][i + 1], b[0], b[1]);
+                }
             }
         }
       }
@@ -730,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               else v = key < len ? v * (kFormat == kE4M3 ? ks * mult[n][e] : mult[n][e]) : -INFINITY;
             }
         }
-      // e2m1: the least score of the step. (A row behind the sequence has 0, which counts here and does no harm.)
+      // e2m1: the least score of the step (a row behind the sequence has 0, which counts here and does no harm)
       float least_score[kNT][2];
       if (kFormat == kE2M1) {
 #pragma unroll
@@ -764,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < Ly::kSub; ++u)
 #pragma unroll
             for (int r = 0; r < 2; ++r) tx[n][e] = fmaxf(tx[n][e], x[n][u][2 * r + e]);
-          grow |= tx[n][e] > mx[n][e] + kGrow;
+          grow |= tx[n][e] > mx[n][e] + (kGrow + kLift);
         }
       if (__any_sync(0xffffffffu, grow)) {
         float shift = 1.0f;
@@ -779,7 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int w = 4; w <= 16; w <<= 1) tx[n][e] = fmaxf(tx[n][e], __shfl_xor_sync(0xffffffffu, tx[n][e], w));
-            const float nx = fmaxf(mx[n][e], tx[n][e]), f = weight(mx[n][e], nx), fo = f * shift;
+            const float to = kFormat == kE2M1 && fabsf(tx[n][e]) < kLiftMost ? tx[n][e] - kLift : tx[n][e];
+            const float nx = fmaxf(mx[n][e], to), f = weight(mx[n][e], nx), fo = f * shift;
             l[n][e] *= f;
 #pragma unroll
             for (int m = 0; m < Ly::kMT; ++m) {
@@ -802,7 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float& y = x[n][u][2 * r + e];
-              y -= mx[n][e] == -INFINITY ? 0.0f : mx[n][e] - kLift;
+              const float ref = mx[n][e] == -INFINITY ? 0.0f : mx[n][e];
+              y -= ref;
               p[e] = ex2(y);
               l[n][e] += p[e];
               if (kFormat == kE4M3) {
@@ -821,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) least = fminf(least, least_score[n][e] - (mx[n][e] == -INFINITY ? 0.0f : mx[n][e] - kLift));
+          for (int e = 0; e < 2; ++e) least = fminf(least, least_score[n][e] - (mx[n][e] == -INFINITY ? 0.0f : mx[n][e]));
       const bool low = kFp16 && __any_sync(0xffffffffu, least < -14.0f || top_ev > 7);
       // O^T += V^T P^T; kWide: 8-bit or 4-bit rows times their scales in bf16, with ph and pl
       auto add_values = [&](auto wide) {

@@ -143,6 +143,35 @@ def test_columns_of_small_weights_alone(drop, where):
     check(pool, q, out, float(np.float32(scale)))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale,k0", [(1.0, 4096.0), (0.125, 4.0), (1.0, -4096.0), (2.0 ** 30, 4096.0), (1e30, 2.0 ** -10), (0.0, 64.0),
+                                      (1e-37, 64.0), (2.0 ** -9, 4.0)])
+@pytest.mark.parametrize("lens", [[400], [5000, 33]])
+def test_scores_of_any_size(d, scale, k0, lens):
+    """Scores that fp32 holds exactly: each is one product, about 2^20 k0 times 1, 1.5 or 2, times the scale. So weights are
+    known to the rounding of an exponent of at most 2^-23 |score|, and where the scores differ by more than 2^9 they are 0
+    and 1."""
+    t, hq, hk = sum(lens), 2, 1
+    k = torch.zeros(t, hk, d, device="cuda")
+    k[:, :, 0] = k0 * (1 + (torch.arange(t, device="cuda") * 5 % 3)[:, None] / 2)
+    pool = fill(Pool(lens, hk, d, 16), 2, k=k.to(torch.bfloat16))
+    held = pool.held()[0]
+    q = torch.zeros(len(lens), hq, d, device="cuda")
+    q[:, :, 0] = 2.0 ** 20
+    q = q.to(torch.bfloat16)
+    out = f64(run(pool, q, scale))
+    scale = float(np.float32(scale))
+    top = abs(k0) * 2.0 ** 21.1 * scale                       # more than the largest score's size
+    assert top < 2.0 ** 14 or top / 8 > 2.0 ** 9
+    for b, n in enumerate(lens):
+        kk, vv = sequence(pool, b, held)[:, 0], sequence(pool, b, pool.held()[1])[:, 0]
+        sizes = np.unique(np.abs(kk[:, 0])) / abs(k0)         # what 4 bits make of 1, 1.5 and 2: an eighth of top apart or more
+        assert len(sizes) <= 3 and sizes[-1] < 2.1 and (np.diff(sizes) > 0.4).all()
+        ref, mag = serving.attend(f64(q[b]), kk, vv, scale, np.ones((hq, n), dtype=bool))
+        tol = U * np.abs(ref) + (W + (top * 2.0 ** -21 if top < 2.0 ** 14 else 0.0) + (n + 8) * 2.0 ** -23) * mag
+        assert (np.abs(out[b] - ref) <= tol).all()
+
+
 def test_rising_scores():
     """Each later key scores higher, so every step moves the reference."""
     n, d = 3000, 64
