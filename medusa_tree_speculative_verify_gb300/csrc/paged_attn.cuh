@@ -49,7 +49,7 @@
 namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kUnitCost = 2;     // what a unit costs beside its steps, in steps (128 sequences of up to 2000 keys: 30 us, with 1: 35)
+constexpr int kUnitMost = 2;     // the largest Layout::kUnitCost
 constexpr int kShortSteps = 16;  // steps of one warp up to which a sequence may go a unit to each warp
 constexpr unsigned int kEvenMost = 20;  // places of a piece up to which all have one length
 constexpr int kMaxCtas = 160;    // counters at the start of the workspace; CTAs of a launch
@@ -91,6 +91,9 @@ struct Layout {
   static constexpr int kKeys = 16 * kSub;                // keys of a warp's step
   static constexpr int kStepKeys = kWarps * kKeys;       // of all warps'
   // a step: for each box of the row the regions of its kSub tiles, K, then the same of V
+  // What a unit costs beside its steps, in steps (128 sequences of up to 2000 keys: 30 us, with 1: 35; e2m1, whose steps are
+  // longer, with 1 and with 2: 24 and 30)
+  static constexpr int kUnitCost = kFormat == kE2M1 ? 1 : 2;
   // steps of a warp's queue: as many as shared memory holds
   static constexpr int kStages = kFormat != kE2M1 ? 3 : kDim > 64 ? 2 : 4;
   static constexpr int kV = kBoxes * kSub * kRegion, kStage = 2 * kV;
@@ -215,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
   using Ly = Layout<kDim, kFormat, kNT>;
   constexpr bool kFp16 = kFormat != kBf16;  // products in fp16
+  constexpr int kUnitCost = Ly::kUnitCost;
   constexpr float kGrow = kFormat == kE2M1 ? 2.0f : 8.0f, kLift = kFormat == kE2M1 ? 13.0f : 0.0f;  // see e2m1 above
   constexpr float kLiftMost = 4194304.0f;  // 2^22: larger references are not lifted, a difference of 13 may round to 16 there
   extern __shared__ uint8_t smem_raw[];
@@ -1249,7 +1253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Places on the line that a sequence of all that the table holds would take, steps of `keys` keys.
 int64_t most_places(const AttnArgs& a, int keys) {
   return (int64_t)a.c.heads * a.parts *
-         (((int64_t)a.c.max_pages * a.c.page_size + keys - 1) / keys + kUnitCost + kShortSteps);
+         (((int64_t)a.c.max_pages * a.c.page_size + keys - 1) / keys + kUnitMost + kShortSteps);
 }
 
 // Clusters of `size` CTAs of the kernel that the device holds at once (found once for each device and size).
@@ -1290,8 +1294,10 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   AttnArgs a = args;
   // Sequences short enough for one warp to a unit: while there are units for every warp, up to kShortSteps of its steps (128
   // sequences of 160 keys, 8 kv heads: 15 us, cut across warps 28; of half as many steps at most, 128 of up to 300 keys take
-  // 16 in place of 20, but those of 160 keys 28)
-  a.short_keys = std::min(kShortSteps, 2 * (a.c.n_seq * units / grid)) * Ly::kKeys;
+  // 16 in place of 20, but those of 160 keys 28). e2m1, with more work for the same bytes: three quarters of that where units
+  // are few (128 sequences of up to 2000 keys: 24 us; with all 36, with half 25)
+  const int even = a.c.n_seq * units / grid;
+  a.short_keys = std::min(kShortSteps, kFormat == kE2M1 ? 3 * even / 2 : 2 * even) * Ly::kKeys;
   const int page16 = a.c.page_size / 16;
   a.box_tiles = page16 % Ly::kSub == 0 ? Ly::kSub : Ly::kSub == 4 && page16 % 2 == 0 ? 2 : 1;
   a.groups_log2 = Ly::kSub / a.box_tiles == 4 ? 2 : Ly::kSub / a.box_tiles == 2 ? 1 : 0;
