@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads) paged_resize_kernel(const ResizeArgs
   pdl_trigger();
   pdl_wait();
   const int held = __ldcg(a.free);
-  bool bad = held < 0 || held > a.n_pages;
+  bool bad = false;
   // Sums stop at kMost, so that none is taken for a small one.
   auto add = [](uint32_t x, uint32_t y) { return min(x + y, kMost); };
   uint32_t carry[3] = {0, 0, 0};
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads) paged_resize_kernel(const ResizeArgs
     }
     __syncthreads();
   }
-  const bool over = carry[0] > (a.positions || a.slots ? (uint32_t)a.n_rows : kMost) || max(carry[0], max(carry[1], carry[2])) == kMost ||
+  const bool over = held < 0 || carry[0] > (a.positions || a.slots ? (uint32_t)a.n_rows : kMost) || max(carry[0], max(carry[1], carry[2])) == kMost ||
                     (int64_t)held + carry[2] > a.n_pages || carry[1] > (int64_t)held + carry[2];
   if (over && rank == 0 && tid == 0) mv_set_error_detail(a.err, kPagedResizeSite, MV_DEVERR_INDEX, (uint32_t)n);
   bad = __syncthreads_or(bad || over);

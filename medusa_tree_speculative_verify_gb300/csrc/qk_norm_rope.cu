@@ -86,17 +86,6 @@ __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const
   const int h_to = min(h_from + a.span[is_k], heads);
   const int64_t t_first = (int64_t)block << log2, t = t_first + group / per_token;
   const bool real = t < a.n_tokens;
-  uint4 g0 = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), g1 = g0;
-  const uint16_t* gain = is_k ? a.k_gain : a.q_gain;
-  if (gain && mine) {
-    g0 = *reinterpret_cast<const uint4*>(gain + e0);
-    g1 = *reinterpret_cast<const uint4*>(gain + e1);
-  }
-  uint64_t turns[8];
-  if (rot) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turns[i] = __ldg(a.turns + 8 * j + i);
-  }
   pdl_trigger();
   pdl_wait();
   if (t_first >= a.n_tokens) return;  // the whole warp
@@ -118,6 +107,17 @@ __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) ask(i);
+  uint4 g0 = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), g1 = g0;
+  const uint16_t* gain = is_k ? a.k_gain : a.q_gain;
+  if (gain && mine) {
+    g0 = *reinterpret_cast<const uint4*>(gain + e0);  // from L1 but for the first: 27 us in place of 77 for 8192 tokens
+    g1 = *reinterpret_cast<const uint4*>(gain + e1);
+  }
+  uint64_t turns[8];
+  if (rot) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turns[i] = a.turns[8 * j + i];
+  }
   // The first piece's elements times `a0`, plus the other element of their pairs times `b0`; the second piece's `a1`, `b1`.
   // Pairs of halves: the other piece's element of the same place. Neighbours: the one beside it.
   uint64_t a0[4], a1[4], b0[4] = {}, b1[4] = {};

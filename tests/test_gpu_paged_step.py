@@ -149,6 +149,7 @@ def test_resize_outputs_that_are_not_wanted(what):
     ([10, 20], [2 ** 31 - 1, 5], None), ([10, 20], [-2 ** 31, 5], None),
     ([10, 20], [60, 60], 5),                                   # pages do not suffice
     ([10, 20], [1, 1], -1), ([10, 20], [1, 1], 41),            # a stack of no such size
+    ([100, 20], [-60, 0], -1), ([100, 20], [-60, 0], 41), ([100, 20], [0, 0], -2 ** 31), ([100, 20], [0, 0], 2 ** 31 - 1),
     ([100, 20], [-100, 1], 38)])                               # more pages than there are
 def test_resize_refused_on_the_device(lens, by, free, rows):
     """Nothing changes, no rows come, the error word says so; the next call is done as ever."""
