@@ -63,7 +63,8 @@ struct AttnArgs {
   PagedArgs c;
   RowsArgs q, out;
   int group, parts;  // query heads of a kv head, units of a kv head
-  int cluster;       // CTAs of a cluster
+  int cluster_log2;  // CTAs of a cluster: 2^cluster_log2
+  unsigned int grid_inv;  // 2^32 / CTAs, rounded down: divisions by their number without one
   int short_keys;    // sequences of at most so many keys go a unit to each warp
   int box_tiles;     // 16-key tiles of a copy: 1, 2 or 4, never over a page's end
   // divisions by a page's 16-key tiles, done once on the host: of a tile number n by n * page_inv >> 36; pages and tiles in
@@ -306,11 +307,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   // sooner, and units would have more parts (12 sequences of up to 38 k keys, 16 heads of one kv head: 17 us, spread 21; 4 of
   // 2000, 8 kv heads: 12 and 14.5). Long pieces are spread, the first `rest` of them one longer: there the last few SMs count
   // for their bandwidth (64 sequences of up to 8191 keys, 33 places a piece: 38.7 us, of one length 39.9).
-  const unsigned int all = (unsigned)total, least = (all + gridDim.x - 1) / gridDim.x;
+  const unsigned int all = (unsigned)total;
+  unsigned int share = __umulhi(all, a.grid_inv), over = all - share * gridDim.x;  // all / gridDim.x, or one less, and the rest
+  if (over >= gridDim.x) {
+    ++share;
+    over -= gridDim.x;
+  }
+  const unsigned int least = share + (over ? 1 : 0);
   const bool even = least <= kEvenMost;
-  const int each = kCluster ? 1 : max(1, (int)(even ? least : all / gridDim.x)), rest = even ? 0 : total - each * (int)gridDim.x;
-  const int ctas = kCluster ? 1 : even ? (int)((all + each - 1) / (unsigned)each) : (int)gridDim.x, cta = blockIdx.x;
-  if (!kCluster && cta >= ctas) return;
+  const int each = kCluster ? 1 : max(1, (int)(even ? least : share)), rest = even ? 0 : (int)over, cta = blockIdx.x;
+  if (!kCluster && even && (unsigned)cta * (unsigned)each >= all) return;
   auto piece = [&](int c) { return (int)min((unsigned)c * (unsigned)each + min(c, rest), all); };
   const int s_first = kCluster ? 0 : piece(cta);
   int s_end = kCluster ? 0 : piece(cta + 1);
@@ -338,20 +344,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   Place ahead;
   int s_begin;  // the first step at or after s_first that this CTA does
-  const int c_rank = kCluster ? (int)cluster_rank() : 0, c_size = kCluster ? a.cluster : 1;
+  const int c_rank = kCluster ? (int)cluster_rank() : 0, c_size = kCluster ? 1 << a.cluster_log2 : 1;
   if (kCluster) {  // an equal share of the unit's steps, possibly none; places counted from 0
     enter(ahead, 0);
-    ahead.idx = cta / c_size;
-    ahead.step = (int)((int64_t)ahead.n * c_rank / c_size);
+    ahead.idx = cta >> a.cluster_log2;
+    ahead.step = (int)((int64_t)ahead.n * c_rank >> a.cluster_log2);
     s_begin = 0;
-    s_end = (int)((int64_t)ahead.n * (c_rank + 1) / c_size) - ahead.step;
+    s_end = (int)((int64_t)ahead.n * (c_rank + 1) >> a.cluster_log2) - ahead.step;
   } else {
-    int lo = 0, hi = n_seq;  // the last b with pre[b] <= s_first: one with places
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_pre[mid] <= s_first) lo = mid;
-      else hi = mid;
-    }
+    // the last b with pre[b] <= s_first: one with places. A 32nd of the sequences at a time, then one (kChunkSeq = 32 x 32)
+    const int part = (n_seq + 31) >> 5;
+    auto last = [&](int first, int step, int n) {  // of lanes' first + lane * step, those of lanes below n
+      const int b = first + lane * step;
+      return 31 - __clz(__ballot_sync(0xffffffffu, lane < n && b < n_seq && s_pre[min(b, n_seq)] <= s_first));
+    };
+    int lo = last(0, part, 32) * part;
+    if (part > 1) lo += last(lo, 1, part);
     enter(ahead, lo);
     const int in_b = s_first - s_pre[lo], width = kUnitCost + ahead.n;
     ahead.idx = (unsigned)in_b / (unsigned)width;
@@ -366,6 +374,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!kCluster && s_begin >= s_end) return;
   Place here = ahead;
   auto head_of = [&](int unit) { return a.parts == 1 ? unit : (int)((unsigned)unit / (unsigned)a.parts); };
+
+  // the words of Q of a unit: head g of each tile of 8, the pieces as of K
+  uint32_t q_raw[kNT][kDim / 8];
+  auto load_q = [&](const Place& p) {
+    constexpr int kPieces = Ly::kRow < 64 ? 1 : Ly::kRow / 64, kWords = kDim / 8 / kPieces;  // words of Q for a piece of K
+    const int unit = p.one ? p.idx * kWarps + warp : p.idx, kh = head_of(unit);
+    const int head0 = kh * a.group + (unit - kh * a.parts) * Ly::kHeads;
+    const int n_heads = unit < units ? min(Ly::kHeads, (kh + 1) * a.group - head0) : 0;
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      const int h = 8 * n + g;
+      const uint16_t* row = a.q.p + (int64_t)p.b * a.q.ts + (int64_t)(h < n_heads ? head0 + h : 0) * a.q.hs;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int d = 2 * kWords * (t + 4 * i);
+#pragma unroll
+        for (int j = 0; j < kWords; j += 4) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (h < n_heads && d + 2 * j < a.c.dim) v = *reinterpret_cast<const uint4*>(row + d + 2 * j);
+          q_raw[n][i * kWords + j] = v.x;
+          q_raw[n][i * kWords + j + 1] = v.y;
+          q_raw[n][i * kWords + j + 2] = v.z;
+          q_raw[n][i * kWords + j + 3] = v.w;
+        }
+      }
+    }
+  };
+  load_q(here);  // on its way while the table is looked up
 
   // ---- this warp's queue. A lane is there for one of a step's copies (its tiles from my_u on, a box of K or V; from lane
   // 16 on: the exponents of one tile's K or V). Page and tile in it are carried along: a step is kWarps * kSub tiles after
@@ -518,37 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ks_off = g * per_row + (kDim > 64 ? 2 * t : t), vs_off = Ly::kExps / 2 + 2 * t * per_row + (kDim > 64 ? g : g >> 1);
   const bool ks_any = kWhole || (kDim > 64 ? 2 * t : t) < per_row, vs_any = kWhole || (kDim > 64 ? g : g >> 1) < per_row;
 
-  // the words of Q of a unit: head g of each tile of 8, the pieces as of K
-  uint32_t q_raw[kNT][kDim / 8];
-  auto load_q = [&](const Place& p) {
-    constexpr int kPieces = Ly::kRow < 64 ? 1 : Ly::kRow / 64, kWords = kDim / 8 / kPieces;  // words of Q for a piece of K
-    const int unit = p.one ? p.idx * kWarps + warp : p.idx, kh = head_of(unit);
-    const int head0 = kh * a.group + (unit - kh * a.parts) * Ly::kHeads;
-    const int n_heads = unit < units ? min(Ly::kHeads, (kh + 1) * a.group - head0) : 0;
-#pragma unroll
-    for (int n = 0; n < kNT; ++n) {
-      const int h = 8 * n + g;
-      const uint16_t* row = a.q.p + (int64_t)p.b * a.q.ts + (int64_t)(h < n_heads ? head0 + h : 0) * a.q.hs;
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        const int d = 2 * kWords * (t + 4 * i);
-#pragma unroll
-        for (int j = 0; j < kWords; j += 4) {
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (h < n_heads && d + 2 * j < a.c.dim) v = *reinterpret_cast<const uint4*>(row + d + 2 * j);
-          q_raw[n][i * kWords + j] = v.x;
-          q_raw[n][i * kWords + j + 1] = v.y;
-          q_raw[n][i * kWords + j + 2] = v.z;
-          q_raw[n][i * kWords + j + 3] = v.w;
-        }
-      }
-    }
-  };
-
   // ---- unit after unit
   int s = s_begin, slot = 0, phase = 0;
   bool once = kCluster;  // a CTA of a cluster puts its results together even where it has no step
-  load_q(here);
   while (s < s_end || once) {
     once = false;
     const int b = here.b, len = here.len, nb = here.n, step0 = here.step;
@@ -1136,7 +1144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- units over several CTAs: the last one to come joins the partial results in the order of the line
   __syncthreads();
   auto cta_of = [&](int place) {  // the CTA whose piece holds a place: guessed, and put right
-    int c = min(ctas - 1, (int)((unsigned)place / (unsigned)each));
+    int c = min((int)gridDim.x - 1, (int)((unsigned)place / (unsigned)each));
     while (piece(c) > place) --c;
     return c;
   };
@@ -1298,6 +1306,8 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
   // are few (128 sequences of up to 2000 keys: 24 us; with all 36, with half 25)
   const int even = a.c.n_seq * units / grid;
   a.short_keys = std::min(kShortSteps, kFormat == kE2M1 ? 3 * even / 2 : 2 * even) * Ly::kKeys;
+  a.cluster_log2 = 0;
+  a.grid_inv = grid > 1 ? (unsigned int)((uint64_t(1) << 32) / grid) : 0xffffffffu;
   const int page16 = a.c.page_size / 16;
   a.box_tiles = page16 % Ly::kSub == 0 ? Ly::kSub : Ly::kSub == 4 && page16 % 2 == 0 ? 2 : 1;
   a.groups_log2 = Ly::kSub / a.box_tiles == 4 ? 2 : Ly::kSub / a.box_tiles == 2 ? 1 : 0;
@@ -1330,7 +1340,7 @@ mv_status launch(const AttnArgs& args, cudaStream_t stream) {
         c_wide[dev] = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess ? 1 : -1;
       if (size > 8 && c_wide[dev] < 0) cudaGetLastError();
       if ((size <= 8 || c_wide[dev] > 0) && most_clusters<kDim, kFormat, kNT, kWhole>(size, Ly::bytes(1)) >= units) {
-        a.cluster = size;
+        a.cluster_log2 = size == 16 ? 4 : size == 8 ? 3 : size == 4 ? 2 : size == 2 ? 1 : 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(units * size);
         cfg.blockDim = dim3(kThreads);
