@@ -7,9 +7,9 @@
 //
 // Bound by latency: lengths, sums, then one dependent load for each page or row. A cluster of CTAs, each of which does the
 // sums for itself, moves the pages; all have read the lengths before the first of them writes (the cluster's barrier). One
-// CTA would take 41 us for 200 prompts of up to 8192 tokens let in and out in place of 15.5. More than kRowsHere rows go to a
-// second kernel over the whole GPU, which looks them up in what the first one wrote (19200 rows: 10.8 us there and back, 13.0
-// without).
+// CTA took 41 us for 200 prompts of up to 8192 tokens let in and out where eight took 15.5; with four pages of a thread at once
+// they take 12.1. More than kRowsHere rows go to a second kernel over the whole GPU, which looks them up in what the first one
+// wrote (19200 rows: 10.8 us there and back, 13.0 without).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -44,6 +44,22 @@ MV_DEV int find(const int* sums, int n, int i) {
   }
   return lo;
 }
+
+// The same for kAtOnce of them, whose steps do not wait for each other. top: the largest power of two below n, or 0.
+template <int kAtOnce>
+MV_DEV void find(const int* sums, int n, int top, const int (&i)[kAtOnce], int (&b)[kAtOnce]) {
+#pragma unroll
+  for (int k = 0; k < kAtOnce; ++k) b[k] = 0;
+  for (int step = top; step; step >>= 1)
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int next = b[k] + step;
+      if (next < n && sums[next] <= i[k]) b[k] = next;
+    }
+}
+
+MV_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+MV_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) paged_resize_kernel(const ResizeArgs a) {
@@ -94,10 +110,22 @@ __global__ void __launch_bounds__(kThreads) paged_resize_kernel(const ResizeArgs
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       uint32_t before = carry[k], all = carry[k];
-      for (int w = 0; w < used; ++w) {
-        const uint32_t one = s_scan[k][w];
-        if (w < warp) before = add(before, one);
-        all = add(all, one);
+      if (used <= 4) {  // one after the other, soonest for few
+        for (int w = 0; w < used; ++w) {
+          const uint32_t one = s_scan[k][w];
+          if (w < warp) before = add(before, one);
+          all = add(all, one);
+        }
+      } else {
+        uint32_t to = lane < used ? s_scan[k][lane] : 0u;  // of the warps up to `lane`
+#pragma unroll
+        for (int o = 1; o < kWarps; o <<= 1) {
+          const uint32_t up = __shfl_up_sync(0xffffffffu, to, o);
+          if (lane >= o) to = add(to, up);
+        }
+        const uint32_t one = __shfl_sync(0xffffffffu, to, max(warp - 1, 0));
+        if (warp) before = add(before, one);
+        all = add(all, __shfl_sync(0xffffffffu, to, kWarps - 1));
       }
       if (b < n) s_all[k * (n + 1) + b] = (int)(add(before, incl[k]) - x[k]);  // where nothing stopped at kMost
       carry[k] = all;
@@ -121,22 +149,43 @@ __global__ void __launch_bounds__(kThreads) paged_resize_kernel(const ResizeArgs
   __syncthreads();
 
   auto pages_of = [&](int len) { return (int)((unsigned)(len + a.page_size - 1) / (unsigned)a.page_size); };
-  auto given = [&](int i) {  // page i of those given up
-    const int b = find(s_give, n, i), left = pages_of(s_len[b]) - (s_give[b + 1] - s_give[b]);
+  auto given = [&](int i, int b) {  // page i of those given up, which is sequence b's
+    const int left = pages_of(s_len[b]) - (s_give[b + 1] - s_give[b]);
     return __ldcg(a.table + (int64_t)b * a.ld_table + left + i - s_give[b]);
   };
-  auto taken = [&](int j) { return j < give ? given(j) : __ldcg(a.free + 1 + (held + give - 1 - j)); };
-  const int step = kThreads * (int)gridDim.x, first = rank * kThreads + tid;
+  auto taken = [&](int j) { return j < give ? given(j, find(s_give, n, j)) : __ldcg(a.free + 1 + (held + give - 1 - j)); };
+  cluster_arrive();  // this CTA has read what is overwritten at the end
+  constexpr int kAtOnce = 4;
+  const int step = kThreads * (int)gridDim.x, first = rank * kThreads + tid, top = n > 1 ? 1 << (31 - __clz(n - 1)) : 0;
   bool odd = false;  // a page outside the pool
-  for (int i = first; i < give; i += step) {
-    const int page = given(i);
-    odd |= page < 0 || page >= a.n_pages;
-    a.free[1 + (held + give - 1 - i)] = page;  // at or over `held`: nothing here reads that
+  for (int64_t i0 = first; i0 < give; i0 += kAtOnce * step) {
+    int i[kAtOnce], b[kAtOnce], page[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) i[k] = (int)min(i0 + k * step, (int64_t)give - 1);
+    find(s_give, n, top, i, b);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) page[k] = given(i[k], b[k]);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (i0 + k * step >= give) break;
+      odd |= page[k] < 0 || page[k] >= a.n_pages;
+      a.free[1 + (held + give - 1 - i[k])] = page[k];  // at or over `held`: nothing here reads that
+    }
   }
-  for (int j = first; j < take; j += step) {
-    const int page = taken(j), b = find(s_take, n, j);
-    odd |= page < 0 || page >= a.n_pages;
-    a.table[(int64_t)b * a.ld_table + pages_of(s_len[b]) + j - s_take[b]] = page;
+  for (int64_t j0 = first; j0 < take; j0 += kAtOnce * step) {
+    int j[kAtOnce], b[kAtOnce], page[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      j[k] = (int)min(j0 + k * step, (int64_t)take - 1);
+      page[k] = taken(j[k]);
+    }
+    find(s_take, n, top, j, b);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (j0 + k * step >= take) break;
+      odd |= page[k] < 0 || page[k] >= a.n_pages;
+      a.table[(int64_t)b[k] * a.ld_table + pages_of(s_len[b[k]]) + j[k] - s_take[b[k]]] = page[k];
+    }
   }
   if (odd) mv_set_error_detail(a.err, kPagedResizeSite, MV_DEVERR_INDEX, (uint32_t)n + 1);
   if (a.rows_here)
@@ -155,7 +204,8 @@ __global__ void __launch_bounds__(kThreads) paged_resize_kernel(const ResizeArgs
       if (a.positions) a.positions[i] = pos;
       if (a.slots) a.slots[i] = slot;
     }
-  cluster_sync_all();  // all have read what is overwritten now
+  __syncwarp();
+  cluster_wait();
   if (rank != 0) return;
   if (a.cu)
     for (int b = tid; b <= n; b += kThreads) a.cu[b] = bad ? 0 : s_rows[b];
@@ -249,8 +299,8 @@ extern "C" mv_status paged_kv_resize(const int32_t* by, int32_t n_seq, int32_t p
   a.rows_here = a.n_rows <= kRowsHere;
   a.err = mv_error_word();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // Few sequences have few pages, and fewer warps meet sooner: 48 growing by a token and back 5.7 us, of 512 threads 6.4; 200
-  // prompts let in and out 17.9 and 15.5.
+  // Few sequences have few pages, and fewer warps meet sooner: 48 growing by a token and back 5.7 us, with 512 threads 6.4; 200
+  // prompts let in and out 17.9 and 15.5 (before four pages went at once).
   const mv_status s = n_seq <= 64 ? launch_resize<256>(a, st) : launch_resize<512>(a, st);
   if (s != MV_OK) return s;
   if (!a.rows_here) {
