@@ -542,7 +542,8 @@ mv_status paged_kv_read(const mv_paged_kv* cache, const int32_t* block_table, in
  * not matter, NaN included; an infinity or a NaN in a value row that is attended to makes that element of out one of the two.
  * q, out device bf16 rows, token b = sequence b; out must not overlap q or the cache. Scores, softmax statistics and
  * output sums in fp32. The weights have 16 bits for the product with v, over e4m3 pools 11 where fp16's normal range holds
- * all of a step's (16 to 64 keys) times their rows' scales. The result does not depend on the order in which the parts of
+ * all of a step's (16 to 64 keys) times their rows' scales, over e2m1 pools 11 where all of a step's (64 keys) are at least
+ * 2^-27 of the largest so far. The result does not depend on the order in which the parts of
  * a split sequence finish. scale >= 0 and log2(e) * scale finite, here and in prompt_attention.
  * Limits: n_heads % n_kv_heads == 0, n_heads <= 256; units * (max_pages * page_size / 128 + 19) < 2^31 with units =
  * n_kv_heads * ceil(n_heads / n_kv_heads / 16). workspace: device memory of paged_attention_workspace() bytes,

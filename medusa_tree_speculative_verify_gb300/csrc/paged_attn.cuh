@@ -1,4 +1,5 @@
-// Attention of one new token for each sequence over a paged cache (bf16, or e4m3 with an exponent for each row).
+// Attention of one new token for each sequence over a paged cache (bf16, e4m3 with an exponent for each row, or e2m1 with a
+// scale for each group of 16 elements).
 //
 // Bound by the cache's bytes: every row is read once for up to 16 query heads of a kv head (once for each 16 of more). What
 // they share is read for all of them together, 8 (or 16) heads a work unit, on the tensor cores with the keys as the rows of the products (mma.sync
@@ -29,7 +30,14 @@
 // e2m1: K and V convert exactly to fp16 and are multiplied there with their groups' scales, exactly (6 significant bits, at
 // most 61440). Q as for e4m3. Weights go into one product in fp16, 2^13 times as large: the reference follows the largest
 // within 2^2, so they fill fp16's range from 2^15 down, and those of 2^-27 and more of the largest keep 11 bits. A step
-// with smaller ones is done as for bf16 (V to bf16, exactly).
+// with smaller ones is done as for bf16 (V to bf16, exactly): 16 x 24576 keys of 64/8 heads 90 us, with all steps so 115.
+// V's rows 2 t and 2 t + 1 are interleaved while they are 4-bit values, so that one conversion gives both elements of an
+// operand. Bound by these conversions, not by the copies: for 16 keys of 128 dims 64 of them (2 cycles each on the ALU), 64
+// products with scales (2 cycles of the FMA pipe) and 16 tensor products (8 cycles each, which keep the FMA pipe too): 306
+// cycles of a scheduler by themselves, 485 with everything else, where HBM's rate would leave 436.
+// Copies here are by all lanes (cp.async), 16 bytes each, as 16 rows are 1 KB in one piece: a fifth of the instructions of one
+// TMA box after the other with its scales (111 -> 91 us with the masks that only the last step needs; 64 ragged sequences over
+// pages of 16 keys 43 -> 32). 12 or 16 warps with steps of half as many keys: 98 and 99 us.
 //
 // Split. The work is a line of steps, kWarps tiles of keys each, over all units (sequence, kv head, 8 or 16 of its
 // heads); every CTA takes an equal piece of the line, whatever the lengths are. A unit's start and end (its Q, putting the

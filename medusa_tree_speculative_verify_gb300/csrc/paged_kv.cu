@@ -10,9 +10,12 @@
 // 8, so x / s is a border or at least 2^-8 of itself from one. x times the rounded 1 / s, rounded to a multiple of 2^-11 by
 // adding 6144 and taking it off again, is a border just where x / s is one, and on the same side of it elsewhere.
 //
-// Bound by memory: 2 * dim bytes read (written) and dim + 1 or 2 * dim written (read) for each row, K and V. A CTA takes up
-// to 64 consecutive tokens, all heads, K and V: their places are looked up once, by 16 to 4 lanes a token; what a
-// thread computes of an address serves a row of K and one of V.
+// Bound by memory: 2 * dim bytes read (written) and dim + 1, 9 / 16 * dim or 2 * dim written (read) for each row, K and V. A
+// CTA takes up to 64 consecutive tokens, all heads, K and V: their places are looked up once, in shared memory where all
+// sequences fit there (8294 e4m3 tokens x 8 heads written and read back 26.6 -> 20.1 us, 38 k read 40.7 -> 37.6), else by 16
+// to 4 lanes a token; what a thread computes of an address serves a row of K and one of V. 4-bit rows: a thread has two pairs
+// of rows on their way when it writes, four when it reads (8294 tokens written and read back 19.2 us, one pair and lookups
+// as for many sequences 28.4).
 #include <algorithm>
 
 #include "kernels.cuh"
