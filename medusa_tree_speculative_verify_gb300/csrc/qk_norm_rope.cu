@@ -11,7 +11,7 @@
 // several), a group of lanes to a head: side by side in memory and then the next ones. A lane has 16 elements of a head as two pieces of 16 bytes, chosen
 // so that pairs meet in it; what is left to exchange
 // is the sum of squares. What a lane's elements are multiplied with but for the row's own factor, cosines and sines times
-// gains, it computes once for all its heads. Sine and cosine are the special-function unit's (within 2^-21.4, below the
+// gains, it computes once for all its heads. Sine and cosine are the special-function unit's (within 2^-21.1, below the
 // 2^-9 of the result's rounding); the angle is within half a turn of zero there.
 #include <algorithm>
 

@@ -5,7 +5,7 @@ Tolerances. Whole numbers and what a cache holds are compared exactly. A rotated
   2^-8 |ref|     its rounding to bf16 (half a step),
   40 2^-24 size  with size the length of its pair: fp32 sums of at most 256 squares in 16 + 4 steps (under a root: 10 units of
                  2^-24), the reciprocal root (2), products with it and the gain (3), the angle (rounded to 2^-24 of at most
-                 pi, and its factor: 7), its sine and cosine within 2^-21.4 each (6 each), two products and a sum (3), rounded up.
+                 pi, and its factor: 7), its sine and cosine within 2^-21.1 (7 each), two products and a sum (3), rounded up.
 """
 import numpy as np
 import pytest
@@ -526,3 +526,43 @@ def test_rows_of_a_bad_page_are_left_out():
     want = paged_step.stored_value(paged_step.pack(code), byte)
     want[16:32] = 7.0
     assert np.array_equal(f64(ko), want)
+
+
+# ------------------------------------------------------------------------------------------------ what the binding refuses
+
+def test_refusals_with_tensors():
+    """Wrong types, sizes, layouts and tensors of the host: an error before anything is launched, and nothing is written."""
+    b = Batch([5, 40], 16, 40, 10)
+    by, (cu, pos, slots) = i32([1, 1]), b.outputs(8)
+    call = lambda by=by, table=b.d_table, lens=b.d_lens, free=b.d_free, cu=cu, pos=pos, slots=slots, **kw: \
+        mv.paged_kv_resize(by, b.cache, table, lens, free, cu, pos, slots, **kw)
+    for kw in (dict(by=by.long()), dict(by=i32([1, 1, 1])), dict(by=by.cpu()), dict(table=b.d_table.long()), dict(table=b.d_table[0]),
+               dict(table=b.d_table.t()), dict(lens=b.d_lens[:1]), dict(free=b.d_free[:-1]), dict(cu=cu[:2]), dict(cu=None), dict(pos=pos[::2]),
+               dict(pos=pos.long()), dict(slots=slots.int()), dict(slots=slots[:7]), dict(slots=slots[None]), dict(by=[1, 1])):
+        with pytest.raises((ValueError, TypeError)):
+            call(**kw)
+    b.check_state()
+    assert (cu == 77).all() and (pos == 77).all() and (slots == 77).all()
+
+    q, k, gain, at, rope = normal(1, 4, 3, 64), normal(2, 4, 2, 64), normal(3, 64), i32(range(4)), mv.Rope(64)
+    out = torch.full_like(q, 7.0)
+    turn = lambda q=q, k=k, qg=gain, kg=gain, at=at, rope=rope, qo=out, ko=None, eps=1e-6: \
+        mv.qk_norm_rope(q, k, qg, kg, eps, at, rope, qo, ko)
+    for kw in (dict(q=q.float()), dict(q=q[0]), dict(q=q.cpu()), dict(k=normal(2, 5, 2, 64)), dict(k=normal(2, 4, 2, 32)),
+               dict(q=normal(1, 4, 3, 128)[..., ::2]), dict(qg=gain.float()), dict(kg=gain[:32]), dict(at=at.long()), dict(at=at[:3]), dict(at=None),
+               dict(qo=out[:, :2]), dict(q=None), dict(rope=mv.Rope(64, device="cpu"))):
+        with pytest.raises((ValueError, TypeError)):
+            turn(**kw)
+    for kw in (dict(rope=mv.Rope(128)), dict(eps=-1.0), dict(q=normal(1, 4, 3, 72)[..., 4:68].contiguous()[:, :, :56], k=None, kg=None, qg=None)):
+        with pytest.raises((ValueError, mv.MVError)):
+            turn(**kw)
+    assert (out == 7.0).all()
+
+    pages = torch.zeros(4, 2, 16, 32, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(4, 2, 16, 4, dtype=torch.uint8, device="cuda")
+    mv.PagedKV(pages, pages.clone(), scales, scales.clone())
+    for args in ((pages, pages, None, None), (pages, pages, scales, None), (pages, pages, scales[..., :3], scales[..., :3]),
+                 (pages, pages, scales[..., 0].contiguous(), scales[..., 0].contiguous()), (pages, pages.to(torch.int8), scales, scales),
+                 (pages.transpose(1, 2), pages.transpose(1, 2), scales, scales), (pages, pages, scales.int(), scales.int())):
+        with pytest.raises(ValueError):
+            mv.PagedKV(*args)
