@@ -168,10 +168,13 @@ __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const
     for (int o = kLanes >> 1; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     ask(slot);
     slot = slot + 1 == kAhead ? 0 : slot + 1;
+    // first of all by the row's factor: |x| times it is sqrt(D) at most, while x times a gain may leave fp32's range
     const float by = rsqrtf(sum * inv + a.eps);
     uint64_t y0[4], y1[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      u[e] = mul2(u[e], pack2(by, by));
+      v[e] = mul2(v[e], pack2(by, by));
       y0[e] = mul2(u[e], a0[e]);
       y1[e] = mul2(v[e], a1[e]);
     }
@@ -182,11 +185,6 @@ __global__ void __launch_bounds__(kThreads, kResident) qk_norm_rope_kernel(const
         y0[e] = fma2(kNeighbours ? pack2(p.y, p.x) : v[e], b0[e], y0[e]);
         y1[e] = fma2(kNeighbours ? pack2(r.y, r.x) : u[e], b1[e], y1[e]);
       }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      y0[e] = mul2(y0[e], pack2(by, by));
-      y1[e] = mul2(y1[e], pack2(by, by));
-    }
     if (mine && h0 + group % per_token < h_to && pos >= 0) {
       *reinterpret_cast<uint4*>(dst + e0) = pack8(y0);
       *reinterpret_cast<uint4*>(dst + e1) = pack8(y1);

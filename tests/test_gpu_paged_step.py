@@ -323,6 +323,19 @@ def test_rope_eps_and_small_rows(eps):
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("by,gain_by,eps", [(57, 100, 1e-6), (57, -100, 0.0), (0, 120, 1e-6), (-55, -100, 0.0), (-55, 100, 0.0)])
+@pytest.mark.parametrize("d,rot,neighbours", [(64, 64, False), (128, 64, True), (32, 0, False)])
+def test_rope_of_any_size(by, gain_by, eps, d, rot, neighbours):
+    """Rows and gains times powers of two, the results within bf16's range: the bound is the one of the gains without theirs.
+    (What a product of a gain and a sine loses below 2^-126 is 2^-150, 2^-50 of a row's size.)"""
+    rope = mv.Rope(rot, neighbours=neighbours) if rot else None
+    pos, gain = np.arange(30), 1 + normal(3, d, std=0.3)
+    for h, x in ((3, normal(4, 30, 3, d) * 2.0 ** by), (1, normal(5, 30, 1, d) * 2.0 ** by)):
+        out = torch.full_like(x, 7.0)
+        mv.qk_norm_rope(x, None, gain * 2.0 ** gain_by, None, eps, i32(pos), rope, out)
+        check_rope(out.double() * 2.0 ** -gain_by, x, gain, eps, pos, rope)
+
+
 @pytest.mark.parametrize("order", ["fused", "planes", "in_place_fused"])
 def test_rope_strides(order):
     """Slices of a fused projection, [heads][tokens][D] planes, and a slice in place: what lies between stays."""
