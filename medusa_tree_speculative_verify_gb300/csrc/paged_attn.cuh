@@ -795,7 +795,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < Ly::kSub; ++u)
 #pragma unroll
             for (int r = 0; r < 2; ++r) tx[n][e] = fmaxf(tx[n][e], x[n][u][2 * r + e]);
-          grow |= tx[n][e] > mx[n][e] + (kGrow + kLift);
+          // the difference that the exponent is: over 2^24 the reference plus this may round to more than it stands for, and a
+          // weight of 2^16 is none in fp16 (-inf - -inf is no number, and not greater)
+          grow |= tx[n][e] - mx[n][e] > kGrow + kLift;
         }
       if (__any_sync(0xffffffffu, grow)) {
         float shift = 1.0f;
