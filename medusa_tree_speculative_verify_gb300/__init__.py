@@ -13,7 +13,7 @@ import os
 
 import numpy as np
 
-from .build import LIB, build
+from .build import LIB, build, build_calls, build_library
 
 __all__ = ["lib", "MVError", "Tree", "AcceptParams", "PosteriorResult", "GREEDY", "TYPICAL", "Model", "Session",
            "RootParams", "ROOT_ARGMAX", "ROOT_TYPICAL", "ROOT_NUCLEUS", "sample_root",
@@ -156,7 +156,7 @@ def lib(auto_build: bool = True):
     global _lib
     if _lib is None:
         if auto_build:
-            build()
+            build_library()
         if not os.path.exists(LIB):
             raise RuntimeError(f"{LIB} is missing: build it with medusa_tree_speculative_verify_gb300.build.build()")
         L = ctypes.CDLL(LIB)
@@ -397,11 +397,12 @@ _compiled = None    # the compiled part of the binding: checks of tensors, and t
 
 
 def _load_calls():
-    """The compiled calls, loaded by the first call that takes tensors."""
+    """The compiled calls, loaded by the first call that takes tensors (built first if missing or stale)."""
     global _compiled
     if _compiled is None:
         import torch  # noqa: F401  (whose libraries the module is linked against)
         lib()
+        build_calls()
         from . import _calls
         _compiled = _calls
     return _compiled

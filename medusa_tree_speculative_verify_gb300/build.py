@@ -2,9 +2,10 @@
 
 Each .cu under csrc/ is compiled in parallel into _build/, then linked into
 medusa_tree_speculative_verify_gb300/libmedusa_verify.so against the shared
-CUDA runtime. Beside it _calls.so, the compiled part of the Python binding, is
-made from csrc/calls.cpp with the host compiler and torch's headers. A rebuild
-happens only when a source or header is newer than either (or when forced).
+CUDA runtime; that takes nvcc alone. Beside it _calls.so, the compiled part of
+the Python binding, is made from csrc/calls.cpp with the host compiler and
+torch's headers, where torch is installed. Each is rebuilt only when one of its
+own sources or headers is newer (or when forced).
 """
 from __future__ import annotations
 
@@ -62,18 +63,37 @@ def calls_commands(obj: str, out: str):
              "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"])
 
 
+def _older(path: str, deps) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
+
+
+def _headers():
+    return [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)]
+
+
+def _library_stale() -> bool:
+    return _older(LIB, sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + _headers())
+
+
+def _calls_stale() -> bool:
+    return _older(CALLS, [CALLS_SRC] + _headers())
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    deps = [CALLS_SRC] + sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    deps += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [os.path.abspath(__file__)]
-    return any(os.path.getmtime(p) > t for p in deps)
+    return _library_stale() or _calls_stale()
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+def _run(cmd, what: str, verbose: bool = False) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(f"== {what}\n{r.stdout}{r.stderr}")
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed")
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link the library if needed; returns its path."""
-    if not force and not _stale():
+    if not force and not _library_stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -85,29 +105,51 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    calls_obj, calls_tmp = os.path.join(BUILD, "calls.cpp.o"), CALLS + ".tmp"
-    compile_calls, link_calls = calls_commands(calls_obj, calls_tmp)
-    jobs = min(len(sources()) + 1, os.cpu_count() or 4)
+    jobs = min(len(sources()), os.cpu_count() or 4)
     with ThreadPoolExecutor(jobs) as ex:
-        calls = ex.submit(subprocess.run, compile_calls, capture_output=True, text=True)
         results = list(ex.map(compile_one, sources()))
-        results_calls = [(CALLS_SRC, calls_obj, calls.result())]
-    failed = [(s, r) for s, _, r in results + results_calls if r.returncode != 0]
-    for s, _, r in results + results_calls:
+    failed = [(s, r) for s, _, r in results if r.returncode != 0]
+    for s, _, r in results:
         if verbose or ptxas_info or r.returncode != 0:
             sys.stderr.write(f"== {os.path.basename(s)}\n{r.stdout}{r.stderr}")
     if failed:
-        raise RuntimeError("compilation failed for: " + ", ".join(os.path.basename(s) for s, _ in failed))
+        raise RuntimeError("nvcc failed for: " + ", ".join(os.path.basename(s) for s, _ in failed))
     tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp] + [o for _, o, _ in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+    _run([cc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp] + [o for _, o, _ in results], "link of libmedusa_verify.so")
     os.replace(tmp, LIB)
-    r = subprocess.run(link_calls, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
-    os.replace(calls_tmp, CALLS)
+    return LIB
+
+
+def _compile_calls(verbose: bool = False):
+    """Compiles the binding; returns the link, which wants the library there."""
+    os.makedirs(BUILD, exist_ok=True)
+    tmp = CALLS + ".tmp"
+    compile_cmd, link_cmd = calls_commands(os.path.join(BUILD, "calls.cpp.o"), tmp)
+    _run(compile_cmd, "compilation of calls.cpp", verbose)
+
+    def link():
+        _run(link_cmd, "link of _calls.so")
+        os.replace(tmp, CALLS)
+    return link
+
+
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    """Compile and link the compiled part of the binding if needed, beside a library that is there; returns its path."""
+    if force or _calls_stale():
+        _compile_calls(verbose)()
+    return CALLS
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Build the library and, where torch is installed, the compiled part of the binding, if needed; returns the library's
+    path. The library is there even where the binding could not be built."""
+    with ThreadPoolExecutor(1) as ex:
+        compiled = None
+        if importlib.util.find_spec("torch") is not None and (force or _calls_stale()):
+            compiled = ex.submit(_compile_calls, verbose)  # beside the library's kernels, which take longer
+        build_library(force, verbose, ptxas_info)
+    if compiled is not None:
+        compiled.result()()
     return LIB
 
 
