@@ -8,6 +8,7 @@ or fails to load, :func:`lib` raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 
@@ -402,9 +403,10 @@ def _load_calls():
     if _compiled is None:
         import torch  # noqa: F401  (whose libraries the module is linked against)
         lib()
-        build_calls()
-        from . import _calls
-        _compiled = _calls
+        spec = importlib.util.spec_from_file_location(__name__ + "._calls", build_calls())
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _compiled = module
     return _compiled
 
 

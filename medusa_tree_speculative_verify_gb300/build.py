@@ -2,13 +2,15 @@
 
 Each .cu under csrc/ is compiled in parallel into _build/, then linked into
 medusa_tree_speculative_verify_gb300/libmedusa_verify.so against the shared
-CUDA runtime; that takes nvcc alone. Beside it _calls.so, the compiled part of
-the Python binding, is made from csrc/calls.cpp with the host compiler and
-torch's headers, where torch is installed. Each is rebuilt only when one of its
-own sources or headers is newer (or when forced).
+CUDA runtime; that takes nvcc alone. Beside it _calls-<key>.so, the compiled
+part of the Python binding, is made from csrc/calls.cpp with the host compiler
+and torch's headers, where torch is installed; its name says for which torch and
+interpreter. Each is rebuilt only when one of its own sources or headers is
+newer (or when forced).
 """
 from __future__ import annotations
 
+import hashlib
 import importlib.util
 import os
 import shutil
@@ -24,7 +26,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmedusa_verify.so")
 CALLS_SRC = os.path.join(CSRC, "calls.cpp")
-CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-O2",
@@ -51,7 +52,7 @@ def torch_dir() -> str:
 
 
 def calls_commands(obj: str, out: str):
-    """The compile and the link of _calls.so."""
+    """The compile and the link of the binding."""
     torch = torch_dir()
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
@@ -61,6 +62,16 @@ def calls_commands(obj: str, out: str):
     return ([cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{d}" for d in include), "-c", CALLS_SRC, "-o", obj],
             [cxx, "-shared", obj, "-o", out, f"-L{PKG}", "-l:libmedusa_verify.so", f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
              "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"])
+
+
+def calls_path() -> str:
+    """Where the binding for this torch and this interpreter lies. It has torch's structures and the interpreter's compiled in
+    and torch's libraries as its run path, so that one made for others must not be loaded."""
+    torch = torch_dir()
+    with open(os.path.join(torch, "version.py"), encoding="utf-8") as f:
+        made_for = (torch, f.read(), sys.version, sysconfig.get_config_var("EXT_SUFFIX"))
+    key = hashlib.sha256(repr(made_for).encode()).hexdigest()[:12]
+    return os.path.join(PKG, f"_calls-{key}{made_for[3]}")
 
 
 def _older(path: str, deps) -> bool:
@@ -76,7 +87,7 @@ def _library_stale() -> bool:
 
 
 def _calls_stale() -> bool:
-    return _older(CALLS, [CALLS_SRC] + _headers())
+    return _older(calls_path(), [CALLS_SRC] + _headers())
 
 
 def _stale() -> bool:
@@ -123,13 +134,14 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool =
 def _compile_calls(verbose: bool = False):
     """Compiles the binding; returns the link, which wants the library there."""
     os.makedirs(BUILD, exist_ok=True)
-    tmp = CALLS + ".tmp"
-    compile_cmd, link_cmd = calls_commands(os.path.join(BUILD, "calls.cpp.o"), tmp)
+    path = calls_path()
+    tmp = path + ".tmp"
+    compile_cmd, link_cmd = calls_commands(os.path.join(BUILD, os.path.basename(path) + ".o"), tmp)
     _run(compile_cmd, "compilation of calls.cpp", verbose)
 
     def link():
-        _run(link_cmd, "link of _calls.so")
-        os.replace(tmp, CALLS)
+        _run(link_cmd, f"link of {os.path.basename(path)}")
+        os.replace(tmp, path)
     return link
 
 
@@ -137,7 +149,7 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     """Compile and link the compiled part of the binding if needed, beside a library that is there; returns its path."""
     if force or _calls_stale():
         _compile_calls(verbose)()
-    return CALLS
+    return calls_path()
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

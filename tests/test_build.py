@@ -79,3 +79,39 @@ def test_each_is_rebuilt_for_its_own_sources(tree):
     os.utime(pkg / "csrc" / "one.cu", (later, later))
     b.build()
     assert any("one.cu" in c for c in commands) and not any("calls.cpp" in c for c in commands)
+
+
+def test_binding_belongs_to_one_torch_and_interpreter(tree, monkeypatch, tmp_path):
+    """Another torch, or another version in its place, or another interpreter: what was built for the old one is not taken."""
+    pkg, _ = tree
+    b.build()
+    assert not b._stale()
+    other = tmp_path / "torch"
+    other.mkdir()
+    monkeypatch.setattr(b, "torch_dir", lambda: str(other))
+    (other / "version.py").write_text("__version__ = '2.0.0'\n")
+    assert b._stale()
+
+
+def test_binding_follows_torchs_version_and_the_interpreters(tree, monkeypatch, tmp_path):
+    pkg, _ = tree
+    fake = tmp_path / "torch"
+    fake.mkdir()
+    (fake / "version.py").write_text("__version__ = '2.0.0'\n")
+    monkeypatch.setattr(b, "torch_dir", lambda: str(fake))
+    names = {b.calls_path()}
+    (fake / "version.py").write_text("__version__ = '2.0.1'\n")
+    names.add(b.calls_path())
+    monkeypatch.setattr(b.sys, "version", b.sys.version + " (other)")
+    names.add(b.calls_path())
+    monkeypatch.setattr(b.sysconfig, "get_config_var", lambda name: ".cpython-399-x.so")
+    names.add(b.calls_path())
+    assert len(names) == 4 and all(os.path.basename(n).startswith("_calls") for n in names)
+
+
+def test_binding_of_another_name_is_not_loaded():
+    """What is imported is the file that belongs to this torch and interpreter."""
+    code = ("import medusa_tree_speculative_verify_gb300 as mv, importlib;"
+            "print(mv._load_calls().__file__ == importlib.import_module(mv.__name__ + '.build').calls_path())")
+    r = subprocess.run([b.sys.executable, "-c", code], capture_output=True, text=True, cwd=b.ROOT)
+    assert r.stdout.strip() == "True", r.stdout + r.stderr
