@@ -572,9 +572,10 @@ mv_status paged_attention(mv_rows q, int32_t n_heads, const mv_paged_kv* cache, 
  * So growing and then shrinking by the same numbers leaves the stack as it was, and rows, lengths and table are what
  * paged_kv_append and qk_norm_rope take. Table entries and stack places that are given up keep their last value.
  * Everything is read on the device, so the call can be captured and replayed. Where a length would leave 0 .. max_pages *
- * page_size, the pages do not suffice (or are more than n_pages), or there are more than n_rows rows, nothing of this is
- * done: the device error word is set, cu_rows is all zeros, positions and slots are all -1, the rest is as it was. A page
- * number outside the pool is moved like another, and sets the error word.
+ * page_size, the pages do not suffice (or are more than n_pages), or more than n_rows rows come while positions or slots are
+ * wanted (n_rows = 0 with an address: room for none), nothing of this is done: the device error word is set, cu_rows is all
+ * zeros, positions and slots are all -1, the rest is as it was. A page number outside the pool is moved like another, and
+ * sets the error word.
  * Limits: page_size as above, 0 <= n_seq <= 4096, n_pages >= 1. The arrays do not overlap.
  * Errors: MV_ERR_INVALID_ARG (null, unaligned, negative), MV_ERR_SHAPE, MV_ERR_CUDA. */
 mv_status paged_kv_resize(const int32_t* by, int32_t n_seq, int32_t page_size, int32_t n_pages, int32_t* block_table,

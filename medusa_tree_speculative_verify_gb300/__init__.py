@@ -533,7 +533,8 @@ def paged_kv_resize(by, cache: PagedKV, block_table, seq_lens, free_pages, cu_ro
                     stream=None):
     """Each sequence grows or shrinks by ``by`` int32 [n_seq] tokens: seq_lens, block_table and free_pages int32 [1 +
     n_pages] (how many are free, then the stack of them) follow; cu_rows int32 [n_seq + 1], positions int32 [rows] and slots
-    int64 [rows] are written for the rows that come, -1 behind the last one. ``cache``: any of the layers' caches."""
+    int64 [rows] are written for the rows that come, -1 behind the last one; a call with more rows than these have room for
+    changes nothing and sets the device error word. ``cache``: any of the layers' caches."""
     _check((_compiled or _load_calls()).paged_kv_resize(by, free_pages, cu_rows, positions, slots, cache._at, cache.device,
                                                      block_table, seq_lens, stream), "paged_kv_resize")
 

@@ -190,6 +190,7 @@ PyObject* resize(PyObject* const* a) {
   const Sequences s(a[7], a[8], dev);
   const int32_t* by = ints(a[0], "by", dev, s.n);
   int32_t* free_pages = ints(a[1], "free_pages", dev, 1 + (int64_t)c->n_pages);
+  static int64_t no_rows;  // the address of tensors without elements, whose own says that they are not wanted; never used
   int32_t *cu = nullptr, *positions = nullptr;
   int64_t *slots = nullptr, n = 0;
   if (a[2] != Py_None) cu = ints(a[2], "cu_rows", dev, (int64_t)s.n + 1);
@@ -197,11 +198,13 @@ PyObject* resize(PyObject* const* a) {
   if (a[3] != Py_None) {
     n = tensor(a[3], "positions").numel();
     positions = ints(a[3], "positions", dev, n);
+    if (!n) positions = reinterpret_cast<int32_t*>(&no_rows);
   }
   if (a[4] != Py_None) {
     const at::Tensor& t = tensor(a[4], "slots");
     if (!positions) n = t.numel();
     slots = vector_of<int64_t>(t, "slots", dev, n, at::kLong);
+    if (!n) slots = &no_rows;
   }
   const int32_t n_rows = int32_of(n, "rows");
   const On on(a[9], dev, "paged_kv_resize");
