@@ -593,7 +593,7 @@ mv_status paged_kv_resize(const int32_t* by, int32_t n_seq, int32_t page_size, i
  * pi) in units of 2^-64, the angle of one position as a part of a turn; the product with a position is taken modulo whole
  * turns, so it is exact for every position. rot_dim = 0: the norm alone, turns may be NULL. positions device int32
  * [n_tokens]; the rows of a token with a negative one (padding, see paged_kv_resize) are left as they were. With rot_dim = 0
- * positions may be NULL.
+ * or n_tokens = 0 positions may be NULL.
  * q_out and k_out may be q and k themselves (the same address and strides), and must not overlap them otherwise.
  * Limits: head_dim % 16 == 0, 16 <= head_dim <= 256; rot_dim % 16 == 0, rot_dim <= head_dim; 0 <= n_heads, n_kv_heads <= 256
  * (rows of no heads are not looked at); eps >= 0; rows as in prompt_attention, gains 16-byte aligned.

@@ -243,7 +243,7 @@ PyObject* norm_rope(PyObject* const* a) {
   int32_t rot_dim = 0;
   if (a[8] != Py_None) {
     const at::Tensor& w = tensor(a[8], "rope");
-    if (!positions) refuse("qk_norm_rope: a rotation wants positions");
+    if (a[7] == Py_None) refuse("qk_norm_rope: a rotation wants positions");
     turns = vector_of<uint64_t>(w, "rope", dev, w.numel(), at::kLong);
     rot_dim = int32_of(2 * w.numel(), "rope");
   }

@@ -210,7 +210,7 @@ extern "C" mv_status qk_norm_rope(mv_rows q, mv_rows k, int32_t n_tokens, int32_
   if (head_dim < 16 || head_dim > kMaxRopeDim || head_dim % 16 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
     return MV_ERR_SHAPE;
   if (!(eps >= 0.0f && eps < INFINITY) || (neighbours != 0 && neighbours != 1)) return MV_ERR_INVALID_ARG;
-  if (rot_dim && (!positions || !turns || (reinterpret_cast<uintptr_t>(turns) & 7))) return MV_ERR_INVALID_ARG;
+  if (rot_dim && ((!positions && n_tokens) || !turns || (reinterpret_cast<uintptr_t>(turns) & 7))) return MV_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(positions) & 3) ||
       ((reinterpret_cast<uintptr_t>(q_gain) | reinterpret_cast<uintptr_t>(k_gain)) & 15))
     return MV_ERR_INVALID_ARG;

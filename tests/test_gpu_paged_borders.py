@@ -5,7 +5,7 @@ import torch
 
 import medusa_tree_speculative_verify_gb300 as mv
 from oracle import paged_step
-from test_gpu_paged_step import SITE_RESIZE, Batch
+from test_gpu_paged_step import SITE_RESIZE, Batch, i32, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,19 @@ def test_resize_into_room_for_fewer_rows(what, room):
     b.check_state()
     for x, given in ((pos, what != "slots"), (slots, what != "positions")):
         assert x.tolist() == [-1 if given else 77] * room
+
+
+@pytest.mark.parametrize("rope", [True, False])
+def test_heads_of_no_tokens(rope):
+    """A step without rows: nothing to do, whether or not the heads would be turned."""
+    q, k = normal(1, 0, 4, 64), normal(2, 0, 2, 64)
+    gain, at, r = normal(3, 64), i32([]), mv.Rope(64) if rope else None
+    mv.qk_norm_rope(q, k, gain, gain, 1e-6, at, r)
+    mv.qk_norm_rope(q, None, gain, None, 1e-6, at, r, torch.empty_like(q))
+    with pytest.raises(ValueError):
+        mv.qk_norm_rope(q, k, gain, gain, 1e-6, None, mv.Rope(64))   # a rotation wants positions, be it of no tokens
+    q = normal(1, 3, 4, 64)
+    out = torch.full_like(q, 7.0)
+    with pytest.raises(ValueError):
+        mv.qk_norm_rope(q, None, gain, None, 1e-6, at, r, out)       # no positions for three tokens
+    assert (out == 7.0).all()

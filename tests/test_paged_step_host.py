@@ -140,3 +140,9 @@ def test_oracle_resize():
     assert got[0] == [25, 3, 1, 0] and got[1].tolist() == [[7, 4, 0], [2, 4, 6], [6, 0, 0], [1, 0, 0]]
     assert got[2] == [3, 3, 5, 1, 6, 4, 9, 9] and got[3] == [0, 20, 20, 21, 21]
     assert got[4] == list(range(5, 25)) + [0] and got[5] == [7 * 16 + p for p in range(5, 16)] + [4 * 16 + p for p in range(9)] + [96]
+
+
+def test_rope_of_no_tokens_wants_no_positions():
+    assert rope(n=0, pos=None) == 0
+    assert rope(n=1, pos=None) == INVALID and rope(n=0, pos=None, turns=None) == INVALID
+    assert rope(n=0, pos=FAKE + 2) == INVALID
