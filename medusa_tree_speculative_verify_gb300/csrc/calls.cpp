@@ -103,12 +103,20 @@ struct On {
     if (o == Py_None) {
       stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
     } else {
-      PyObject *raw = PyObject_GetAttrString(o, "cuda_stream"), *at = raw ? PyObject_GetAttrString(o, "device_index") : nullptr;
-      const int64_t ptr = raw ? PyLong_AsLongLong(raw) : -1, index = at ? PyLong_AsLongLong(at) : -1;
+      // whatever has a device and a raw pointer: torch's streams, and those of others that say as much
+      PyObject *raw = PyObject_GetAttrString(o, "cuda_stream"), *at = raw ? PyObject_GetAttrString(o, "device") : nullptr;
+      PyObject* nth = at ? PyObject_GetAttrString(at, "index") : nullptr;
+      const bool here = nth && PyLong_Check(nth) && PyLong_AsLongLong(nth) == dev;
+      const int64_t ptr = raw ? PyLong_AsLongLong(raw) : -1;
+      PyObject* is_on = nth && !here && !PyErr_Occurred() ? PyObject_Str(at) : nullptr;
+      const char* text = is_on ? PyUnicode_AsUTF8(is_on) : nullptr;
+      const std::string device = text ? text : "";
       Py_XDECREF(raw);
       Py_XDECREF(at);
+      Py_XDECREF(nth);
+      Py_XDECREF(is_on);
       if (PyErr_Occurred()) throw Raised();
-      if (index != dev) refuse(name, ": the stream is on cuda:", index, ", the tensors are on CUDA device ", dev);
+      if (!here) refuse(name, ": the stream is on ", device, ", the tensors are on CUDA device ", dev);
       stream = reinterpret_cast<mv_stream>(ptr);
     }
     if (c10::cuda::current_device() != dev) guard.set_index((c10::DeviceIndex)dev);

@@ -1,11 +1,12 @@
-"""The operators around a paged step at the borders of what their calls allow: tensors without elements."""
+"""The operators around a paged step at the borders of what their calls allow: tensors without elements, streams that are no
+torch.cuda.Stream."""
 import numpy as np
 import pytest
 import torch
 
 import medusa_tree_speculative_verify_gb300 as mv
 from oracle import paged_step
-from test_gpu_paged_step import SITE_RESIZE, Batch, i32, normal
+from test_gpu_paged_step import SITE_RESIZE, Batch, check_rope, i32, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +54,38 @@ def test_heads_of_no_tokens(rope):
     with pytest.raises(ValueError):
         mv.qk_norm_rope(q, None, gain, None, 1e-6, at, r, out)       # no positions for three tokens
     assert (out == 7.0).all()
+
+
+class Wrapped:
+    """A stream as other libraries hand it on: a device and a raw pointer."""
+
+    def __init__(self, stream):
+        self.device, self.cuda_stream = stream.device, stream.cuda_stream
+
+
+def test_streams_of_other_libraries():
+    side = torch.cuda.Stream()
+    b = Batch([5, 40, 0], 16, 40, 10)
+    torch.cuda.synchronize()
+    by = [30, -20, 17]
+    b.call(by, b.outputs(50), stream=Wrapped(side))
+    side.synchronize()
+    b.lens, b.table, b.free, *_ = paged_step.resize(by, b.lens, b.table, b.free, 16)
+    b.check_state()
+    q, pos, rope = normal(1, 20, 3, 64), np.arange(20), mv.Rope(64)
+    at, out = i32(pos), torch.full_like(q, 7.0)
+    torch.cuda.synchronize()
+    for stream in (Wrapped(side), torch.cuda.ExternalStream(side.cuda_stream), side):
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        mv.qk_norm_rope(q, None, None, None, 1e-6, at, rope, out, stream=stream)
+        side.synchronize()
+        check_rope(out, q, None, 1e-6, pos, rope)
+    far = Wrapped(side)
+    for device in (torch.device("cuda", 7), torch.device("cpu"), torch.device("cuda")):
+        far.device = device
+        with pytest.raises(ValueError, match=f"the stream is on {device},"):
+            mv.qk_norm_rope(q, None, None, None, 1e-6, at, rope, out, stream=far)
+    for stream in (object(), side.cuda_stream):
+        with pytest.raises(AttributeError):
+            mv.qk_norm_rope(q, None, None, None, 1e-6, at, rope, out, stream=stream)
