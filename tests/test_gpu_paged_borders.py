@@ -1,12 +1,12 @@
 """The operators around a paged step at the borders of what their calls allow: tensors without elements, streams that are no
-torch.cuda.Stream."""
+torch.cuda.Stream, rows on 16-byte boundaries."""
 import numpy as np
 import pytest
 import torch
 
 import medusa_tree_speculative_verify_gb300 as mv
 from oracle import paged_step
-from test_gpu_paged_step import SITE_RESIZE, Batch, check_rope, i32, normal
+from test_gpu_paged_step import SITE_RESIZE, Batch, Pool, check_rope, f64, i32, normal, rows_of_many_sizes
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,24 @@ def test_streams_of_other_libraries():
     for stream in (object(), side.cuda_stream):
         with pytest.raises(AttributeError):
             mv.qk_norm_rope(q, None, None, None, 1e-6, at, rope, out, stream=stream)
+
+
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("lens,hk", [([1], 1), ([60, 30, 7], 2), ([2000, 1500], 3)])
+def test_rows_on_16_byte_boundaries(d, lens, hk):
+    """Rows of the caller's that start 16 bytes past a multiple of 32, and whose strides are odd multiples of 16 bytes."""
+    pool, t = Pool(lens, hk, d, 16, seed=d), sum(lens)
+    cu = i32(np.concatenate([[0], np.cumsum(lens)]))
+    # (a buffer starts on a multiple of 32 bytes and more)
+    held = [torch.full((t * hk * (d + 8) + 8,), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    k, v, ko, vo = (x[8:].view(t, hk, d + 8)[..., :d] for x in held)
+    assert all(x.data_ptr() % 32 == 16 and x.stride(1) * 2 % 32 == 16 for x in (k, v, ko, vo))
+    k.copy_(rows_of_many_sizes(d, t, hk, d))
+    v.copy_(rows_of_many_sizes(d + 1, t, hk, d))
+    mv.paged_kv_append(k, v, cu, pool.cache, pool.d_table, pool.d_lens)
+    mv.paged_kv_read(pool.cache, pool.d_table, pool.d_lens, cu, ko, vo)
+    for x, out in ((k, ko), (v, vo)):
+        code, byte = paged_step.quantise(f64(x))
+        assert np.array_equal(f64(out), paged_step.stored_value(paged_step.pack(code), byte))
+    for x in held[2:]:                                         # what lies between stays
+        assert (x[:8] == 7.0).all() and (x[8:].view(t, hk, d + 8)[..., d:] == 7.0).all()

@@ -146,3 +146,22 @@ def test_rope_of_no_tokens_wants_no_positions():
     assert rope(n=0, pos=None) == 0
     assert rope(n=1, pos=None) == INVALID and rope(n=0, pos=None, turns=None) == INVALID
     assert rope(n=0, pos=FAKE + 2) == INVALID
+
+
+def test_product_with_the_reciprocal_scale_rounds_as_the_quotient_for_every_value():
+    """The argument of the test above for all scale bytes and all bf16 values from 2^-6 to 8 scales (below, monotonic rounding
+    leaves them under the first border, 0.25): products have 8 + 24 bits from 2^-37 up, so that they and their sums with 6144
+    are exact in fp64 and each is rounded to fp32 once, as a fused multiply-add does."""
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    every = (np.arange(0x7f80, dtype=np.uint32) << 16).view(np.float32).astype(np.float64)   # bf16 >= 0, finite, in order
+    sides = 0
+    for byte in range(1, paged_step.TOP_BYTE + 1):
+        s = np.float32(paged_step.scale_value(byte))
+        inv = float(np.float32(1.0) / s)
+        x = every[(every >= float(s) / 64) & (every <= 8 * float(s))]
+        y = ((x * inv + 6144.0).astype(np.float32) - np.float32(6144.0)).astype(np.float64)
+        # x against border times scale, which has 7 bits: exact
+        assert np.array_equal(np.sign(x[:, None] - borders * float(s)), np.sign(y[:, None] - borders)), byte
+        assert y[0] < 0.25
+        sides += len(x)
+    assert sides > 200000
