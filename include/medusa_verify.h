@@ -588,12 +588,13 @@ mv_status paged_kv_resize(const int32_t* by, int32_t n_seq, int32_t page_size, i
  * For each token's head x of head_dim elements, q's with q_gain and k's with k_gain (device bf16 [head_dim]; NULL: ones):
  *   y = x / sqrt(mean(x^2) + eps) * gain, then of the first rot_dim elements each pair (a, b) = (y[i], y[i + rot_dim / 2]),
  *   or (y[2 i], y[2 i + 1]) with neighbours = 1, becomes (a cos w - b sin w, a sin w + b cos w), w = positions[t] * f_i.
- * In fp32, rounded to bf16 once (|x| below 2^60, and with eps = 0 a row's largest at least 2^-58, so that fp32 holds the
- * sum of squares; a row of zeros then gives NaNs). Gains may have any size. turns device [rot_dim / 2]: f_i / (2
- * pi) in units of 2^-64, the angle of one position as a part of a turn; the product with a position is taken modulo whole
- * turns, so it is exact for every position. rot_dim = 0: the norm alone, turns may be NULL. positions device int32
- * [n_tokens]; the rows of a token with a negative one (padding, see paged_kv_resize) are left as they were. With rot_dim = 0
- * or n_tokens = 0 positions may be NULL.
+ * In fp32, rounded to bf16 once (|x| below 2^60, and with eps = 0 a row's largest at least 2^-58, so that fp32 holds the sum
+ * of squares; a row of zeros then gives NaNs). Cosines and sines are within 2^-21, the root's reciprocal within 2 units of
+ * fp32: before its rounding an element is off by 2^-18 of its pair's length at most, however small it is itself. Gains may
+ * have any size. turns device [rot_dim / 2]: f_i / (2 pi) in units of 2^-64, the angle of one position as a part of a turn;
+ * the product with a position is taken modulo whole turns, so it is exact for every position. rot_dim = 0: the norm alone,
+ * turns may be NULL. positions device int32 [n_tokens]; the rows of a token with a negative one (padding, see
+ * paged_kv_resize) are left as they were. With rot_dim = 0 or n_tokens = 0 positions may be NULL.
  * q_out and k_out may be q and k themselves (the same address and strides), and must not overlap them otherwise.
  * Limits: head_dim % 16 == 0, 16 <= head_dim <= 256; rot_dim % 16 == 0, rot_dim <= head_dim; 0 <= n_heads, n_kv_heads <= 256
  * (rows of no heads are not looked at); eps >= 0; rows as in prompt_attention, gains 16-byte aligned.

@@ -1,9 +1,10 @@
 // Rows of keys and values written into a paged cache, and read back.
 //
-// A row is one token's head_dim values of one kv head. A group of kLanes threads moves one row, 16 elements a thread. Writing e4m3: the group's largest |x| gives the exponent e, the smallest with max|x| <=
-// 448 * 2^e: with max|x| = 1.m * 2^(E-127), 448 = 1.75 * 2^8, that is e = E - 135, one more when 1.m > 1.75. The
-// product with 2^-e is exact (short of underflow), so the row is rounded once, by the conversion, and what it stands
-// for is exact in bf16 again.
+// A row is one token's head_dim values of one kv head. A group of kLanes threads moves one row, 16 elements a thread.
+//
+// Writing e4m3: the group's largest |x| gives the exponent e, the smallest with max|x| <= 448 * 2^e: with max|x| =
+// 1.m * 2^(E-127), 448 = 1.75 * 2^8, that is e = E - 135, one more when 1.m > 1.75. The product with 2^-e is exact (short of
+// underflow), so the row is rounded once, by the conversion, and what it stands for is exact in bf16 again.
 //
 // Writing e2m1: a thread's 16 elements are a group. Its scale s is the one nearest to max|x| / 6 and each element goes to the
 // value nearest to x / s. A border between two values (0.25, 0.75, 1.25 .. 5) times s has at most 7 significant bits and x has

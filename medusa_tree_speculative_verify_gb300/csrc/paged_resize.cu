@@ -8,7 +8,7 @@
 // Bound by latency: lengths, sums, then one dependent load for each page or row. A cluster of CTAs, each of which does the
 // sums for itself, moves the pages; all have read the lengths before the first of them writes (the cluster's barrier). One
 // CTA took 41 us for 200 prompts of up to 8192 tokens let in and out where eight took 15.5; with four pages of a thread at once
-// they take 12.1. More than kRowsHere rows go to a second kernel over the whole GPU, which looks them up in what the first one
+// they take 12.5. More than kRowsHere rows go to a second kernel over the whole GPU, which looks them up in what the first one
 // wrote (19200 rows: 10.8 us there and back, 13.0 without).
 #include <algorithm>
 
@@ -136,8 +136,9 @@ __global__ void __launch_bounds__(kThreads) paged_resize_kernel(const ResizeArgs
     }
     __syncthreads();
   }
-  const bool over = held < 0 || carry[0] > (a.positions || a.slots ? (uint32_t)a.n_rows : kMost) || max(carry[0], max(carry[1], carry[2])) == kMost ||
-                    (int64_t)held + carry[2] > a.n_pages || carry[1] > (int64_t)held + carry[2];
+  const bool over = held < 0 || carry[0] > (a.positions || a.slots ? (uint32_t)a.n_rows : kMost) ||
+                    max(carry[0], max(carry[1], carry[2])) == kMost || (int64_t)held + carry[2] > a.n_pages ||
+                    carry[1] > (int64_t)held + carry[2];
   if (over && rank == 0 && tid == 0) mv_set_error_detail(a.err, kPagedResizeSite, MV_DEVERR_INDEX, (uint32_t)n);
   bad = __syncthreads_or(bad || over);
   const int rows = bad ? 0 : (int)carry[0], take = bad ? 0 : (int)carry[1], give = bad ? 0 : (int)carry[2];
@@ -299,8 +300,8 @@ extern "C" mv_status paged_kv_resize(const int32_t* by, int32_t n_seq, int32_t p
   a.rows_here = a.n_rows <= kRowsHere;
   a.err = mv_error_word();
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // Few sequences have few pages, and fewer warps meet sooner: 48 growing by a token and back 5.7 us, with 512 threads 6.4; 200
-  // prompts let in and out 17.9 and 15.5 (before four pages went at once).
+  // Few sequences have few pages, and fewer warps meet sooner: 48 growing by a token and back 5.5 us, with 512 threads 5.8; 200
+  // prompts let in and out 13.7 and 12.5.
   const mv_status s = n_seq <= 64 ? launch_resize<256>(a, st) : launch_resize<512>(a, st);
   if (s != MV_OK) return s;
   if (!a.rows_here) {

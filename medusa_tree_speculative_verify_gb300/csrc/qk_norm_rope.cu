@@ -1,18 +1,20 @@
 // Norms of the heads of Q and K and their rotation by position, in one pass.
 //
 // A row x is one token's head of D elements: y = x / sqrt(mean x^2 + eps) * gain, then each pair of y's first R elements, (i,
-// i + R/2) or (2 i, 2 i + 1), is turned by the angle position * f_i. In fp32, rounded once.
+// i + R/2) or (2 i, 2 i + 1), is turned by the angle position * f_i. In fp32 (but see below), rounded once.
 //
 // Angles. f_i comes as a fraction of a turn in 64 bits, f_i / 2 pi = turns_i 2^-64, so position * turns_i modulo 2^64 is the
 // angle without its whole turns, exact to position * 2^-64 turns: a position of 2^31 is as good as one of 1. (In fp32 an
 // angle of a million radians is off by up to 0.03.)
 //
 // Bound by memory: 2 bytes read and 2 written for each element. A warp takes some heads of one token (few heads: of
-// several), a group of lanes to a head: side by side in memory and then the next ones. A lane has 16 elements of a head as two pieces of 16 bytes, chosen
-// so that pairs meet in it; what is left to exchange
-// is the sum of squares. What a lane's elements are multiplied with but for the row's own factor, cosines and sines times
-// gains, it computes once for all its heads. Sine and cosine are the special-function unit's (within 2^-21.1, below the
-// 2^-9 of the result's rounding); the angle is within half a turn of zero there.
+// several), a group of lanes to a head: side by side in memory and then the next ones. A lane has 16 elements of a head as two
+// pieces of 16 bytes, chosen so that pairs meet in it; what is left to exchange is the sum of squares. What a lane's elements
+// are multiplied with but for the row's own factor, cosines and sines times gains, it computes once for all its heads.
+//
+// Sine and cosine are the special-function unit's, the angle being within half a turn of zero: off by 2^-21.1 at most, that is
+// of the pair's length, where the result's rounding is 2^-9 of the element. (An element that nearly cancels, or is a sine
+// of almost nothing, has the former.) The root's reciprocal is rsqrtf, 2 units of fp32.
 #include <algorithm>
 
 #include "kernels.cuh"
